@@ -56,7 +56,7 @@ extern "C" {
 #define NS_OK 0
 #define NS_EINVAL (-1)   /* null pointer, negative dims/count/steps, bad dtype, a side above
                             2^30 - 1 or a matrix above 2^40 elements, overlapping matrices */
-#define NS_EALIGN (-2)   /* a matrix pointer is not aligned to its element size */
+#define NS_EALIGN (-2)   /* a pointer is not aligned to its element size (8-bit checkpoints: 16 bytes) */
 #define NS_ENOMEM (-3)   /* workspace allocation failed / caller workspace too small */
 #define NS_ECUDA (-4)    /* a CUDA runtime or driver call failed */
 #define NS_ETIMEOUT (-5) /* a bounded device-side wait gave up (reported by ns_get_status) */
@@ -180,6 +180,154 @@ int ns_muon_update_batched(void *const *G, void *const *Mom, void *const *Out, c
                            int count, int steps, const float *coeffs, float mu, int nesterov,
                            float scale, int dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the training step around the optimizer: the token embedding
+ * and its gradient, the clipped policy loss on logits, activations held for
+ * the backward pass in 8 bits, and the weight gradients formed from them
+ * (the matrices ns_muon_update_batched takes as G).
+ *
+ * The conventions at the top of this file hold: device pointers on the
+ * current device, stream-ordered, no synchronisation, validated before
+ * anything is launched. Matrices are row-major with a row pitch ld_* in
+ * elements (at least the row's length; no other requirement: rows and bases
+ * need only their element's alignment, 16-byte aligned ones are faster).
+ * dtype NS_F32 or NS_BF16; arithmetic and every sum in fp32, each output
+ * rounded once. Results are the same bits from call to call: no sum's order
+ * depends on the schedule. Outputs must not overlap inputs or each other
+ * unless stated (NS_EINVAL). Scratch comes from the internal per-(device,
+ * stream) workspace cache; once a call of the same sizes has run on a stream,
+ * a repeat allocates nothing and may be captured into a CUDA graph.
+ */
+
+/* types of token ids and targets */
+#define NS_I32 0
+#define NS_I64 1
+
+/*
+ * ns_embed_lookup -- Out[t, :] = scale * Table[ids[t], :] for `count` ids.
+ *   table  vocab x dim of dtype; ids: count integers of id_type on the device;
+ *   out    count x dim of dtype.
+ * An id outside [0, vocab) is padding: its row of Out is zero.
+ */
+int ns_embed_lookup(const void *table, int64_t ld_table, int64_t vocab, int64_t dim, const void *ids, int id_type,
+                    int64_t count, float scale, void *out, int64_t ld_out, int dtype, void *stream);
+
+/*
+ * ns_embed_grad -- gradient of ns_embed_lookup with respect to the table:
+ *     S[v, :] = scale * sum over t with ids[t] == v of dOut[t, :]
+ *     Grad    = S                 accumulate 0: every row written, zero where no id points
+ *     Grad   += S                 accumulate 1: only the rows that an id points to are touched
+ *   dout   count x dim of dtype;  grad  vocab x dim of grad_dtype (NS_F32 or
+ *   NS_BF16, whatever dtype is).
+ * Sums run in fp32 over the positions in a fixed order and are rounded once.
+ * Ids outside [0, vocab) have no gradient; their rows of dOut are not read.
+ * count <= 2^30, vocab < 2^31 - 1, count * dim below 2^43.
+ */
+int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids, int id_type, int64_t count, float scale,
+                  void *grad, int64_t ld_grad, int64_t vocab, int64_t dim, int dtype, int grad_dtype, int accumulate,
+                  void *stream);
+
+/*
+ * ns_token_logprobs -- logp[t] = z[y] - log sum_j exp z[j] with z =
+ * Logits[t, :] * inv_temperature and y = targets[t], for `rows` rows of
+ * `vocab` logits. A row whose target is outside [0, vocab) is masked: its
+ * logits are not read and its logp is 0. A row of logits that are all
+ * -infinity holds no distribution and gives 0 as well. logp: rows floats.
+ */
+int ns_token_logprobs(const void *logits, int64_t ld_logits, int64_t rows, int64_t vocab, const void *targets,
+                      int id_type, float inv_temperature, float *logp, int dtype, void *stream);
+
+/*
+ * ns_policy_loss -- clipped policy loss with a KL term, and its gradient with
+ * respect to the logits. With logp as ns_token_logprobs, per row t:
+ *     r    = exp(logp - old_logp)                (1 when old_logp is NULL)
+ *     gain = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),  A = advantage
+ *     k    = exp(ref_logp - logp) - (ref_logp - logp) - 1   (0 when ref_logp is NULL)
+ *     loss = sum over rows of weight * (kl_coef * k - gain)
+ *     g    = weight * inv_temperature *
+ *            ((r A <= clipped r A ? -r A : 0) + kl_coef * (1 - exp(ref_logp - logp)))
+ *     dLogits[t, j] = g * ((j == y) - softmax(z)[j])
+ *   targets    rows integers of id_type; old_logp, ref_logp (either may be
+ *              NULL), advantage, weight: rows floats
+ *   loss       one float; logp, kl: rows floats (kl[t] = k)
+ *   dlogits    rows x vocab of dtype; NULL for no gradient; may be logits
+ *              itself (same pointer and pitch: the gradient written over them)
+ * A row is masked when its target is outside [0, vocab), its weight is 0 or its
+ * logits are all -infinity: it adds nothing to the loss, its logp and kl are
+ * 0, its gradient row is zero, and (but for the last case) its logits and its
+ * other inputs are not looked at, whatever they hold. kl_coef, clip_low,
+ * clip_high finite and >= 0, inv_temperature finite and > 0.
+ */
+int ns_policy_loss(const void *logits, int64_t ld_logits, int64_t rows, int64_t vocab, const void *targets,
+                   int id_type, const float *old_logp, const float *ref_logp, const float *advantage,
+                   const float *weight, float inv_temperature, float clip_low, float clip_high, float kl_coef,
+                   float *loss, float *logp, float *kl, void *dlogits, int64_t ld_dlogits, int dtype, void *stream);
+
+/*
+ * Activations held in 8 bits ("checkpoints"). A rows x cols matrix is held
+ * as int8 values and one scale byte per block of 32 consecutive values of a
+ * row (the last block of a row may be shorter):
+ *     E     = exponent field of the block's largest magnitude as a float32, at least 7
+ *     q     = x * 2^(133 - E) rounded half to even, at most 127 in magnitude
+ *     value = q * 2^(E - 133)
+ * The scale is a power of two, so q comes without a division and every value
+ * is exact in bf16 (7 magnitude bits): the backward pass can feed it to the
+ * tensor cores as it is. The error is at most half a unit, 1/128 of the
+ * block's largest magnitude, (for magnitudes that round to 128 units: one
+ * unit). A block that holds an infinity or NaN has E = 255 and reads back as
+ * NaN throughout.
+ *   q       rows x ns_ckpt_pitch(cols) bytes; bytes beyond cols are 0
+ *   scales  rows x ns_ckpt_scale_pitch(cols) bytes; beyond the last block 0
+ * Both 16-byte aligned (NS_EALIGN). cols <= 2^30.
+ */
+int64_t ns_ckpt_pitch(int64_t cols);       /* cols rounded up to a multiple of 16; -1 if negative */
+int64_t ns_ckpt_scale_pitch(int64_t cols); /* ceil(cols / 32) rounded up to a multiple of 4 */
+
+/* ns_ckpt_store -- hold X in 8 bits.  ns_ckpt_load -- Out = the values held. */
+int ns_ckpt_store(const void *x, int64_t ld_x, int64_t rows, int64_t cols, void *q, void *scales, int dtype,
+                  void *stream);
+int ns_ckpt_load(const void *q, const void *scales, int64_t rows, int64_t cols, void *out, int64_t ld_out, int dtype,
+                 void *stream);
+
+/*
+ * ns_gated_forward -- H = silu(Gate) * Up, silu(x) = x / (1 + exp(-x)), and
+ * Gate and Up held in 8 bits for the backward pass, in one pass over both.
+ * All rows x cols; gate and up share the pitch ld_in, so they may be the two
+ * halves of one rows x 2 cols matrix.
+ */
+int ns_gated_forward(const void *gate, const void *up, int64_t ld_in, int64_t rows, int64_t cols, void *h, int64_t ld_h,
+                     void *q_gate, void *s_gate, void *q_up, void *s_up, int dtype, void *stream);
+
+/*
+ * ns_gated_backward -- from dH and the values g, u that the two checkpoints
+ * hold: dGate = dH u s (1 + g (1 - s)), dUp = dH g s, with s = 1 / (1 +
+ * exp(-g)); and, unless h is NULL, H = g s u again (the input of the next
+ * layer's weight gradient). dgate and dup share the pitch ld_d.
+ */
+int ns_gated_backward(const void *dh, int64_t ld_dh, const void *q_gate, const void *s_gate, const void *q_up,
+                      const void *s_up, int64_t rows, int64_t cols, void *dgate, void *dup, int64_t ld_d, void *h,
+                      int64_t ld_h, int dtype, void *stream);
+
+/*
+ * ns_ckpt_wgrad -- weight gradients from an input held in 8 bits. With X the
+ * rows x n_in values of the checkpoint and dY rows x n_out:
+ *     G[e] (+)= sum over rows t of group e of dY[t, :]^T X[t, :]      (n_out x n_in)
+ *   offsets  groups + 1 ascending int32 on the device: group e is rows
+ *            [offsets[e], offsets[e+1]) (values are clamped to [0, rows]);
+ *            NULL with groups = 1 for all rows. A group without rows gives 0.
+ *   grad     groups x n_out x n_in of grad_dtype, contiguous: a stack of
+ *            matrices as ns_muon_update_batched takes them
+ *   accumulate  0: G is overwritten; 1: the sum is added to it
+ * dY of dtype: bf16, or fp32 (held as three bf16 slices inside, so products
+ * are exact to 2^-24). Rows of other groups never reach a group's sum,
+ * whatever they hold. Sums in fp32: the tensor cores' accumulators are added
+ * to fp32 registers every 512 rows (their own sum loses up to a unit in the
+ * last place per instruction).
+ */
+int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_t n_out, const void *q, const void *scales,
+                  int64_t n_in, const int32_t *offsets, int groups, void *grad, int dtype, int grad_dtype,
+                  int accumulate, void *stream);
+
 /*
  * ns_cost -- Newton-Schulz cost of an M x N matrix, max(M,N) * min(M,N)^2
  * (second page, "Changes" item 1: the dominant term of the orthogonalization).
@@ -292,8 +440,11 @@ int64_t ns_num_workspace_allocations(void);
  * 5 resident, 6 gemm (the tensor-core kernel running every step and phase of
  * a call in one launch), 7 prep (fp32: the normalising copy, or its bf16
  * slices on the tensor cores), 8 momentum
- * (ns_muon_update_batched's element-wise step), the total milliseconds into
- * ms[k] and the launch count into launches[k] for k < n (n <= 9). Returns
+ * (ns_muon_update_batched's element-wise step), 9 embedding lookup, 10 sort of
+ * the ids, 11 embedding gradient, 12 log probabilities and policy loss, 13
+ * 8-bit checkpoints and the gated activation, 14 weight gradient (with its
+ * preparation), the total milliseconds into
+ * ms[k] and the launch count into launches[k] for k < n (n <= 15). Returns
  * NS_OK or NS_EINVAL / NS_ECUDA.
  */
 int ns_set_kernel_timing(int enable);

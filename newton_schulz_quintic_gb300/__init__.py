@@ -9,12 +9,23 @@ missing: there is no CPU fallback.
 from .api import (  # noqa: F401
     NS_BF16,
     NS_F32,
+    Checkpoint8,
     NSError,
+    PolicyLoss,
+    checkpoint_load,
+    checkpoint_store,
+    checkpoint_wgrad,
     cost,
+    embed_grad,
+    embed_lookup,
+    gated_backward,
+    gated_forward,
     get_status,
     library_path,
     load_library,
     orthogonalize_batched,
     orthogonalize_batched_host,
+    policy_loss,
+    token_logprobs,
     workspace_bytes,
 )

@@ -343,7 +343,7 @@ def num_kernel_launches() -> int:
 
 
 KERNEL_KINDS = ("norm_pass", "norm_finish", "gram", "square", "apply", "resident", "gemm", "prep",
-                "momentum")
+                "momentum", "embed_lookup", "embed_sort", "embed_grad", "policy", "checkpoint", "wgrad")
 
 
 def set_kernel_timing(enable: bool) -> None:
@@ -444,3 +444,19 @@ def set_gemm_schedule(mode: str) -> None:
     rc = load_library().ns_set_gemm_schedule(GEMM_SCHEDULES[mode])
     if rc != 0:
         raise NSError(rc, "ns_set_gemm_schedule")
+
+
+# the operators of the training step around the optimizer
+from .training import (  # noqa: E402,F401
+    Checkpoint8,
+    PolicyLoss,
+    checkpoint_load,
+    checkpoint_store,
+    checkpoint_wgrad,
+    embed_grad,
+    embed_lookup,
+    gated_backward,
+    gated_forward,
+    policy_loss,
+    token_logprobs,
+)

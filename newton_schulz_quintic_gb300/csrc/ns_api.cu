@@ -566,8 +566,9 @@ int ensure_ws(CachedWs &c, size_t bytes, cudaStream_t s) {
 // kinds: 0 norm pass (the read of the caller's matrices), 1 norm finish (bf16:
 // per-matrix scale), 2 gram, 3 square, 4 apply, 5 resident, 6 gemm (one
 // launch running every step and phase), 7 prep (fp32: the normalising copy),
-// 8 momentum (ns_muon_update_batched's element-wise step)
-constexpr int kKinds = 9;
+// 8 momentum (ns_muon_update_batched's element-wise step), 9.. the training
+// operators (OpKind in ns_internal.h)
+constexpr int kKinds = kOpKindEnd;
 
 // How the tensor-core path is launched (ns_set_gemm_schedule): one launch per
 // step and phase (default) or one launch per call with per-matrix counters.
@@ -593,7 +594,10 @@ bool nvtx_on() {
   return v != 0;
 }
 const char *const kKindNames[] = {"ns norm pass", "ns norm finish", "ns gram", "ns square", "ns apply",
-                                  "ns resident", "ns gemm (all phases)", "ns prep", "ns momentum"};
+                                  "ns resident", "ns gemm (all phases)", "ns prep", "ns momentum",
+                                  "ns embed lookup", "ns embed sort", "ns embed grad", "ns policy",
+                                  "ns checkpoint", "ns wgrad"};
+static_assert(sizeof(kKindNames) / sizeof(kKindNames[0]) == kKinds, "one name per kind");
 struct NvtxRange {
   bool on;
   explicit NvtxRange(const char *name) : on(nvtx_on()) {
@@ -875,6 +879,54 @@ int check_call(void *const *X, const int64_t *shapes, int count, int steps, int 
   std::lock_guard<std::mutex> lock(g_mu);
   DevInfo *di = nullptr;
   return device_info(&di);
+}
+
+// ------------------------------------------------------------ operator calls
+OpCall::OpCall(void *stream) : s(static_cast<cudaStream_t>(stream)), lock(g_mu) {
+  if (nvtx_on()) {
+    nvtxRangePushA("ns call");
+    ranged = true;
+  }
+  DevInfo *di = nullptr;
+  rc = device_info(&di);
+  if (rc) return;
+  sms = di->sms;
+  status = di->status;
+  cudaGetDevice(&dev);
+}
+
+OpCall::~OpCall() {
+  if (ranged) nvtxRangePop();
+}
+
+int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr) {
+  CachedWs &c = g_ws[WsKey{dev, s, slot}];
+  const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s);
+  *ptr = c.ptr;
+  return e;
+}
+
+int OpCall::tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
+                       const int64_t *pitch_bytes, const int *box) {
+  if (const int e = get_encode()) return e;
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], one[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(std::max<int64_t>(dims[i], 1));
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    if (i) st[i - 1] = static_cast<cuuint64_t>(pitch_bytes[i - 1]);
+  }
+  const bool wide = elt == 2;
+  const CUresult r = g_encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                              static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, bx, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NS_OK : NS_ECUDA;
+}
+
+int OpCall::timed_launch(int kind, int (*fn)(void *), void *arg) {
+  return timed(kind, s, [&] { return fn(arg); }) ? NS_ECUDA : NS_OK;
 }
 
 }  // namespace ns

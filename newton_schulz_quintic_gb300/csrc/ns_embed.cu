@@ -1,0 +1,482 @@
+// ns_embed.cu -- token embedding of the training operators (include/ns.h):
+// ns_embed_lookup and the table's gradient ns_embed_grad.
+//
+// The gradient is a sum over positions grouped by token id. Atomic adds into
+// the table would make the sums depend on the schedule (and serialise on the
+// few very frequent ids of real text), so the positions are sorted by id
+// first, stably, and each id's rows are added in the order of their
+// positions:
+//   sort      one cluster of 8 CTAs, a stable radix sort of (id, position);
+//             padding ids sort to the end;
+//   segments  the sorted list in fixed pieces of kSeg positions, one piece and
+//             column range per CTA, whatever the ids are: a run of equal ids
+//             inside a piece is written to the table, the parts of a run
+//             that crosses piece borders go to scratch as fp32 sums;
+//   joins     adds the parts of each crossing run in piece order;
+//   zeros     (not accumulating) the rows no id points to.
+#include <algorithm>
+
+#include "../../include/ns.h"
+#include "ns_rows.cuh"
+
+namespace ns {
+
+namespace {
+
+// ------------------------------------------------------------------ lookup
+struct LookupParams {
+  const void *table;
+  void *out;
+  Ids ids;
+  int64_t count, ld_table, ld_out;
+  int dim;
+  float scale;
+  int *status;
+};
+
+constexpr int kLookupPacks = 4;  // packs a lane has in flight
+
+// One warp per (row, stretch of 32 * kLookupPacks packs).
+template <int DT, int VEC>
+__global__ void __launch_bounds__(256) ns_embed_lookup_kernel(const __grid_constant__ LookupParams p) {
+  using P = Pack<DT, VEC>;
+  using E = typename P::E;
+  constexpr int kSpan = 32 * kLookupPacks * VEC;
+  const int lane = threadIdx.x & 31;
+  const int per_row = (p.dim + kSpan - 1) / kSpan;
+  const int64_t items = p.count * per_row;
+  const size_t size = static_cast<size_t>((p.count - 1) * p.ld_out + p.dim) * sizeof(E);
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t t = it / per_row;
+    const int c0 = static_cast<int>(it - t * per_row) * kSpan + lane * VEC;
+    const int id = p.ids.get(t);
+    const E *src = static_cast<const E *>(p.table) + static_cast<int64_t>(id < 0 ? 0 : id) * p.ld_table;
+    E *dst = static_cast<E *>(p.out) + t * p.ld_out;
+    P v[kLookupPacks];
+#pragma unroll
+    for (int k = 0; k < kLookupPacks; ++k) {
+      const int c = c0 + k * 32 * VEC;
+      if (id >= 0 && c < p.dim) v[k].load(src + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kLookupPacks; ++k) {
+      const int c = c0 + k * 32 * VEC;
+      if (c >= p.dim) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[k].set(e, id >= 0 ? v[k].get(e) * p.scale : 0.f);
+      v[k].store(dst + c, p.out, size, p.status);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sort
+constexpr int kSortCluster = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 4;                                 // keys per thread and tile
+constexpr int kSortTile = kSortThreads * kSortRounds;
+constexpr int kSortBins = 512;                                 // 9 bits a pass at most
+
+struct SortParams {
+  Ids ids;
+  int n;
+  int bits, passes;      // digit width and number of passes
+  int *keys[2], *pos[2];  // ping-pong; the last pass writes [0]
+  int *status;
+};
+
+// Stable least-significant-digit radix sort by one cluster. Each CTA owns a
+// contiguous share of the list. Per pass: every CTA counts its share's
+// digits; the counts are exchanged through distributed shared memory, which
+// gives each CTA where its keys of each digit go; then the share is ranked
+// tile by tile: within a warp by matching digits, across warps by a prefix
+// over the warps' counts, so equal digits keep their order.
+__global__ void __launch_bounds__(kSortThreads) ns_embed_sort_kernel(const __grid_constant__ SortParams p) {
+  __shared__ int hist[kSortBins];
+  __shared__ int base[kSortBins];
+  __shared__ int wsum[kSortWarps];
+  __shared__ uint16_t wcount[kSortWarps][kSortBins];
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int share = (p.n + kSortCluster - 1) / kSortCluster;
+  const int lo = min(p.n, rank * share), hi = min(p.n, lo + share);
+  const int bins = 1 << p.bits;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    const int to = (p.passes - 1 - pass) & 1, from = to ^ 1;
+    auto key_at = [&](int i) {
+      if (pass) return __ldcg(p.keys[from] + i);
+      const int id = p.ids.get(i);
+      return id < 0 ? p.ids.vocab : id;
+    };
+    for (int d = threadIdx.x; d < kSortBins; d += kSortThreads) hist[d] = 0;
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) atomicAdd(&hist[(key_at(i) >> shift) & (bins - 1)], 1);
+    cluster_sync();
+    // base[d] = keys of smaller digits anywhere + keys of digit d in lower shares
+    int total = 0, before = 0;
+    if (threadIdx.x < bins) {
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        const int v = static_cast<int>(ld_shared_cluster_u32(mapa_shared(smem_u32(&hist[threadIdx.x]), c)));
+        total += v;
+        before += c < rank ? v : 0;
+      }
+    }
+    int scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) wsum[warp] = scan;
+    __syncthreads();
+    if (warp == 0) {
+      int v = wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      wsum[lane] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < bins) base[threadIdx.x] = scan - total + (warp ? wsum[warp - 1] : 0) + before;
+    for (int t0 = lo; t0 < hi; t0 += kSortTile) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kSortWarps * kSortBins / 2; i += kSortThreads)
+        reinterpret_cast<uint32_t *>(&wcount[0][0])[i] = 0;
+      __syncthreads();
+      int key[kSortRounds], at[kSortRounds], loc[kSortRounds];
+#pragma unroll
+      for (int r = 0; r < kSortRounds; ++r) {
+        const int i = t0 + warp * (32 * kSortRounds) + r * 32 + lane;
+        key[r] = i < hi ? key_at(i) : -1;
+        at[r] = i < hi ? (pass ? __ldcg(p.pos[from] + i) : i) : 0;
+      }
+#pragma unroll
+      for (int r = 0; r < kSortRounds; ++r) {
+        const bool live = key[r] >= 0;
+        const int d = (key[r] >> shift) & (bins - 1);
+        const uint32_t peers = __match_any_sync(0xffffffffu, live ? d : -1);
+        const int seen = live ? wcount[warp][d] : 0;
+        loc[r] = seen + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
+        if (live && (peers >> lane) == 1u) wcount[warp][d] = static_cast<uint16_t>(seen + __popc(peers));
+        __syncwarp();
+      }
+      __syncthreads();
+      int tile_total = 0;
+      if (threadIdx.x < bins) {
+        for (int w = 0; w < kSortWarps; ++w) {
+          const int v = wcount[w][threadIdx.x];
+          wcount[w][threadIdx.x] = static_cast<uint16_t>(tile_total);
+          tile_total += v;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kSortRounds; ++r) {
+        if (key[r] < 0) continue;
+        const int d = (key[r] >> shift) & (bins - 1);
+        const int dst = base[d] + wcount[warp][d] + loc[r];
+        if (in_bounds(p.keys[to] + dst, 4, p.keys[to], static_cast<size_t>(p.n) * 4, p.status)) {
+          p.keys[to][dst] = key[r];
+          p.pos[to][dst] = at[r];
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < bins) base[threadIdx.x] += tile_total;
+    }
+    cluster_sync();  // the pass's output is complete and every histogram read
+  }
+}
+
+// ------------------------------------------------------------------ segment sums
+constexpr int kSeg = 32;         // sorted positions per piece
+constexpr int kSegThreads = 128;
+constexpr int kSegAhead = 8;     // rows in flight per thread
+
+struct GradParams {
+  const void *dout;
+  void *grad;
+  const int *keys, *pos;  // sorted; keys == vocab is padding
+  float *parts;           // [piece][2][dim_pad]: the piece's share of the run that enters it / leaves it
+  int64_t ld_dout, ld_grad;
+  int n, vocab, dim, dim_pad, pieces;
+  int chunks;             // column ranges per piece (one CTA each)
+  float scale;
+  int accumulate;
+  int *status;
+};
+
+template <int GT, int VEC>
+__device__ __forceinline__ void write_row(const GradParams &p, int id, int c, const float (&sum)[VEC]) {
+  using P = Pack<GT, VEC>;
+  typename P::E *g = static_cast<typename P::E *>(p.grad) + static_cast<int64_t>(id) * p.ld_grad + c;
+  P v;
+  if (p.accumulate) v.load(g);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v.set(e, p.accumulate ? fmaf(p.scale, sum[e], v.get(e)) : p.scale * sum[e]);
+  v.store(g, p.grad, static_cast<size_t>((p.vocab - 1) * p.ld_grad + p.dim) * sizeof(typename P::E), p.status);
+}
+
+template <int DT, int GT, int VEC>
+__global__ void __launch_bounds__(kSegThreads) ns_embed_segments_kernel(const __grid_constant__ GradParams p) {
+  using P = Pack<DT, VEC>;
+  using E = typename P::E;
+  __shared__ int key[kSeg + 2];  // with the neighbours on either side
+  __shared__ int at[kSeg];
+  const int piece = blockIdx.x / p.chunks, chunk = blockIdx.x - piece * p.chunks;
+  const int i0 = piece * kSeg;
+  const int len = min(kSeg, p.n - i0);
+  if (threadIdx.x < kSeg + 2) {
+    const int i = i0 - 1 + static_cast<int>(threadIdx.x);
+    key[threadIdx.x] = i >= 0 && i < p.n ? p.keys[i] : -1;
+    if (threadIdx.x < len) at[threadIdx.x] = p.pos[i0 + threadIdx.x];
+  }
+  __syncthreads();
+  const int c = (chunk * kSegThreads + threadIdx.x) * VEC;
+  if (c >= p.dim) return;
+  float sum[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
+  const E *src = static_cast<const E *>(p.dout) + c;
+  float *parts = p.parts + static_cast<int64_t>(piece) * 2 * p.dim_pad + c;
+  bool entered = key[0] == key[1];  // the current run began in an earlier piece
+  for (int k0 = 0; k0 < len; k0 += kSegAhead) {
+    P v[kSegAhead];
+#pragma unroll
+    for (int k = 0; k < kSegAhead; ++k)
+      if (k0 + k < len && key[k0 + k + 1] < p.vocab) v[k].load_stream(src + static_cast<int64_t>(at[k0 + k]) * p.ld_dout);
+#pragma unroll
+    for (int k = 0; k < kSegAhead; ++k) {
+      const int i = k0 + k;
+      if (i >= len) break;
+      const int id = key[i + 1];
+      if (id >= p.vocab) break;  // padding: the rest of the list
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[e] += v[k].get(e);
+      const bool ends = key[i + 2] != id;
+      if (ends || i == len - 1) {
+        if (ends && !entered) {
+          write_row<GT, VEC>(p, id, c, sum);
+        } else {
+          float *to = parts + (entered ? 0 : p.dim_pad);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (in_bounds(to + e, 4, p.parts, static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, p.status)) to[e] = sum[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
+        entered = false;
+      }
+    }
+  }
+}
+
+// The run that leaves a piece having begun in it: its share there, the whole
+// pieces it fills and its share of the piece where it ends.
+template <int GT, int VEC>
+__global__ void __launch_bounds__(kSegThreads) ns_embed_joins_kernel(const __grid_constant__ GradParams p) {
+  const int b = blockIdx.x / p.chunks;
+  const int last = (b + 1) * kSeg - 1;
+  if (last + 1 >= p.n) return;
+  const int id = p.keys[last];
+  if (id >= p.vocab || p.keys[last + 1] != id) return;              // nothing leaves
+  if (b > 0 && p.keys[b * kSeg] == id && p.keys[b * kSeg - 1] == id) return;  // began earlier
+  const int c = ((blockIdx.x - b * p.chunks) * kSegThreads + threadIdx.x) * VEC;
+  if (c >= p.dim) return;
+  // pieces b + 1 .. q hold it: q is where its last position lies
+  int lo = last + 1, hi = p.n;  // keys[lo] == id; hi: the first known not to be
+  while (lo + 1 < hi) {
+    const int m = lo + (hi - lo) / 2;
+    if (p.keys[m] == id) lo = m; else hi = m;
+  }
+  const int q = lo / kSeg;
+  const float *parts = p.parts + static_cast<int64_t>(b) * 2 * p.dim_pad + c;
+  float sum[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sum[e] = parts[p.dim_pad + e];
+  for (int k = b + 1; k <= q; ++k) {
+    parts += 2 * p.dim_pad;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[e] += parts[e];
+  }
+  write_row<GT, VEC>(p, id, c, sum);
+}
+
+// Rows without an id: a warp looks its 32 rows up in the sorted keys, a lane
+// each, and clears those that are absent.
+template <int GT, int VEC>
+__global__ void __launch_bounds__(256) ns_embed_zeros_kernel(const __grid_constant__ GradParams p) {
+  using P = Pack<GT, VEC>;
+  using E = typename P::E;
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 32;
+  if (r0 >= p.vocab) return;
+  const int row = static_cast<int>(r0) + lane;
+  int a = 0, b = p.n;
+  while (a < b) {
+    const int m = (a + b) >> 1;
+    if (p.keys[m] < row) a = m + 1; else b = m;
+  }
+  const bool absent = row < p.vocab && (a >= p.n || p.keys[a] != row);
+  uint32_t todo = __ballot_sync(0xffffffffu, absent);
+  P z;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) z.set(e, 0.f);
+  const size_t size = static_cast<size_t>((p.vocab - 1) * p.ld_grad + p.dim) * sizeof(E);
+  while (todo) {
+    const int k = __ffs(todo) - 1;
+    todo &= todo - 1;
+    E *g = static_cast<E *>(p.grad) + (r0 + k) * p.ld_grad;
+    for (int c = lane * VEC; c < p.dim; c += 32 * VEC) z.store(g + c, p.grad, size, p.status);
+  }
+}
+
+template <int DT, int VEC>
+int run_lookup(const LookupParams &p, int sms, cudaStream_t s) {
+  const int span = 32 * kLookupPacks * VEC;
+  const int64_t items = p.count * ((p.dim + span - 1) / span);
+  const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, static_cast<int64_t>(sms) * 8));
+  ns_embed_lookup_kernel<DT, VEC><<<grid, 256, 0, s>>>(p);
+  count_launch();
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+int run_sort(const SortParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSortCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(kSortCluster, 1, 1);
+  cfg.blockDim = dim3(kSortThreads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, ns_embed_sort_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  count_launch();
+  return 0;
+}
+
+template <int DT, int GT, int VEC>
+int run_grad(const GradParams &p, cudaStream_t s) {
+  const int per = kSegThreads * VEC;
+  GradParams q = p;
+  q.chunks = (p.dim + per - 1) / per;
+  if (static_cast<int64_t>(p.pieces) * q.chunks > INT32_MAX) return -1;
+  if (p.n > 0) {
+    ns_embed_segments_kernel<DT, GT, VEC><<<p.pieces * q.chunks, kSegThreads, 0, s>>>(q);
+    count_launch();
+    ns_embed_joins_kernel<GT, VEC><<<p.pieces * q.chunks, kSegThreads, 0, s>>>(q);
+    count_launch();
+  }
+  if (!p.accumulate) {
+    ns_embed_zeros_kernel<GT, VEC><<<static_cast<int>((p.vocab + 255ll) / 256), 256, 0, s>>>(p);
+    count_launch();
+  }
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+}  // namespace ns
+
+using namespace ns;
+
+extern "C" int ns_embed_lookup(const void *table, int64_t ld_table, int64_t vocab, int64_t dim, const void *ids,
+                               int id_type, int64_t count, float scale, void *out, int64_t ld_out, int dtype,
+                               void *stream) {
+  if ((dtype != NS_F32 && dtype != NS_BF16) || (id_type != NS_I32 && id_type != NS_I64)) return NS_EINVAL;
+  if (bad_shape(vocab, dim, ld_table) || bad_shape(count, dim, ld_out)) return NS_EINVAL;
+  if (count == 0 || dim == 0) return NS_OK;
+  if (!ids || !out || (!table && vocab > 0)) return NS_EINVAL;
+  const int elt = dtype == NS_BF16 ? 2 : 4;
+  if (misaligned(table, elt) || misaligned(out, elt) || misaligned(ids, id_type == NS_I64 ? 8 : 4)) return NS_EALIGN;
+  const Range ro(out, count, dim, ld_out, elt);
+  if (ro.overlaps(Range(table, vocab, dim, ld_table, elt)) ||
+      ro.overlaps(Range(ids, 1, count, count, id_type == NS_I64 ? 8 : 4)))
+    return NS_EINVAL;
+  OpCall call(stream);
+  if (call.rc) return call.rc;
+  LookupParams p{table, out, {ids, id_type == NS_I64, static_cast<int>(vocab)}, count, ld_table, ld_out,
+                 static_cast<int>(dim), scale, call.status};
+  // 16-byte packs when every row allows them; else single elements
+  const int vec = 16 / elt;
+  const bool wide = dim % vec == 0 && rows_aligned(table, ld_table, elt, vec) && rows_aligned(out, ld_out, elt, vec);
+  return call.launch(kOpLookup, [&] {
+    if (dtype == NS_BF16) return wide ? run_lookup<kBF16, 8>(p, call.sms, call.s) : run_lookup<kBF16, 1>(p, call.sms, call.s);
+    return wide ? run_lookup<kF32, 4>(p, call.sms, call.s) : run_lookup<kF32, 1>(p, call.sms, call.s);
+  });
+}
+
+extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids, int id_type, int64_t count,
+                             float scale, void *grad, int64_t ld_grad, int64_t vocab, int64_t dim, int dtype,
+                             int grad_dtype, int accumulate, void *stream) {
+  if ((dtype != NS_F32 && dtype != NS_BF16) || (grad_dtype != NS_F32 && grad_dtype != NS_BF16) ||
+      (id_type != NS_I32 && id_type != NS_I64) || (accumulate != 0 && accumulate != 1))
+    return NS_EINVAL;
+  if (bad_shape(vocab, dim, ld_grad) || bad_shape(count, dim, ld_dout) || vocab >= INT32_MAX) return NS_EINVAL;
+  if (count > (1 << 30) || (count / kSeg + 1) * (dim / kSegThreads + 1) > INT32_MAX) return NS_EINVAL;
+  if (vocab == 0 || dim == 0 || (count == 0 && accumulate)) return NS_OK;
+  if (!grad || (count > 0 && (!ids || !dout))) return NS_EINVAL;
+  const int elt = dtype == NS_BF16 ? 2 : 4, gelt = grad_dtype == NS_BF16 ? 2 : 4;
+  if (misaligned(dout, elt) || misaligned(grad, gelt) || misaligned(ids, id_type == NS_I64 ? 8 : 4)) return NS_EALIGN;
+  const Range rg(grad, vocab, dim, ld_grad, gelt);
+  if (rg.overlaps(Range(dout, count, dim, ld_dout, elt)) ||
+      rg.overlaps(Range(ids, 1, count, count, id_type == NS_I64 ? 8 : 4)))
+    return NS_EINVAL;
+  OpCall call(stream);
+  if (call.rc) return call.rc;
+  const int n = static_cast<int>(count);
+  GradParams p{};
+  p.dout = dout;
+  p.grad = grad;
+  p.ld_dout = ld_dout;
+  p.ld_grad = ld_grad;
+  p.n = n;
+  p.vocab = static_cast<int>(vocab);
+  p.dim = static_cast<int>(dim);
+  p.dim_pad = static_cast<int>((dim + 7) / 8 * 8);
+  p.pieces = (n + kSeg - 1) / kSeg;
+  p.scale = scale;
+  p.accumulate = accumulate;
+  p.status = call.status;
+  const size_t list = (static_cast<size_t>(n) * 4 + 255) / 256 * 256;
+  uint8_t *ws = nullptr;
+  int rc = call.workspace(kSlotEmbed, 4 * list + static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, &ws);
+  if (rc) return rc;
+  SortParams sp{};
+  sp.ids = Ids{ids, id_type == NS_I64, p.vocab};
+  sp.n = n;
+  for (int k = 0; k < 2; ++k) {
+    sp.keys[k] = reinterpret_cast<int *>(ws + 2 * k * list);
+    sp.pos[k] = reinterpret_cast<int *>(ws + (2 * k + 1) * list);
+  }
+  int bits = 1;
+  while (bits < 31 && (vocab >> bits)) ++bits;  // keys are 0 .. vocab
+  sp.passes = (bits + 8) / 9;
+  sp.bits = (bits + sp.passes - 1) / sp.passes;
+  sp.status = call.status;
+  p.keys = sp.keys[0];
+  p.pos = sp.pos[0];
+  p.parts = reinterpret_cast<float *>(ws + 4 * list);
+  if (n > 0 && (rc = call.launch(kOpSort, [&] { return run_sort(sp, call.s); }))) return rc;
+  const int vec = 16 / elt;
+  const bool wide = dim % vec == 0 && rows_aligned(dout, ld_dout, elt, vec) && rows_aligned(grad, ld_grad, gelt, vec);
+  return call.launch(kOpEmbedGrad, [&] {
+    if (dtype == NS_BF16) {
+      if (grad_dtype == NS_BF16)
+        return wide ? run_grad<kBF16, kBF16, 8>(p, call.s) : run_grad<kBF16, kBF16, 1>(p, call.s);
+      return wide ? run_grad<kBF16, kF32, 8>(p, call.s) : run_grad<kBF16, kF32, 1>(p, call.s);
+    }
+    if (grad_dtype == NS_BF16) return wide ? run_grad<kF32, kBF16, 4>(p, call.s) : run_grad<kF32, kBF16, 1>(p, call.s);
+    return wide ? run_grad<kF32, kF32, 4>(p, call.s) : run_grad<kF32, kF32, 1>(p, call.s);
+  });
+}

@@ -33,7 +33,10 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <mutex>
 
 namespace ns {
 
@@ -228,5 +231,64 @@ struct SmemOptIn {
 // ns_orthogonalize_batched makes before launching) and the current-device
 // check: NS_OK, or the status code such a call would return.
 int check_call(void *const *X, const int64_t *shapes, int count, int steps, int dtype);
+
+// ------------------------------------------------------------ operator calls
+// Kinds of the training operators' launches (kernel timing, NVTX names),
+// after the Newton-Schulz kinds 0..8.
+enum OpKind : int {
+  kOpLookup = 9,
+  kOpSort,
+  kOpEmbedGrad,
+  kOpPolicy,
+  kOpCkpt,
+  kOpWgrad,
+  kOpKindEnd
+};
+// Workspace cache slots of the operators (one scratch per operator and
+// stream, so one operator's growth never moves another's scratch).
+enum OpSlot : int { kSlotEmbed = 1000, kSlotPolicy, kSlotWgrad };
+
+// One operator call, once its arguments are validated: holds the library's
+// lock, knows the current device (rc != NS_OK: unusable), and reaches the
+// workspace cache, the tensor-map encoder and the launch records.
+struct OpCall {
+  cudaStream_t s;
+  std::unique_lock<std::mutex> lock;
+  int rc = 0;
+  int dev = 0;
+  int sms = 0;
+  int *status = nullptr;
+  bool ranged = false;
+  explicit OpCall(void *stream);
+  ~OpCall();
+  int workspace(int slot, size_t bytes, uint8_t **ptr);
+  // elt 2: bf16 with 128-byte swizzle; elt 1: bytes without swizzle; reads outside give 0
+  int tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
+                 const int64_t *pitch_bytes, const int *box);
+  // fn() launches kernels of one kind and returns 0, or -1 on a launch error
+  template <typename F>
+  int launch(int kind, F &&fn) {
+    return timed_launch(kind, [](void *f) { return (*static_cast<F *>(f))(); }, &fn);
+  }
+
+ private:
+  int timed_launch(int kind, int (*fn)(void *), void *arg);
+};
+
+// Byte range of a rows x cols matrix with a row pitch, for overlap checks.
+struct Range {
+  uintptr_t begin, end;
+  Range(const void *p, int64_t rows, int64_t cols, int64_t ld, int elt)
+      : begin(reinterpret_cast<uintptr_t>(p)),
+        end(begin + (p && rows > 0 && cols > 0 ? static_cast<uintptr_t>((rows - 1) * ld + cols) * elt : 0)) {}
+  bool overlaps(const Range &o) const { return begin < o.end && o.begin < end; }
+};
+// Shape checks shared by the operators: sides in [0, 2^31), a pitch no shorter
+// than the row, fewer than 2^46 elements spanned.
+inline bool bad_shape(int64_t rows, int64_t cols, int64_t ld) {
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || ld < cols || ld > (int64_t(1) << 31)) return true;
+  return rows > 0 && ld > 0 && rows > (int64_t(1) << 46) / ld;
+}
+inline bool misaligned(const void *p, int to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
 }  // namespace ns
