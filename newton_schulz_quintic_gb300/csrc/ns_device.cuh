@@ -134,6 +134,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
   }
 }
 
+// A wait of a whole warp that only lane 0 polls (the other lanes sleep in
+// the shuffle that broadcasts the outcome), leaving the warp converged.
+template <bool kCluster>
+__device__ __forceinline__ bool warp_mbar_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster>(bar, parity, w) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // ---------------------------------------------------------------- counters
 __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
   int v;

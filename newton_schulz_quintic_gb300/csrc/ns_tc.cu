@@ -1023,15 +1023,6 @@ __device__ __forceinline__ bool epilogue_item_split(const StepCtx &sc, const Til
   return true;
 }
 
-// A wait of a whole warp that only lane 0 polls (the other lanes sleep in
-// the shuffle that broadcasts the outcome), leaving the warp converged.
-template <bool kCluster>
-__device__ __forceinline__ bool warp_mbar_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster>(bar, parity, w) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 // The producer's copies of one segment of an item in one CTA: for each
 // k-block, wait for the stage to be free, and load this CTA's share of both
 // operands (a0, b0: first tile row of each share) onto the leader's full
