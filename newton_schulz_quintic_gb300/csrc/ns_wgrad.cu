@@ -14,13 +14,15 @@
 //   0       TMA of dY: its 128 columns x 64 rows of a k-block (two 64 x 64
 //           boxes, 128-byte swizzle) into a 5-stage ring
 //   1       TMEM (two accumulators of 256 columns); in the leader the MMAs
-//   2, 3    X as it is held: q by TMA, a row's 4 scales per lane by cp.async,
-//           into a ring of their own, 4 k-blocks ahead
-//   4..7    X made bf16 (see widen4), from that ring to where the MMA reads
-//           it, in the swizzled layout. They also clear the rows beyond the
-//           group's end in both operands, so nothing of the next group
-//           (infinities, NaN) takes part, and then pass the stage on.
-//   8..15   sums: every kChunk k-blocks the accumulator is added to fp32
+//   2       X as it is held: q by TMA, the rows' scales by cp.async, into a
+//           ring of their own, up to 4 k-blocks ahead
+//   3       passes on to the MMA warp that dY has landed
+//   4..11   X made bf16 (see widen4), from that ring to where the MMA reads
+//           it, in the swizzled layout, two groups of four warps taking
+//           k-blocks in turn: what a warp spends on a k-block is mostly
+//           latency. They also clear the rows beyond the group's end in both
+//           operands, so nothing of the next group (infinities, NaN) takes part.
+//   12..19  sums: every kChunk k-blocks the accumulator is added to fp32
 //           registers (128 columns x 1 row per thread) while the MMAs go on in
 //           the other one; the tile is written at its end. The tensor cores'
 //           own accumulation loses up to a unit in the last place per
@@ -29,8 +31,8 @@
 // X goes through shared memory twice because loads into registers do not
 // stay in flight here: the proxy fence and the release of a stage wait for
 // them (measured: 6600 cycles per k-block against 512 of MMA).
-// Registers are split by warpgroup with setmaxnreg: 176 for the sums, 80
-// elsewhere, together the 128 x 512 the CTA is launched with.
+// Registers are split by warpgroup with setmaxnreg: 160 for the sums, 48
+// elsewhere, together no more than the 96 x 640 the CTA is launched with.
 //
 // fp32 dY is held as three bf16 slices (the h + m + l of ns_tc.cu) and the
 // k-loop runs over the slices too, smallest first; X needs no slices. A dY that
@@ -56,8 +58,9 @@ constexpr int kRawScales = 4 * kBK;              // and their scales
 constexpr int kShare = 128 * kBK * 2;            // one operand's share of a stage: 16 KB
 constexpr int kBoxBytes = 64 * kBK * 2;          // one TMA box
 constexpr int kChunk = 8;                        // k-blocks between two drains of an accumulator
-constexpr int kThreads = 512;
-constexpr int kConvWarps = 4, kSumWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kConvWarps = 4, kConvGroups = 2, kSumWarps = 8;
+constexpr int kConv0 = 4, kSum0 = kConv0 + kConvWarps * kConvGroups;  // first warps of the roles
 constexpr int kTmemCols = 512;
 constexpr int kPatch = 32 * 32 * 4;              // staging of one 32 x 32 block per sum warp
 
@@ -86,6 +89,7 @@ struct WgradBarriers {
   uint64_t tfull[2];         // each CTA: an accumulator holds a chunk
   uint64_t tempty[2];        // leader: both CTAs have drained an accumulator
   uint64_t drain;
+  int left[kRawStages];      // rows of the group in this k-block and after; -1: no more
   uint32_t tmem_base;
   int abort;
 };
@@ -147,10 +151,12 @@ __device__ __forceinline__ void tma_bytes(void *dst, const void *map, int x, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// 4 bytes to shared memory, zeros when !inside; the arrival on `bar` (one of
-// its expected count) follows this thread's copies.
-__device__ __forceinline__ void copy4_and_arrive(void *dst, const void *src, bool inside, uint64_t *bar) {
+// 4 bytes to shared memory, zeros when !inside.
+__device__ __forceinline__ void copy4(void *dst, const void *src, bool inside) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(inside ? 4 : 0) : "memory");
+}
+// One of the barrier's expected arrivals, made when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void tma_box(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
@@ -166,6 +172,17 @@ __device__ __forceinline__ void tma_box(void *dst, const void *map, int x, int y
 // wait for every outstanding access of the warp, the loads ahead included.
 __device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// 32 lanes x 16 columns of TMEM words, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -278,7 +295,8 @@ __device__ __forceinline__ void store_tile(const WgradParams &p, const WTile &t,
 
 __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_constant__ WgradParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // 1024-byte aligned, by an offset so that accesses stay in the shared window
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *sA = smem, *sB = smem + kStages * kShare;
   uint8_t *sQ = smem + 2 * kStages * kShare, *sS = sQ + kRawStages * kRaw;
   WgradBarriers *bar = reinterpret_cast<WgradBarriers *>(sS + kRawStages * kRawScales);
@@ -291,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar->afull[s], 1);
-      mbar_init(&bar->ready[s], 2 * kConvWarps);
+      mbar_init(&bar->ready[s], 2 * (kConvWarps + 1));
       mbar_init(&bar->empty[s], 1);
     }
     for (int s = 0; s < kRawStages; ++s) {
-      mbar_init(&bar->rawfull[s], 1 + kBK);
+      mbar_init(&bar->rawfull[s], 1 + 32);
       mbar_init(&bar->rawempty[s], kConvWarps);
     }
     for (int a = 0; a < 2; ++a) {
@@ -320,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   volatile int *abort = &bar->abort;
   const Waiter w{abort, p.status, p.wait_limit_ns};
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp < kConv0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (tmem_ok && warp == 0) {
       // -------------------------------------------------- dY by TMA
       if (lane == 0) {
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
         uint32_t issued = 0, last = 0;  // per stage: whether copies were issued, the parity of the last
         BlockWalk k;
         for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-          if (!mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
+          if (!mbar_wait<true, 40>(&bar->empty[stage], parity ^ 1u, w)) break;
           mbar_arrive_expect_tx(&bar->afull[stage], kShare);
           const int x = k.t.n0 + static_cast<int>(rank) * 128, y = k.t.lo + k.b * kBK;
           tma_box(sA + stage * kShare, &p.tm_dy, x, y, k.z, &bar->afull[stage]);
@@ -346,25 +364,42 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
           for (int s = 0; s < kStages; ++s)
             if ((issued >> s) & 1u) drain_wait(&bar->afull[s], (last >> s) & 1u, w.limit_ns);
       }
-    } else if (tmem_ok && warp >= 2) {
+    } else if (tmem_ok && warp == 2) {
       // -------------------------------------------------- X as it is held
-      const int row_in = (warp - 2) * 32 + lane;
       int raw = 0;
       uint32_t parity = 0;
       uint32_t issued = 0, last = 0;
+      int end = 0;  // end marks published, one for each converter group
       BlockWalk k;
-      for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-        if (!warp_mbar_wait<false>(&bar->rawempty[raw], parity ^ 1u, w)) break;
-        const int col0 = k.t.k0 + static_cast<int>(rank) * 128, row = k.t.lo + k.b * kBK + row_in;
-        if (warp == 2 && lane == 0) {
-          mbar_arrive_expect_tx(&bar->rawfull[raw], kRaw);
-          tma_bytes(sQ + raw * kRaw, &p.tm_q, col0, k.t.lo + k.b * kBK, &bar->rawfull[raw]);
+      k.start(p, pair, npairs);
+      while (end < kConvGroups) {
+        if (!warp_mbar_wait<false, 40>(&bar->rawempty[raw], parity ^ 1u, w)) break;
+        if (k.done) {
+          if (lane == 0) {
+            bar->left[raw] = -1;
+            mbar_arrive(&bar->rawfull[raw]);
+          }
+          mbar_arrive(&bar->rawfull[raw]);
+          ++end;
+        } else {
+          const int col0 = k.t.k0 + static_cast<int>(rank) * 128, row0 = k.t.lo + k.b * kBK;
+          if (lane == 0) {
+            bar->left[raw] = k.t.hi - row0;
+            mbar_arrive_expect_tx(&bar->rawfull[raw], kRaw);
+            tma_bytes(sQ + raw * kRaw, &p.tm_q, col0, row0, &bar->rawfull[raw]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = row0 + h * 32 + lane;
+            const bool inside = row < k.t.hi && col0 / 32 < p.scale_pitch;
+            copy4(sS + raw * kRawScales + 4 * (h * 32 + lane),
+                  inside ? p.s + static_cast<int64_t>(row) * p.scale_pitch + col0 / 32 : p.s, inside);
+          }
+          arrive_after_copies(&bar->rawfull[raw]);
+          issued |= 1u << raw;
+          last = (last & ~(1u << raw)) | (parity << raw);
+          k.next(p, npairs);
         }
-        const bool inside = row < k.t.hi && col0 / 32 < p.scale_pitch;
-        copy4_and_arrive(sS + raw * kRawScales + 4 * row_in,
-                         inside ? p.s + static_cast<int64_t>(row) * p.scale_pitch + col0 / 32 : p.s, inside, &bar->rawfull[raw]);
-        issued |= 1u << raw;
-        last = (last & ~(1u << raw)) | (parity << raw);
         if (++raw == kRawStages) {
           raw = 0;
           parity ^= 1u;
@@ -373,6 +408,21 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       if (*abort)
         for (int s = 0; s < kRawStages; ++s)
           if ((issued >> s) & 1u) drain_wait(&bar->rawfull[s], (last >> s) & 1u, w.limit_ns);
+    } else if (tmem_ok && warp == 3) {
+      // -------------------------------------------------- dY landed
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t parity = 0;
+        BlockWalk k;
+        for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
+          if (!mbar_wait<true, 20>(&bar->afull[stage], parity, w)) break;
+          arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
+      }
     } else if (tmem_ok && warp == 1 && leader) {
       // -------------------------------------------------- MMAs
       constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
@@ -427,54 +477,60 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       }
       __syncwarp();
     }
-  } else if (warp < 4 + kConvWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  } else if (warp < kSum0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (tmem_ok) {
       // -------------------------------------------------- X to bf16
-      const int j = lane & 7, row_in = (warp - 4) * 4 + (lane >> 3);
+      const int group = (warp - kConv0) / kConvWarps, part = (warp - kConv0) % kConvWarps;
+      const int j = lane & 7, row_in = part * 4 + (lane >> 3);
       // 16 values are two 16-byte pieces of a 64-column box row; lanes of the
       // right box store their second piece first, so the 8 lanes of a row
       // cover all banks
-      const int box = (j >> 2) * kBoxBytes, p0 = 2 * (j & 3) + (j >> 2), p1 = p0 ^ 1;
-      int stage = 0, raw = 0;
+      // (the swizzle depends on the row modulo 8, the same for a lane's four rows)
+      const int out0 = (j >> 2) * kBoxBytes + row_in * 128 + (((2 * (j & 3) + (j >> 2)) ^ (row_in & 7)) << 4);
+      const int out1 = out0 ^ 16, in = row_in * 128 + j * 16, in_scale = 4 * row_in + (j >> 1);
+      const bool swap = j >> 2;
+      int stage = group, raw = group;  // k-blocks group, group + kConvGroups, ...
       uint32_t parity = 0, raw_parity = 0;
-      BlockWalk k;
-      for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-        const int left = k.t.hi - k.t.lo - k.b * kBK;  // rows of the group in this block
+      for (;;) {
         if (!warp_mbar_wait<false>(&bar->rawfull[raw], raw_parity, w)) break;
+        const int left = bar->left[raw];
+        if (left < 0) break;
         uint4 q[4];
         uint32_t sc[4];
+        const uint8_t *src = sQ + raw * kRaw + in, *scales = sS + raw * kRawScales + in_scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = i * 16 + row_in;
-          q[i] = *reinterpret_cast<const uint4 *>(sQ + raw * kRaw + r * 128 + j * 16);
-          sc[i] = sS[raw * kRawScales + 4 * r + (j >> 1)];
-          if (r >= left) q[i] = make_uint4(0, 0, 0, 0);  // and its scale is 0: the value is 0
+          q[i] = *reinterpret_cast<const uint4 *>(src + i * 2048);
+          sc[i] = scales[i * 64];
+        }
+        if (left < kBK) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i * 16 + row_in >= left) q[i] = make_uint4(0, 0, 0, 0);  // and its scale is 0: the value is 0
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->rawempty[raw]);
-        if (++raw == kRawStages) {
-          raw = 0;
+        if ((raw += kConvGroups) >= kRawStages) {
+          raw -= kRawStages;
           raw_parity ^= 1u;
         }
         if (!warp_mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
-        uint8_t *dst = sB + stage * kShare + box;
+        uint8_t *dst0 = sB + stage * kShare + out0, *dst1 = sB + stage * kShare + out1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = i * 16 + row_in;
           const __nv_bfloat162 unit = unit_pair(sc[i]);
           uint4 a, b;
           widen4(q[i].x, unit, a.x, a.y);
           widen4(q[i].y, unit, a.z, a.w);
           widen4(q[i].z, unit, b.x, b.y);
           widen4(q[i].w, unit, b.z, b.w);
-          const bool swap = j >> 2;
-          *reinterpret_cast<uint4 *>(dst + r * 128 + ((p0 ^ (r & 7)) << 4)) = swap ? b : a;
-          *reinterpret_cast<uint4 *>(dst + r * 128 + ((p1 ^ (r & 7)) << 4)) = swap ? a : b;
+          *reinterpret_cast<uint4 *>(dst0 + i * 2048) = swap ? b : a;
+          *reinterpret_cast<uint4 *>(dst1 + i * 2048) = swap ? a : b;
         }
-        if (!warp_mbar_wait<true>(&bar->afull[stage], parity, w)) break;
         if (left < kBK) {  // clear dY beyond the group's end: 64 rows of 8 pieces in each box
-          for (int i = (warp - 4) * 32 + lane; i < 2 * kBK * 8; i += 32 * kConvWarps) {
+          if (!warp_mbar_wait<true>(&bar->afull[stage], parity, w)) break;
+          for (int i = part * 32 + lane; i < 2 * kBK * 8; i += 32 * kConvWarps) {
             const int r = (i >> 3) & (kBK - 1);
             if (r >= left)
               *reinterpret_cast<uint4 *>(sA + stage * kShare + (i >> 9) * kBoxBytes + r * 128 + (i & 7) * 16) =
@@ -484,17 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
-        if (++stage == kStages) {
-          stage = 0;
+        if ((stage += kConvGroups) >= kStages) {
+          stage -= kStages;
           parity ^= 1u;
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     if (tmem_ok) {
       // -------------------------------------------------- sums and the tile's store
-      const int e = warp - 8, quarter = warp & 3, half = e >> 2;
+      const int e = warp - kSum0, quarter = warp & 3, half = e >> 2;
       float *patch = patches + e * (kPatch / 4);
       int acc = 0;
       uint32_t acc_parity = 0;
@@ -507,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < 128; ++c) sum[c] = 0.f;
         for (int c = 0; c < nb; c += kChunk) {
-          if (!warp_mbar_wait<true>(&bar->tfull[acc], acc_parity, w)) {
+          if (!warp_mbar_wait<true, 100>(&bar->tfull[acc], acc_parity, w)) {
             ok = false;
             break;
           }
@@ -515,12 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
           tc_fence_after();
           const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[32];
-            tmem_ld32(src + 32 * k, v);
-            tmem_ld_wait(v);
+          for (int k = 0; k < 8; ++k) {
+            uint32_t v[16];
+            tmem_ld16(src + 16 * k, v);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) sum[32 * k + u] += __uint_as_float(v[u]);
+            for (int u = 0; u < 16; ++u) sum[16 * k + u] += __uint_as_float(v[u]);
           }
           tc_fence_before();
           __syncwarp();
