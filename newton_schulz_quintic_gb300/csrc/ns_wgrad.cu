@@ -133,17 +133,6 @@ __device__ __forceinline__ WTile wtile(const WgradParams &p, int item) {
   return t;
 }
 
-// The order of a tile's k-blocks: chunks of kChunk blocks, in each the
-// slices from smallest to largest, in each slice the chunk's blocks.
-template <typename F>
-__device__ __forceinline__ bool for_blocks(int blocks, int c, int slices, F &&f) {
-  const int end = min(c + kChunk, blocks);
-  for (int z = slices - 1; z >= 0; --z)
-    for (int b = c; b < end; ++b)
-      if (!f(b, z)) return false;
-  return true;
-}
-
 __device__ __forceinline__ void tma_bytes(void *dst, const void *map, int x, int y, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -188,20 +177,26 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Four int8 to two bf16 pairs, times a power of two. With l the low 7 bits of
-// a byte and s its sign bit, q = l - 128 s; the bf16 0x4300 | l is 128 + l
-// and 0xC300 | (s << 7) is -(128 + 128 s), so their sum is q, exact in bf16
-// (as is the product: no bits are added, and units are at least 2^-126).
-__device__ __forceinline__ void widen4(uint32_t w, __nv_bfloat162 unit, uint32_t &lo, uint32_t &hi) {
-  const uint32_t l = w & 0x7f7f7f7fu, s = w & 0x80808080u;
-  const uint32_t a0 = __byte_perm(l, 0x43434343u, 0x4140), a1 = __byte_perm(l, 0x43434343u, 0x4342);
-  const uint32_t b0 = __byte_perm(s, 0xC3C3C3C3u, 0x4140), b1 = __byte_perm(s, 0xC3C3C3C3u, 0x4342);
-  auto two = [](const uint32_t &v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+// Four int8 (bytes 0..3 of w) to two bf16 pairs, times a power of two. With l
+// the low 7 bits of a byte and s its sign bit, q = l - 128 s; the bf16 0x4300 |
+// l is 128 + l and 0xC300 | (s << 7) is -(128 + 128 s), so their sum is q,
+// exact in bf16 (as is the product: no bits are added, and units are at least
+// 2^-126). Even bytes make the first pair, odd ones the second, which
+// saves the byte shuffles: the second and third column of every four change
+// places in shared memory and in the accumulator, and the store puts them back
+// (true_column).
+__device__ __forceinline__ void widen4(uint32_t w, __nv_bfloat162 unit, uint32_t &even, uint32_t &odd) {
+  const uint32_t v = w >> 8;
+  const uint32_t a0 = (w & 0x007f007fu) | 0x43004300u, b0 = (w & 0x00800080u) | 0xC300C300u;
+  const uint32_t a1 = (v & 0x007f007fu) | 0x43004300u, b1 = (v & 0x00800080u) | 0xC300C300u;
+  auto two = [](const uint32_t &x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
   const __nv_bfloat162 r0 = __hmul2(__hadd2(two(a0), two(b0)), unit);
   const __nv_bfloat162 r1 = __hmul2(__hadd2(two(a1), two(b1)), unit);
-  lo = *reinterpret_cast<const uint32_t *>(&r0);
-  hi = *reinterpret_cast<const uint32_t *>(&r1);
+  even = *reinterpret_cast<const uint32_t *>(&r0);
+  odd = *reinterpret_cast<const uint32_t *>(&r1);
 }
+// accumulator column of matrix column c (and back)
+__device__ constexpr int true_column(int c) { return (c & 3) == 1 ? c + 1 : (c & 3) == 2 ? c - 1 : c; }
 // 2^(e - 133) twice as bf16 (e below 7 reads as 7; 255 as NaN)
 __device__ __forceinline__ __nv_bfloat162 unit_pair(uint32_t e) {
   const uint32_t u = e == 255u ? 0x7fc0u : (max(e, 7u) - 6u) << 7;
@@ -209,7 +204,18 @@ __device__ __forceinline__ __nv_bfloat162 unit_pair(uint32_t e) {
   return *reinterpret_cast<const __nv_bfloat162 *>(&v);
 }
 
-// The k-blocks of a pair's whole work list in order, for the roles that look ahead.
+// A wait of a whole warp that is over as a rule: every lane polls once, and
+// only if that fails lane 0 goes on polling for all.
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
+  const bool ok = kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return warp_mbar_wait<kCluster>(bar, parity, w);
+}
+
+// The k-blocks of a pair's whole work list in order: tile by tile, a tile's
+// chunks of kChunk blocks, in each the slices of dY from smallest to largest,
+// in each slice the chunk's blocks.
 struct BlockWalk {
   WTile t;
   int item, c, z, b;  // current block: chunk start, slice, block
@@ -272,7 +278,7 @@ __device__ __forceinline__ void store_tile(const WgradParams &p, const WTile &t,
     __syncwarp();
     // row lane, column c at word (c ^ lane): no bank conflict either way
 #pragma unroll
-    for (int c = 0; c < 32; ++c) patch[lane * 32 + (c ^ lane)] = acc[32 * k + c];
+    for (int c = 0; c < 32; ++c) patch[lane * 32 + (c ^ lane)] = acc[32 * k + true_column(c)];
     __syncwarp();
     const int col = col0 + 32 * k + lane;
     if (col >= p.n_in) continue;
@@ -424,58 +430,44 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
         }
       }
     } else if (tmem_ok && warp == 1 && leader) {
-      // -------------------------------------------------- MMAs
-      constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
-      int stage = 0, acc = 0;
-      uint32_t parity = 0, acc_parity = 0;
-      bool ok = true;
-      for (int item = pair; ok && item < p.items; item += npairs) {
-        const WTile t = wtile(p, item);
-        const int nb = t.blocks();
-        for (int c = 0; ok && c < nb; c += kChunk) {
-          if (!warp_mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
-          tc_fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-          uint32_t more = 0;
-          ok = for_blocks(nb, c, p.slices, [&](int, int) {
-            if (!warp_mbar_wait<true>(&bar->ready[stage], parity, w)) return false;
-            __syncwarp();
+      // -------------------------------------------------- MMAs, issued by one lane
+      if (lane == 0) {
+        constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
+        const uint64_t desc_a = sw128_mnmajor_desc(smem_u32(sA)), desc_b = sw128_mnmajor_desc(smem_u32(sB));
+        int stage = 0, acc = 0;
+        uint32_t parity = 0, acc_parity = 0;
+        bool ok = true;
+        for (int item = pair; ok && item < p.items; item += npairs) {
+          const int nb = wtile(p, item).blocks();
+          for (int c = 0; ok && c < nb; c += kChunk) {
+            if (!(ok = mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
             tc_fence_after();
-            const uint32_t a = smem_u32(sA + stage * kShare), b = smem_u32(sB + stage * kShare);
-            if (elect_one()) {
+            const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+            const int n = min(kChunk, nb - c) * p.slices;
+            for (int i = 0; i < n; ++i) {
+              if (!(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
+              tc_fence_after();
+              const uint64_t at = static_cast<uint64_t>(stage * (kShare >> 4));  // addresses are in 16-byte units
 #pragma unroll
-              for (int k = 0; k < kBK / 16; ++k) {
-                umma_bf16_pair(d, sw128_mnmajor_desc(a + k * 2048u), sw128_mnmajor_desc(b + k * 2048u), idesc, more | (k > 0));
-              }
+              for (int k = 0; k < kBK / 16; ++k)
+                umma_bf16_pair(d, desc_a + at + k * 128u, desc_b + at + k * 128u, idesc, i > 0 || k > 0);
               umma_commit_pair_multicast(&bar->empty[stage], 3u);
+              if (++stage == kStages) {
+                stage = 0;
+                parity ^= 1u;
+              }
             }
-            __syncwarp();
-            more = 1;
-            if (++stage == kStages) {
-              stage = 0;
-              parity ^= 1u;
+            if (!ok) break;
+            umma_commit_pair_multicast(&bar->tfull[acc], 3u);
+            if (++acc == 2) {
+              acc = 0;
+              acc_parity ^= 1u;
             }
-            return true;
-          });
-          if (!ok) break;
-          if (elect_one()) umma_commit_pair_multicast(&bar->tfull[acc], 3u);
-          __syncwarp();
-          if (++acc == 2) {
-            acc = 0;
-            acc_parity ^= 1u;
           }
         }
-      }
-      __syncwarp();
-      if (elect_one()) {
         umma_commit_pair_multicast(&bar->drain, 1u);
         drain_wait(&bar->drain, 0, w.limit_ns);
       }
-      __syncwarp();
     }
   } else if (warp < kSum0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -483,31 +475,33 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       // -------------------------------------------------- X to bf16
       const int group = (warp - kConv0) / kConvWarps, part = (warp - kConv0) % kConvWarps;
       const int j = lane & 7, row_in = part * 4 + (lane >> 3);
-      // 16 values are two 16-byte pieces of a 64-column box row; lanes of the
-      // right box store their second piece first, so the 8 lanes of a row
-      // cover all banks
-      // (the swizzle depends on the row modulo 8, the same for a lane's four rows)
-      const int out0 = (j >> 2) * kBoxBytes + row_in * 128 + (((2 * (j & 3) + (j >> 2)) ^ (row_in & 7)) << 4);
-      const int out1 = out0 ^ 16, in = row_in * 128 + j * 16, in_scale = 4 * row_in + (j >> 1);
-      const bool swap = j >> 2;
+      // 16 values are two 16-byte pieces of a 64-column box row. Half of the
+      // lanes take their second piece first: the 8 lanes that store one row
+      // then cover all banks, and so do the 16 that read two rows. The
+      // swizzle depends on the row modulo 8, the same for a lane's four rows.
+      const int swap = ((j >> 2) ^ row_in) & 1;
+      const int out0 = (j >> 2) * kBoxBytes + row_in * 128 + (((2 * (j & 3) + swap) ^ (row_in & 7)) << 4);
+      const int out1 = out0 ^ 16, in = row_in * 128 + j * 16 + 8 * swap, in_scale = 4 * row_in + (j >> 1);
       int stage = group, raw = group;  // k-blocks group, group + kConvGroups, ...
       uint32_t parity = 0, raw_parity = 0;
       for (;;) {
-        if (!warp_mbar_wait<false>(&bar->rawfull[raw], raw_parity, w)) break;
+        if (!warp_wait<false>(&bar->rawfull[raw], raw_parity, w)) break;
         const int left = bar->left[raw];
         if (left < 0) break;
-        uint4 q[4];
+        uint2 q0[4], q1[4];
         uint32_t sc[4];
-        const uint8_t *src = sQ + raw * kRaw + in, *scales = sS + raw * kRawScales + in_scale;
+        const uint8_t *src0 = sQ + raw * kRaw + in, *src1 = sQ + raw * kRaw + (in ^ 8);
+        const uint8_t *scales = sS + raw * kRawScales + in_scale;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          q[i] = *reinterpret_cast<const uint4 *>(src + i * 2048);
+          q0[i] = *reinterpret_cast<const uint2 *>(src0 + i * 2048);
+          q1[i] = *reinterpret_cast<const uint2 *>(src1 + i * 2048);
           sc[i] = scales[i * 64];
         }
         if (left < kBK) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i * 16 + row_in >= left) q[i] = make_uint4(0, 0, 0, 0);  // and its scale is 0: the value is 0
+            if (i * 16 + row_in >= left) q0[i] = q1[i] = make_uint2(0, 0);  // and its scale is 0: the value is 0
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->rawempty[raw]);
@@ -515,18 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
           raw -= kRawStages;
           raw_parity ^= 1u;
         }
-        if (!warp_mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
+        if (!warp_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
         uint8_t *dst0 = sB + stage * kShare + out0, *dst1 = sB + stage * kShare + out1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const __nv_bfloat162 unit = unit_pair(sc[i]);
-          uint4 a, b;
-          widen4(q[i].x, unit, a.x, a.y);
-          widen4(q[i].y, unit, a.z, a.w);
-          widen4(q[i].z, unit, b.x, b.y);
-          widen4(q[i].w, unit, b.z, b.w);
-          *reinterpret_cast<uint4 *>(dst0 + i * 2048) = swap ? b : a;
-          *reinterpret_cast<uint4 *>(dst1 + i * 2048) = swap ? a : b;
+          uint4 a;
+          widen4(q0[i].x, unit, a.x, a.y);
+          widen4(q0[i].y, unit, a.z, a.w);
+          *reinterpret_cast<uint4 *>(dst0 + i * 2048) = a;
+          widen4(q1[i].x, unit, a.x, a.y);
+          widen4(q1[i].y, unit, a.z, a.w);
+          *reinterpret_cast<uint4 *>(dst1 + i * 2048) = a;
         }
         if (left < kBK) {  // clear dY beyond the group's end: 64 rows of 8 pieces in each box
           if (!warp_mbar_wait<true>(&bar->afull[stage], parity, w)) break;
