@@ -916,11 +916,9 @@ int OpCall::tensor_map(CUtensorMap *map, int elt, const void *base, int rank, co
     bx[i] = static_cast<cuuint32_t>(box[i]);
     if (i) st[i - 1] = static_cast<cuuint64_t>(pitch_bytes[i - 1]);
   }
-  const bool wide = elt == 2;
-  const CUresult r = g_encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+  const CUresult r = g_encode(map, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                               static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, bx, one,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? NS_OK : NS_ECUDA;
 }

@@ -116,15 +116,12 @@ struct Waiter {
 // Wait for the phase of `bar` with parity `parity` to complete. Gives up
 // after w.limit_ns or once *w.abort is set; on giving up it sets *w.abort and
 // records the timeout in the status word. Returns true if the phase completed.
-// kSleepNs: pause between polls, for waits that are long as a rule, so that
-// the poller leaves the issue slots to the other warps of its scheduler.
-template <bool kCluster = false, int kSleepNs = 0>
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
   auto test = [&] { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
   if (test()) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (kSleepNs) __nanosleep(kSleepNs);
     if (test()) return true;
     if ((it & 255u) == 0) {
       if (*w.abort) return false;
@@ -139,10 +136,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
 
 // A wait of a whole warp that only lane 0 polls (the other lanes sleep in
 // the shuffle that broadcasts the outcome), leaving the warp converged.
-template <bool kCluster, int kSleepNs = 0>
+template <bool kCluster>
 __device__ __forceinline__ bool warp_mbar_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster, kSleepNs>(bar, parity, w) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster>(bar, parity, w) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 

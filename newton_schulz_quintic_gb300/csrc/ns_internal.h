@@ -262,7 +262,7 @@ struct OpCall {
   explicit OpCall(void *stream);
   ~OpCall();
   int workspace(int slot, size_t bytes, uint8_t **ptr);
-  // elt 2: bf16 with 128-byte swizzle; elt 1: bytes without swizzle; reads outside give 0
+  // elt 2: bf16, elt 4: fp32; 128-byte swizzle; reads outside give 0, writes outside are dropped
   int tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
                  const int64_t *pitch_bytes, const int *box);
   // fn() launches kernels of one kind and returns 0, or -1 on a launch error

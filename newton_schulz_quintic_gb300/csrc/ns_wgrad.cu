@@ -2,43 +2,43 @@
 // (include/ns.h): G[e] (+)= dY[e]^T X[e] over the rows of each group.
 //
 // A GEMM whose contraction runs over rows (tokens): both operands are
-// MN-major as they lie in memory. A value of X is q * 2^(E - 133) with |q| <=
-// 127, exact in bf16, so X is turned into bf16 on its way into shared memory
-// and the product runs at the bf16 rate of the tensor cores with no rounding
-// of X; HBM and L2 move one byte per value of X instead of two.
+// MN-major as they lie in memory, and the tensor cores read them so. A value
+// of X is q * 2^(E - 133) with |q| <= 127, exact in bf16, so the product runs
+// at the bf16 rate with no rounding of X.
 //
-// One persistent kernel of CTA pairs (clusters of 2), one 256 x 256 tile of one
-// group's G at a time (tcgen05.mma.cta_group::2, M = 256, N = 256, K = 16).
-// CTA rank r holds rows (n_out) r*128.. and columns (n_in) r*128.. of the
-// operands. Warps of a CTA:
-//   0       TMA of dY: its 128 columns x 64 rows of a k-block (two 64 x 64
-//           boxes, 128-byte swizzle) into a 5-stage ring
+// X is widened to bf16 in scratch first, one pass over it (with fp32 dY, dY's
+// slices in the same launch). Widening inside the product, on the way to
+// shared memory, was built and measured: every tile of X is then widened
+// again for each tile row of G (32 times at 8192 x 6144), which took 2400 warp
+// instructions and 570 cycles of shared-memory traffic per 64 rows next to the
+// 512 cycles of MMA, 767 us at 8192 x 8192 x 6144.
+//
+// The product is one persistent kernel of CTA pairs (clusters of 2), one 256 x
+// 256 tile of one group's G at a time (tcgen05.mma.cta_group::2, M = 256, N =
+// 256, K = 16). CTA rank r holds rows (n_out) r*128.. and columns (n_in)
+// r*128.. of the operands. Warps of a CTA:
+//   0       TMA: 64 rows of its share of dY and X (two 64 x 64 boxes each,
+//           128-byte swizzle) into a 6-stage ring
 //   1       TMEM (two accumulators of 256 columns); in the leader the MMAs
-//   2       X as it is held: q by TMA, the rows' scales by cp.async, into a
-//           ring of their own, up to 4 k-blocks ahead
-//   3       passes on to the MMA warp that dY has landed
-//   4..11   X made bf16 (see widen4), from that ring to where the MMA reads
-//           it, in the swizzled layout, two groups of four warps taking
-//           k-blocks in turn: what a warp spends on a k-block is mostly
-//           latency. They also clear the rows beyond the group's end in both
-//           operands, so nothing of the next group (infinities, NaN) takes part.
-//   12..19  sums: every kChunk k-blocks the accumulator is added to fp32
+//   2       passes a landed stage on to the MMAs. Where a group ends inside the
+//           stage it first clears the rows beyond, in both operands, so that
+//           nothing of the next group (infinities, NaN) takes part.
+//   4..11   sums: every kChunk k-blocks the accumulator is added to fp32
 //           registers (128 columns x 1 row per thread) while the MMAs go on in
 //           the other one; the tile is written at its end. The tensor cores'
 //           own accumulation loses up to a unit in the last place per
 //           instruction; 32 instructions between two drains keep that near
 //           2^-21 of the sum for any number of rows.
-// X goes through shared memory twice because loads into registers do not
-// stay in flight here: the proxy fence and the release of a stage wait for
-// them (measured: 6600 cycles per k-block against 512 of MMA).
-// Registers are split by warpgroup with setmaxnreg: 160 for the sums, 48
-// elsewhere, together no more than the 96 x 640 the CTA is launched with.
+// The tile leaves through TMA where G's rows are 16-byte aligned: overwritten,
+// or (fp32) added in place, which is one rounding of old + sum; else
+// element by element.
 //
 // fp32 dY is held as three bf16 slices (the h + m + l of ns_tc.cu) and the
-// k-loop runs over the slices too, smallest first; X needs no slices. A dY that
-// TMA cannot address (pitch or base not on 16 bytes) is copied to a padded
-// buffer first. When there are fewer tiles than CTA pairs the rows are split
-// and the parts, fp32 in scratch, are added in order by a second kernel.
+// k-loop runs over the slices too, smallest first; X needs no slices. A bf16
+// dY that TMA cannot address (pitch or base not on 16 bytes) is copied to a
+// padded buffer the same way. When there are fewer tiles than CTA pairs the
+// rows are split and the parts, fp32 in scratch, are added in order by a
+// second kernel.
 // Every wait is bounded (mbar_wait): on a timeout the status word is set, the
 // CTA waits for its own copies and MMAs, frees TMEM and exits.
 #include <algorithm>
@@ -51,50 +51,46 @@ namespace ns {
 namespace {
 
 constexpr int kBK = 64;                          // rows per k-block
-constexpr int kStages = 5;
-constexpr int kRawStages = 4;                    // k-blocks of X as it is held
-constexpr int kRaw = 128 * kBK;                  // q of this CTA's 128 columns: 8 KB
-constexpr int kRawScales = 4 * kBK;              // and their scales
+constexpr int kStages = 6;
 constexpr int kShare = 128 * kBK * 2;            // one operand's share of a stage: 16 KB
 constexpr int kBoxBytes = 64 * kBK * 2;          // one TMA box
 constexpr int kChunk = 8;                        // k-blocks between two drains of an accumulator
-constexpr int kThreads = 640;
-constexpr int kConvWarps = 4, kConvGroups = 2, kSumWarps = 8;
-constexpr int kConv0 = 4, kSum0 = kConv0 + kConvWarps * kConvGroups;  // first warps of the roles
+constexpr int kThreads = 384;
+constexpr int kSum0 = 4, kSumWarps = 8;
 constexpr int kTmemCols = 512;
-constexpr int kPatch = 32 * 32 * 4;              // staging of one 32 x 32 block per sum warp
+constexpr int kPatch = 32 * 32 * 4;              // staging of a block of 32 rows x 128 bytes per sum warp
+
+enum Store : int { kStoreTma, kStoreTmaAdd, kStorePlain };
 
 struct WgradParams {
   CUtensorMap tm_dy;       // bf16 {n_out, rows, slices}, box {64, 64, 1}
-  CUtensorMap tm_q;        // bytes {n_in, rows}, box {128, 64}
-  const uint8_t *s;
+  CUtensorMap tm_x;        // bf16 {n_in, rows}, box {64, 64}
+  CUtensorMap tm_out;      // G, or the parts when splits > 1: {n_in, n_out, matrices}, box of 128 bytes x 32 rows
   const int32_t *offsets;  // nullptr: one group of all rows
   void *grad;              // groups x n_out x n_in
-  float *parts;            // splits x groups x n_out x n_in when splits > 1
-  int rows, n_out, n_in, scale_pitch, groups;
+  float *parts;            // splits x groups x n_out x part_pitch when splits > 1
+  int rows, n_out, n_in, groups;
+  int part_pitch;
   int slices;              // bf16 slices of dY (1 or 3)
   int splits;              // parts of a group's rows
   int tn, tk, items;       // tiles along n_out and n_in; groups * tn * tk * splits
-  int accumulate, gdtype;
+  int accumulate, gdtype, store;
   int *status;
   uint64_t wait_limit_ns;
 };
 
 struct WgradBarriers {
-  uint64_t afull[kStages];   // this CTA's dY boxes landed
+  uint64_t full[kStages];    // this CTA's boxes of a stage landed
   uint64_t ready[kStages];   // leader: both CTAs' operands of a stage are in place
   uint64_t empty[kStages];   // each CTA: the MMAs are done with a stage
-  uint64_t rawfull[kRawStages];   // a k-block of q and scales landed
-  uint64_t rawempty[kRawStages];  // the converters have read it
   uint64_t tfull[2];         // each CTA: an accumulator holds a chunk
   uint64_t tempty[2];        // leader: both CTAs have drained an accumulator
   uint64_t drain;
-  int left[kRawStages];      // rows of the group in this k-block and after; -1: no more
   uint32_t tmem_base;
   int abort;
 };
 constexpr int kBarBytes = (static_cast<int>(sizeof(WgradBarriers)) + 127) / 128 * 128;
-constexpr int kSmem = 1024 + kStages * 2 * kShare + kRawStages * (kRaw + kRawScales) + kBarBytes + kSumWarps * kPatch;
+constexpr int kSmem = 1024 + kStages * 2 * kShare + kSumWarps * kPatch + kBarBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory of the weight-gradient kernel");
 
 // One tile of the work list: its place and its rows [lo, hi), split into k-blocks.
@@ -131,86 +127,6 @@ __device__ __forceinline__ WTile wtile(const WgradParams &p, int item) {
     if (t.hi < t.lo) t.hi = t.lo;
   }
   return t;
-}
-
-__device__ __forceinline__ void tma_bytes(void *dst, const void *map, int x, int y, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-// 4 bytes to shared memory, zeros when !inside.
-__device__ __forceinline__ void copy4(void *dst, const void *src, bool inside) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(inside ? 4 : 0) : "memory");
-}
-// One of the barrier's expected arrivals, made when this thread's copies so far have landed.
-__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void tma_box(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-// Arrive on a barrier of either CTA of the pair once this CTA's operands are
-// in place. What it orders lies in this CTA's own shared memory and has passed
-// the proxy fence, so the release is at CTA scope: at cluster scope it would
-// wait for every outstanding access of the warp, the loads ahead included.
-__device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-// 32 lanes x 16 columns of TMEM words, complete on return.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void fence_proxy_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Four int8 (bytes 0..3 of w) to two bf16 pairs, times a power of two. With l
-// the low 7 bits of a byte and s its sign bit, q = l - 128 s; the bf16 0x4300 |
-// l is 128 + l and 0xC300 | (s << 7) is -(128 + 128 s), so their sum is q,
-// exact in bf16 (as is the product: no bits are added, and units are at least
-// 2^-126). Even bytes make the first pair, odd ones the second, which
-// saves the byte shuffles: the second and third column of every four change
-// places in shared memory and in the accumulator, and the store puts them back
-// (true_column).
-__device__ __forceinline__ void widen4(uint32_t w, __nv_bfloat162 unit, uint32_t &even, uint32_t &odd) {
-  const uint32_t v = w >> 8;
-  const uint32_t a0 = (w & 0x007f007fu) | 0x43004300u, b0 = (w & 0x00800080u) | 0xC300C300u;
-  const uint32_t a1 = (v & 0x007f007fu) | 0x43004300u, b1 = (v & 0x00800080u) | 0xC300C300u;
-  auto two = [](const uint32_t &x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
-  const __nv_bfloat162 r0 = __hmul2(__hadd2(two(a0), two(b0)), unit);
-  const __nv_bfloat162 r1 = __hmul2(__hadd2(two(a1), two(b1)), unit);
-  even = *reinterpret_cast<const uint32_t *>(&r0);
-  odd = *reinterpret_cast<const uint32_t *>(&r1);
-}
-// accumulator column of matrix column c (and back)
-__device__ constexpr int true_column(int c) { return (c & 3) == 1 ? c + 1 : (c & 3) == 2 ? c - 1 : c; }
-// 2^(e - 133) twice as bf16 (e below 7 reads as 7; 255 as NaN)
-__device__ __forceinline__ __nv_bfloat162 unit_pair(uint32_t e) {
-  const uint32_t u = e == 255u ? 0x7fc0u : (max(e, 7u) - 6u) << 7;
-  const uint32_t v = u | (u << 16);
-  return *reinterpret_cast<const __nv_bfloat162 *>(&v);
-}
-
-// A wait of a whole warp that is over as a rule: every lane polls once, and
-// only if that fails lane 0 goes on polling for all.
-template <bool kCluster>
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Waiter &w) {
-  const bool ok = kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  return warp_mbar_wait<kCluster>(bar, parity, w);
 }
 
 // The k-blocks of a pair's whole work list in order: tile by tile, a tile's
@@ -255,6 +171,60 @@ struct BlockWalk {
   }
 };
 
+__device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+template <bool kAdd>
+__device__ __forceinline__ void tma_store_3d(const void *map, int x, int y, int z, const void *src) {
+  if (kAdd)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's bulk stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Arrive on a barrier of either CTA of the pair. What it orders are copies
+// that have landed and writes to this CTA's own shared memory that have
+// passed the proxy fence, so the release is at CTA scope.
+__device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// 32 lanes x 16 columns of TMEM words, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Bounded wait for an already issued copy or MMA after an abort.
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
@@ -262,32 +232,63 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
     if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
-// The sums of one thread (row r of the tile's half in this CTA, 128 columns
-// from c0) written through the warp's staging block, so that a store
-// instruction covers one row's 32 consecutive columns.
-__device__ __forceinline__ void store_tile(const WgradParams &p, const WTile &t, int row0, int col0, const float (&acc)[128],
-                                           float *patch) {
+// The sums of one thread (row row0 + lane, 128 columns from col0) by TMA: 32
+// rows x 128 bytes at a time through the warp's staging block, in the swizzled
+// layout of the map (16-byte pieces XOR the row modulo 8), which also spreads
+// a quarter-warp's 16-byte stores over all banks.
+template <bool kAdd, bool kHalf>
+__device__ __forceinline__ void store_tma(const WgradParams &p, int z, int row0, int col0, const float (&acc)[128],
+                                          uint8_t *patch) {
+  constexpr int kCols = kHalf ? 64 : 32;
   const int lane = threadIdx.x & 31;
-  const int64_t mat = static_cast<int64_t>(p.n_out) * p.n_in;
-  const bool part = p.splits > 1;
-  const int64_t base = (part ? static_cast<int64_t>(t.split) * p.groups * mat : 0) + t.e * mat;
-  const size_t count = static_cast<size_t>(p.groups) * mat;
+#pragma unroll
+  for (int h = 0; h < 128 / kCols; ++h) {
+    if (col0 + h * kCols >= p.n_in) break;
+    if (lane == 0) bulk_read_wait();
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (kHalf) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(acc[h * kCols + 8 * k + 2 * u], acc[h * kCols + 8 * k + 2 * u + 1]);
+          v[u] = *reinterpret_cast<const uint32_t *>(&b);
+        } else {
+          v[u] = __float_as_uint(acc[h * kCols + 4 * k + u]);
+        }
+      }
+      *reinterpret_cast<uint4 *>(patch + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) tma_store_3d<kAdd>(&p.tm_out, col0 + h * kCols, row0, z, patch);
+  }
+}
+
+// The same element by element (rows that TMA cannot address, bf16 sums that
+// are added to what is there): a store instruction covers one row's 32
+// consecutive columns.
+__device__ __forceinline__ void store_plain(const WgradParams &p, int e, int row0, int col0, const float (&acc)[128],
+                                            float *patch) {
+  const int lane = threadIdx.x & 31;
+  const int64_t base = static_cast<int64_t>(e) * p.n_out * p.n_in;
+  const size_t count = static_cast<size_t>(p.groups) * p.n_out * p.n_in;
   const int rows = min(32, p.n_out - row0);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     __syncwarp();
     // row lane, column c at word (c ^ lane): no bank conflict either way
 #pragma unroll
-    for (int c = 0; c < 32; ++c) patch[lane * 32 + (c ^ lane)] = acc[32 * k + true_column(c)];
+    for (int c = 0; c < 32; ++c) patch[lane * 32 + (c ^ lane)] = acc[32 * k + c];
     __syncwarp();
     const int col = col0 + 32 * k + lane;
     if (col >= p.n_in) continue;
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) {
       const float v = patch[r * 32 + (lane ^ r)];
       const int64_t at = base + static_cast<int64_t>(row0 + r) * p.n_in + col;
-      if (part) {
-        if (in_bounds(p.parts + at, 4, p.parts, count * p.splits * 4, p.status)) p.parts[at] = v;
-      } else if (p.gdtype == kF32) {
+      if (p.gdtype == kF32) {
         float *g = static_cast<float *>(p.grad) + at;
         if (in_bounds(g, 4, p.grad, count * 4, p.status)) *g = p.accumulate ? *g + v : v;
       } else {
@@ -303,10 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned, by an offset so that accesses stay in the shared window
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *sA = smem, *sB = smem + kStages * kShare;
-  uint8_t *sQ = smem + 2 * kStages * kShare, *sS = sQ + kRawStages * kRaw;
-  WgradBarriers *bar = reinterpret_cast<WgradBarriers *>(sS + kRawStages * kRawScales);
-  float *patches = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kBarBytes);
+  uint8_t *sA = smem, *sB = smem + kStages * kShare, *patches = sB + kStages * kShare;
+  WgradBarriers *bar = reinterpret_cast<WgradBarriers *>(patches + kSumWarps * kPatch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -314,13 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar->afull[s], 1);
-      mbar_init(&bar->ready[s], 2 * (kConvWarps + 1));
+      mbar_init(&bar->full[s], 1);
+      mbar_init(&bar->ready[s], 2);
       mbar_init(&bar->empty[s], 1);
-    }
-    for (int s = 0; s < kRawStages; ++s) {
-      mbar_init(&bar->rawfull[s], 1 + 32);
-      mbar_init(&bar->rawempty[s], kConvWarps);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bar->tfull[a], 1);
@@ -344,246 +339,149 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   volatile int *abort = &bar->abort;
   const Waiter w{abort, p.status, p.wait_limit_ns};
 
-  if (warp < kConv0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (tmem_ok && warp == 0) {
-      // -------------------------------------------------- dY by TMA
-      if (lane == 0) {
-        int stage = 0;
-        uint32_t parity = 0;
-        uint32_t issued = 0, last = 0;  // per stage: whether copies were issued, the parity of the last
-        BlockWalk k;
-        for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-          if (!mbar_wait<true, 40>(&bar->empty[stage], parity ^ 1u, w)) break;
-          mbar_arrive_expect_tx(&bar->afull[stage], kShare);
-          const int x = k.t.n0 + static_cast<int>(rank) * 128, y = k.t.lo + k.b * kBK;
-          tma_box(sA + stage * kShare, &p.tm_dy, x, y, k.z, &bar->afull[stage]);
-          tma_box(sA + stage * kShare + kBoxBytes, &p.tm_dy, x + 64, y, k.z, &bar->afull[stage]);
-          issued |= 1u << stage;
-          last = (last & ~(1u << stage)) | (parity << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1u;
-          }
-        }
-        if (*abort)
-          for (int s = 0; s < kStages; ++s)
-            if ((issued >> s) & 1u) drain_wait(&bar->afull[s], (last >> s) & 1u, w.limit_ns);
-      }
-    } else if (tmem_ok && warp == 2) {
-      // -------------------------------------------------- X as it is held
-      int raw = 0;
+  if (tmem_ok && warp == 0) {
+    // ---------------------------------------------------- operands by TMA, issued by one lane
+    if (lane == 0) {
+      int stage = 0;
       uint32_t parity = 0;
-      uint32_t issued = 0, last = 0;
-      int end = 0;  // end marks published, one for each converter group
+      uint32_t issued = 0, last = 0;  // per stage: whether copies were issued, the parity of the last
       BlockWalk k;
-      k.start(p, pair, npairs);
-      while (end < kConvGroups) {
-        if (!warp_mbar_wait<false, 40>(&bar->rawempty[raw], parity ^ 1u, w)) break;
-        if (k.done) {
-          if (lane == 0) {
-            bar->left[raw] = -1;
-            mbar_arrive(&bar->rawfull[raw]);
-          }
-          mbar_arrive(&bar->rawfull[raw]);
-          ++end;
-        } else {
-          const int col0 = k.t.k0 + static_cast<int>(rank) * 128, row0 = k.t.lo + k.b * kBK;
-          if (lane == 0) {
-            bar->left[raw] = k.t.hi - row0;
-            mbar_arrive_expect_tx(&bar->rawfull[raw], kRaw);
-            tma_bytes(sQ + raw * kRaw, &p.tm_q, col0, row0, &bar->rawfull[raw]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = row0 + h * 32 + lane;
-            const bool inside = row < k.t.hi && col0 / 32 < p.scale_pitch;
-            copy4(sS + raw * kRawScales + 4 * (h * 32 + lane),
-                  inside ? p.s + static_cast<int64_t>(row) * p.scale_pitch + col0 / 32 : p.s, inside);
-          }
-          arrive_after_copies(&bar->rawfull[raw]);
-          issued |= 1u << raw;
-          last = (last & ~(1u << raw)) | (parity << raw);
-          k.next(p, npairs);
-        }
-        if (++raw == kRawStages) {
-          raw = 0;
+      for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
+        if (!mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
+        mbar_arrive_expect_tx(&bar->full[stage], 2 * kShare);
+        const int x = static_cast<int>(rank) * 128, y = k.t.lo + k.b * kBK;
+        uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
+        tma_load_3d(a, &p.tm_dy, k.t.n0 + x, y, k.z, &bar->full[stage]);
+        tma_load_3d(a + kBoxBytes, &p.tm_dy, k.t.n0 + x + 64, y, k.z, &bar->full[stage]);
+        tma_load_2d(b, &p.tm_x, k.t.k0 + x, y, &bar->full[stage]);
+        tma_load_2d(b + kBoxBytes, &p.tm_x, k.t.k0 + x + 64, y, &bar->full[stage]);
+        issued |= 1u << stage;
+        last = (last & ~(1u << stage)) | (parity << stage);
+        if (++stage == kStages) {
+          stage = 0;
           parity ^= 1u;
         }
       }
       if (*abort)
-        for (int s = 0; s < kRawStages; ++s)
-          if ((issued >> s) & 1u) drain_wait(&bar->rawfull[s], (last >> s) & 1u, w.limit_ns);
-    } else if (tmem_ok && warp == 3) {
-      // -------------------------------------------------- dY landed
-      if (lane == 0) {
-        int stage = 0;
-        uint32_t parity = 0;
-        BlockWalk k;
-        for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-          if (!mbar_wait<true, 20>(&bar->afull[stage], parity, w)) break;
-          arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
-          if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1u;
-          }
-        }
-      }
-    } else if (tmem_ok && warp == 1 && leader) {
-      // -------------------------------------------------- MMAs, issued by one lane
-      if (lane == 0) {
-        constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
-        const uint64_t desc_a = sw128_mnmajor_desc(smem_u32(sA)), desc_b = sw128_mnmajor_desc(smem_u32(sB));
-        int stage = 0, acc = 0;
-        uint32_t parity = 0, acc_parity = 0;
-        bool ok = true;
-        for (int item = pair; ok && item < p.items; item += npairs) {
-          const int nb = wtile(p, item).blocks();
-          for (int c = 0; ok && c < nb; c += kChunk) {
-            if (!(ok = mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
-            tc_fence_after();
-            const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-            const int n = min(kChunk, nb - c) * p.slices;
-            for (int i = 0; i < n; ++i) {
-              if (!(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
-              tc_fence_after();
-              const uint64_t at = static_cast<uint64_t>(stage * (kShare >> 4));  // addresses are in 16-byte units
-#pragma unroll
-              for (int k = 0; k < kBK / 16; ++k)
-                umma_bf16_pair(d, desc_a + at + k * 128u, desc_b + at + k * 128u, idesc, i > 0 || k > 0);
-              umma_commit_pair_multicast(&bar->empty[stage], 3u);
-              if (++stage == kStages) {
-                stage = 0;
-                parity ^= 1u;
-              }
-            }
-            if (!ok) break;
-            umma_commit_pair_multicast(&bar->tfull[acc], 3u);
-            if (++acc == 2) {
-              acc = 0;
-              acc_parity ^= 1u;
-            }
-          }
-        }
-        umma_commit_pair_multicast(&bar->drain, 1u);
-        drain_wait(&bar->drain, 0, w.limit_ns);
-      }
+        for (int s = 0; s < kStages; ++s)
+          if ((issued >> s) & 1u) drain_wait(&bar->full[s], (last >> s) & 1u, w.limit_ns);
     }
-  } else if (warp < kSum0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (tmem_ok) {
-      // -------------------------------------------------- X to bf16
-      const int group = (warp - kConv0) / kConvWarps, part = (warp - kConv0) % kConvWarps;
-      const int j = lane & 7, row_in = part * 4 + (lane >> 3);
-      // 16 values are two 16-byte pieces of a 64-column box row. Half of the
-      // lanes take their second piece first: the 8 lanes that store one row
-      // then cover all banks, and so do the 16 that read two rows. The
-      // swizzle depends on the row modulo 8, the same for a lane's four rows.
-      const int swap = ((j >> 2) ^ row_in) & 1;
-      const int out0 = (j >> 2) * kBoxBytes + row_in * 128 + (((2 * (j & 3) + swap) ^ (row_in & 7)) << 4);
-      const int out1 = out0 ^ 16, in = row_in * 128 + j * 16 + 8 * swap, in_scale = 4 * row_in + (j >> 1);
-      int stage = group, raw = group;  // k-blocks group, group + kConvGroups, ...
-      uint32_t parity = 0, raw_parity = 0;
-      for (;;) {
-        if (!warp_wait<false>(&bar->rawfull[raw], raw_parity, w)) break;
-        const int left = bar->left[raw];
-        if (left < 0) break;
-        uint2 q0[4], q1[4];
-        uint32_t sc[4];
-        const uint8_t *src0 = sQ + raw * kRaw + in, *src1 = sQ + raw * kRaw + (in ^ 8);
-        const uint8_t *scales = sS + raw * kRawScales + in_scale;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q0[i] = *reinterpret_cast<const uint2 *>(src0 + i * 2048);
-          q1[i] = *reinterpret_cast<const uint2 *>(src1 + i * 2048);
-          sc[i] = scales[i * 64];
-        }
-        if (left < kBK) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i * 16 + row_in >= left) q0[i] = q1[i] = make_uint2(0, 0);  // and its scale is 0: the value is 0
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->rawempty[raw]);
-        if ((raw += kConvGroups) >= kRawStages) {
-          raw -= kRawStages;
-          raw_parity ^= 1u;
-        }
-        if (!warp_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
-        uint8_t *dst0 = sB + stage * kShare + out0, *dst1 = sB + stage * kShare + out1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 unit = unit_pair(sc[i]);
-          uint4 a;
-          widen4(q0[i].x, unit, a.x, a.y);
-          widen4(q0[i].y, unit, a.z, a.w);
-          *reinterpret_cast<uint4 *>(dst0 + i * 2048) = a;
-          widen4(q1[i].x, unit, a.x, a.y);
-          widen4(q1[i].y, unit, a.z, a.w);
-          *reinterpret_cast<uint4 *>(dst1 + i * 2048) = a;
-        }
-        if (left < kBK) {  // clear dY beyond the group's end: 64 rows of 8 pieces in each box
-          if (!warp_mbar_wait<true>(&bar->afull[stage], parity, w)) break;
-          for (int i = part * 32 + lane; i < 2 * kBK * 8; i += 32 * kConvWarps) {
-            const int r = (i >> 3) & (kBK - 1);
-            if (r >= left)
-              *reinterpret_cast<uint4 *>(sA + stage * kShare + (i >> 9) * kBoxBytes + r * 128 + (i & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
-        if ((stage += kConvGroups) >= kStages) {
-          stage -= kStages;
-          parity ^= 1u;
-        }
-      }
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    if (tmem_ok) {
-      // -------------------------------------------------- sums and the tile's store
-      const int e = warp - kSum0, quarter = warp & 3, half = e >> 2;
-      float *patch = patches + e * (kPatch / 4);
-      int acc = 0;
-      uint32_t acc_parity = 0;
+  } else if (tmem_ok && warp == 1 && leader) {
+    // ---------------------------------------------------- MMAs, issued by one lane
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
+      const uint64_t desc_a = sw128_mnmajor_desc(smem_u32(sA)), desc_b = sw128_mnmajor_desc(smem_u32(sB));
+      int stage = 0, acc = 0;
+      uint32_t parity = 0, acc_parity = 0;
       bool ok = true;
       for (int item = pair; ok && item < p.items; item += npairs) {
-        const WTile t = wtile(p, item);
-        const int nb = t.blocks();
-        if (nb == 0 && p.accumulate && p.splits == 1) continue;
-        float sum[128];
-#pragma unroll
-        for (int c = 0; c < 128; ++c) sum[c] = 0.f;
-        for (int c = 0; c < nb; c += kChunk) {
-          if (!warp_mbar_wait<true, 100>(&bar->tfull[acc], acc_parity, w)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
+        const int nb = wtile(p, item).blocks();
+        for (int c = 0; ok && c < nb; c += kChunk) {
+          if (!(ok = mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
           tc_fence_after();
-          const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+          const int n = min(kChunk, nb - c) * p.slices;
+          for (int i = 0; i < n; ++i) {
+            if (!(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
+            tc_fence_after();
+            const uint64_t at = static_cast<uint64_t>(stage * (kShare >> 4));  // addresses are in 16-byte units
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t v[16];
-            tmem_ld16(src + 16 * k, v);
-#pragma unroll
-            for (int u = 0; u < 16; ++u) sum[16 * k + u] += __uint_as_float(v[u]);
+            for (int k = 0; k < kBK / 16; ++k)
+              umma_bf16_pair(d, desc_a + at + k * 128u, desc_b + at + k * 128u, idesc, i > 0 || k > 0);
+            umma_commit_pair_multicast(&bar->empty[stage], 3u);
+            if (++stage == kStages) {
+              stage = 0;
+              parity ^= 1u;
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->tempty[acc]), 0));
+          if (!ok) break;
+          umma_commit_pair_multicast(&bar->tfull[acc], 3u);
           if (++acc == 2) {
             acc = 0;
             acc_parity ^= 1u;
           }
         }
-        if (!ok) break;
-        const int row0 = t.n0 + static_cast<int>(rank) * 128 + quarter * 32;
-        if (row0 < p.n_out) store_tile(p, t, row0, t.k0 + half * 128, sum, patch);
+      }
+      umma_commit_pair_multicast(&bar->drain, 1u);
+      drain_wait(&bar->drain, 0, w.limit_ns);
+    }
+  } else if (tmem_ok && warp == 2) {
+    // ---------------------------------------------------- landed stages
+    int stage = 0;
+    uint32_t parity = 0;
+    BlockWalk k;
+    for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
+      if (!warp_mbar_wait<true>(&bar->full[stage], parity, w)) break;
+      const int left = k.t.hi - k.t.lo - k.b * kBK;
+      if (left < kBK) {  // rows left.. of both boxes of both operands, 8 pieces of 16 bytes each
+        uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
+        for (int i = left * 8 + lane; i < kBK * 8; i += 32) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(a + i * 16) = zero;
+          *reinterpret_cast<uint4 *>(a + kBoxBytes + i * 16) = zero;
+          *reinterpret_cast<uint4 *>(b + i * 16) = zero;
+          *reinterpret_cast<uint4 *>(b + kBoxBytes + i * 16) = zero;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
+      if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1u;
       }
     }
+  } else if (tmem_ok && warp >= kSum0) {
+    // ---------------------------------------------------- sums and the tile's store
+    const int e = warp - kSum0, quarter = warp & 3, half = e >> 2;
+    uint8_t *patch = patches + e * kPatch;
+    int acc = 0;
+    uint32_t acc_parity = 0;
+    bool ok = true;
+    for (int item = pair; ok && item < p.items; item += npairs) {
+      const WTile t = wtile(p, item);
+      const int nb = t.blocks();
+      if (nb == 0 && p.accumulate && p.splits == 1) continue;
+      float sum[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+      for (int c = 0; c < nb; c += kChunk) {
+        if (!warp_mbar_wait<true>(&bar->tfull[acc], acc_parity, w)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t v[16];
+          tmem_ld16(src + 16 * k, v);
+#pragma unroll
+          for (int u = 0; u < 16; ++u) sum[16 * k + u] += __uint_as_float(v[u]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->tempty[acc]), 0));
+        if (++acc == 2) {
+          acc = 0;
+          acc_parity ^= 1u;
+        }
+      }
+      if (!ok) break;
+      const int row0 = t.n0 + static_cast<int>(rank) * 128 + quarter * 32, col0 = t.k0 + half * 128;
+      if (row0 >= p.n_out) continue;
+      const int z = t.split * p.groups + t.e;
+      if (p.store == kStorePlain)
+        store_plain(p, t.e, row0, col0, sum, reinterpret_cast<float *>(patch));
+      else if (p.splits > 1 || (p.gdtype == kF32 && p.store == kStoreTma))
+        store_tma<false, false>(p, z, row0, col0, sum, patch);
+      else if (p.store == kStoreTmaAdd)
+        store_tma<true, false>(p, z, row0, col0, sum, patch);
+      else
+        store_tma<false, true>(p, z, row0, col0, sum, patch);
+    }
+    if (lane == 0) bulk_wait();
   }
   __syncwarp();
   tc_fence_before();
@@ -594,32 +492,58 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ around the product
-struct SliceParams {
-  const void *dy;
-  __nv_bfloat16 *out;  // slices x rows x pitch
+struct PrepareParams {
+  const int8_t *q;
+  const uint8_t *s;
+  __nv_bfloat16 *x;    // rows x pitch
+  const void *dy;      // nullptr: the product reads dY itself
+  __nv_bfloat16 *out;  // slices x rows x out_pitch
   int64_t ld;
-  int rows, n_out, pitch, slices;
+  int rows, n_in, pitch, scale_pitch, n_out, out_pitch, slices;
   int *status;
 };
 
-// dY as TMA can address it: bf16 rows of `pitch` elements (a multiple of 8),
-// one slice, or three whose sum is the fp32 value to 2^-24 of it.
+// X widened to bf16 (16 values per thread: its pitch is a multiple of 16),
+// and dY as TMA can address it: bf16 rows of out_pitch elements (a multiple of
+// 8, 8 per thread), one slice, or three whose sum is the fp32 value to 2^-24 of it.
 template <int DT>
-__global__ void __launch_bounds__(256) ns_wgrad_slice_kernel(const __grid_constant__ SliceParams p) {
+__global__ void __launch_bounds__(256) ns_wgrad_prepare_kernel(const __grid_constant__ PrepareParams p) {
   using E = typename Elem<DT>::T;
-  const int64_t slice = static_cast<int64_t>(p.rows) * p.pitch;
-  const size_t size = static_cast<size_t>(slice) * p.slices * 2;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < slice; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / p.pitch;
-    const int c = static_cast<int>(i - r * p.pitch);
-    float v = c < p.n_out ? Elem<DT>::to_f(static_cast<const E *>(p.dy)[r * p.ld + c]) : 0.f;
-    for (int z = 0; z < p.slices; ++z) {
-      __nv_bfloat16 h = __float2bfloat16_rn(v);
-      if (__hisinf(h) && !isinf(v))  // beyond bf16's largest value: that one, the rest in the next slice
-        h = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(v) >> 16));
-      if (in_bounds(p.out + z * slice + i, 2, p.out, size, p.status)) p.out[z * slice + i] = h;
-      const float f = __bfloat162float(h);
-      v = isinf(f) || isnan(f) ? 0.f : v - f;  // an infinity or NaN stays in the first slice alone
+  const int64_t per_row = p.pitch / 16, nx = p.rows * per_row;
+  const int64_t dy_row = p.out_pitch / 8, ny = p.dy ? p.rows * dy_row : 0;
+  const int64_t slice = static_cast<int64_t>(p.rows) * p.out_pitch;
+  const size_t xsize = static_cast<size_t>(p.rows) * p.pitch * 2, ysize = static_cast<size_t>(slice) * p.slices * 2;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < nx + ny; i += static_cast<int64_t>(gridDim.x) * 256) {
+    if (i < nx) {
+      const int64_t r = i / per_row;
+      const int c = static_cast<int>(i - r * per_row) * 16;
+      const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.q + r * p.pitch + c));
+      const int e = p.s[r * p.scale_pitch + c / 32];
+      const float unit = e == 255 ? __int_as_float(0x7fc00000) : __int_as_float((max(e, 7) - 6) << 23);
+      const int8_t *q = reinterpret_cast<const int8_t *>(&w);
+      Pack<kBF16, 16> v;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v.set(u, static_cast<float>(q[u]) * unit);
+      v.store(p.x + r * p.pitch + c, p.x, xsize, p.status);
+    } else {
+      const int64_t k = i - nx, r = k / dy_row;
+      const int c = static_cast<int>(k - r * dy_row) * 8;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = c + u < p.n_out ? Elem<DT>::to_f(static_cast<const E *>(p.dy)[r * p.ld + c + u]) : 0.f;
+      for (int z = 0; z < p.slices; ++z) {
+        Pack<kBF16, 8> h;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          __nv_bfloat16 b = __float2bfloat16_rn(v[u]);
+          if (__hisinf(b) && !isinf(v[u]))  // beyond bf16's largest value: that one, the rest in the next slice
+            b = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(v[u]) >> 16));
+          const float f = __bfloat162float(b);
+          h.set(u, f);
+          v[u] = isinf(f) || isnan(f) ? 0.f : v[u] - f;  // an infinity or NaN stays in the first slice alone
+        }
+        h.store(p.out + z * slice + r * p.out_pitch + c, p.out, ysize, p.status);
+      }
     }
   }
 }
@@ -628,23 +552,24 @@ __global__ void __launch_bounds__(256) ns_wgrad_slice_kernel(const __grid_consta
 template <int GT>
 __global__ void __launch_bounds__(256) ns_wgrad_join_kernel(const __grid_constant__ WgradParams p) {
   using G = typename Elem<GT>::T;
-  const int64_t n = static_cast<int64_t>(p.groups) * p.n_out * p.n_in;
+  const int64_t mats = static_cast<int64_t>(p.groups) * p.n_out, n = mats * p.n_in, part = mats * p.part_pitch;
   G *g = static_cast<G *>(p.grad);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    float v = p.parts[i];
-    for (int s = 1; s < p.splits; ++s) v += p.parts[s * n + i];
+    const int64_t r = i / p.n_in, at = r * p.part_pitch + (i - r * p.n_in);
+    float v = p.parts[at];
+    for (int s = 1; s < p.splits; ++s) v += p.parts[s * part + at];
     if (p.accumulate) v += Elem<GT>::to_f(g[i]);
     if (in_bounds(g + i, sizeof(G), g, static_cast<size_t>(n) * sizeof(G), p.status)) g[i] = Elem<GT>::from_f(v);
   }
 }
 
-int run_slice(const SliceParams &p, int dtype, int sms, cudaStream_t s) {
-  const int64_t n = static_cast<int64_t>(p.rows) * p.pitch;
+int run_prepare(const PrepareParams &p, int dtype, int sms, cudaStream_t s) {
+  const int64_t n = static_cast<int64_t>(p.rows) * (p.pitch / 16 + (p.dy ? p.out_pitch / 8 : 0));
   const int grid = static_cast<int>(std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(sms) * 16));
   if (dtype == NS_BF16)
-    ns_wgrad_slice_kernel<kBF16><<<grid, 256, 0, s>>>(p);
+    ns_wgrad_prepare_kernel<kBF16><<<grid, 256, 0, s>>>(p);
   else
-    ns_wgrad_slice_kernel<kF32><<<grid, 256, 0, s>>>(p);
+    ns_wgrad_prepare_kernel<kF32><<<grid, 256, 0, s>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -700,16 +625,15 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
     return NS_EALIGN;
   WgradParams p{};
   const int64_t q_pitch = ns_ckpt_pitch(n_in);
-  p.scale_pitch = static_cast<int>(ns_ckpt_scale_pitch(n_in));
+  const int64_t scale_pitch = ns_ckpt_scale_pitch(n_in);
   const Range rg(grad, static_cast<int64_t>(groups) * n_out, n_in, n_in, gelt);
   if (rg.overlaps(Range(dy, rows, n_out, ld_dy, elt)) || rg.overlaps(Range(q, rows, q_pitch, q_pitch, 1)) ||
-      rg.overlaps(Range(scales, rows, p.scale_pitch, p.scale_pitch, 1)) ||
+      rg.overlaps(Range(scales, rows, scale_pitch, scale_pitch, 1)) ||
       rg.overlaps(Range(offsets, 1, groups + int64_t(1), groups + int64_t(1), 4)))
     return NS_EINVAL;
   OpCall call(stream);
   if (call.rc) return call.rc;
   WgradParams &k = p;
-  k.s = static_cast<const uint8_t *>(scales);
   k.offsets = offsets;
   k.grad = grad;
   k.rows = static_cast<int>(rows);
@@ -747,30 +671,47 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
   }
   if (tiles * k.splits > INT32_MAX) return NS_EINVAL;
   k.items = static_cast<int>(tiles * k.splits);
+  k.part_pitch = static_cast<int>((n_in + 3) / 4 * 4);
+  // TMA writes what it can address; it adds in fp32 only (bf16 would round the
+  // sum before adding it). Debug builds store where every store is checked.
+  const bool out_rows = !misaligned(grad, 16) && n_in * gelt % 16 == 0;
+  k.store = k.splits > 1                         ? kStoreTma
+            : kDebugBounds || !out_rows          ? kStorePlain
+            : !accumulate                        ? kStoreTma
+            : grad_dtype == NS_F32               ? kStoreTmaAdd
+                                                 : kStorePlain;
 
-  // scratch: dY's slices (fp32, or bf16 that TMA cannot address), the parts of a split
-  const bool direct = dtype == NS_BF16 && rows > 0 && !misaligned(dy, 16) && ld_dy % 8 == 0;
+  // scratch: X in bf16, dY's slices (fp32, or bf16 that TMA cannot address), the parts of a split
+  const bool direct = dtype == NS_BF16 && !misaligned(dy, 16) && ld_dy % 8 == 0;
   const int64_t pitch = (n_out + 7) / 8 * 8;
-  const size_t slice_bytes = direct ? 0 : (static_cast<size_t>(k.slices) * rows * pitch * 2 + 1023) / 1024 * 1024;
-  const size_t part_bytes = k.splits > 1 ? static_cast<size_t>(k.splits) * groups * n_out * n_in * 4 : 0;
+  auto up = [](size_t v) { return (v + 1023) / 1024 * 1024; };
+  const size_t x_bytes = up(static_cast<size_t>(rows) * q_pitch * 2);
+  const size_t dy_bytes = direct ? 0 : up(static_cast<size_t>(k.slices) * rows * pitch * 2);
+  const size_t part_bytes = k.splits > 1 ? static_cast<size_t>(k.splits) * groups * n_out * k.part_pitch * 4 : 0;
   uint8_t *ws = nullptr;
-  int rc = NS_OK;
-  if (slice_bytes + part_bytes && (rc = call.workspace(kSlotWgrad, slice_bytes + part_bytes, &ws))) return rc;
-  k.parts = reinterpret_cast<float *>(ws + slice_bytes);
-  const int64_t use = direct ? ld_dy : pitch;
-  const int64_t dims[3] = {n_out, rows, k.slices}, strides[2] = {use * 2, use * 2 * std::max<int64_t>(rows, 1)};
-  const int box[3] = {64, kBK, 1};
-  // a map wants an address even when no row will be read through it
-  const void *src = direct ? dy : slice_bytes ? ws : grad;
+  int rc = call.workspace(kSlotWgrad, x_bytes + dy_bytes + part_bytes, &ws);
+  if (rc) return rc;
+  k.parts = reinterpret_cast<float *>(ws + x_bytes + dy_bytes);
   if (rows > 0) {
-    if ((rc = call.tensor_map(&k.tm_dy, 2, src, 3, dims, strides, box))) return rc;
-    const int64_t qdims[2] = {n_in, rows}, qstride[1] = {q_pitch};
-    const int qbox[2] = {128, kBK};
-    if ((rc = call.tensor_map(&k.tm_q, 1, q, 2, qdims, qstride, qbox))) return rc;
+    const int64_t use = direct ? ld_dy : pitch;
+    const int64_t dims[3] = {n_out, rows, k.slices}, strides[2] = {use * 2, use * 2 * rows};
+    const int box[3] = {64, kBK, 1};
+    if ((rc = call.tensor_map(&k.tm_dy, 2, direct ? dy : ws + x_bytes, 3, dims, strides, box))) return rc;
+    const int64_t xdims[2] = {n_in, rows}, xstride[1] = {q_pitch * 2};
+    if ((rc = call.tensor_map(&k.tm_x, 2, ws, 2, xdims, xstride, box))) return rc;
+    PrepareParams pp{static_cast<const int8_t *>(q), static_cast<const uint8_t *>(scales),
+                     reinterpret_cast<__nv_bfloat16 *>(ws), direct ? nullptr : dy,
+                     reinterpret_cast<__nv_bfloat16 *>(ws + x_bytes), ld_dy, k.rows, k.n_in, static_cast<int>(q_pitch),
+                     static_cast<int>(scale_pitch), k.n_out, static_cast<int>(pitch), k.slices, k.status};
+    if ((rc = call.launch(kOpWgrad, [&] { return run_prepare(pp, dtype, call.sms, call.s); }))) return rc;
   }
-  if (!direct && rows > 0) {
-    SliceParams sp{dy, reinterpret_cast<__nv_bfloat16 *>(ws), ld_dy, k.rows, k.n_out, static_cast<int>(pitch), k.slices, k.status};
-    if ((rc = call.launch(kOpWgrad, [&] { return run_slice(sp, dtype, call.sms, call.s); }))) return rc;
+  if (k.store != kStorePlain) {
+    const bool f32 = k.splits > 1 || grad_dtype == NS_F32;
+    const int64_t row_bytes = k.splits > 1 ? k.part_pitch * 4ll : n_in * gelt;
+    const int64_t dims[3] = {n_in, n_out, static_cast<int64_t>(groups) * k.splits}, strides[2] = {row_bytes, row_bytes * n_out};
+    const int box[3] = {f32 ? 32 : 64, 32, 1};
+    if ((rc = call.tensor_map(&k.tm_out, f32 ? 4 : 2, k.splits > 1 ? static_cast<void *>(k.parts) : grad, 3, dims, strides, box)))
+      return rc;
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(pairs, k.items)), 1, 1);
   rc = call.launch(kOpWgrad, [&] {
