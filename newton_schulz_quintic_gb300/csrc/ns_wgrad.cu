@@ -23,6 +23,8 @@
 //   2       passes a landed stage on to the MMAs. Where a group ends inside the
 //           stage it first clears the rows beyond, in both operands, so that
 //           nothing of the next group (infinities, NaN) takes part.
+//   3       looks the pair's tiles up (place, group, rows) a few ahead and
+//           hands them to the other warps through a small queue
 //   4..11   sums: every kChunk k-blocks the accumulator is added to fp32
 //           registers (128 columns x 1 row per thread) while the MMAs go on in
 //           the other one; the tile is written at its end. The tensor cores'
@@ -79,7 +81,21 @@ struct WgradParams {
   uint64_t wait_limit_ns;
 };
 
+// One tile of the pair's list as warp 3 hands it out.
+struct alignas(16) WTile {
+  int n0, k0;  // its first row and column in G
+  int e, z;    // its group; its matrix in the output map
+  int lo, hi;  // its rows of dY and X; lo < 0: no more tiles
+  int pad[2];
+  __device__ __forceinline__ int blocks() const { return (hi - lo + kBK - 1) / kBK; }
+};
+constexpr int kQueue = 4;
+
 struct WgradBarriers {
+  WTile queue[kQueue];
+  uint64_t qfull[kQueue];    // a slot holds the next tile
+  uint64_t qempty[kQueue];   // every consumer of this CTA has read it
+
   uint64_t full[kStages];    // this CTA's boxes of a stage landed
   uint64_t ready[kStages];   // leader: both CTAs' operands of a stage are in place
   uint64_t empty[kStages];   // each CTA: the MMAs are done with a stage
@@ -93,21 +109,14 @@ constexpr int kBarBytes = (static_cast<int>(sizeof(WgradBarriers)) + 127) / 128 
 constexpr int kSmem = 1024 + kStages * 2 * kShare + kSumWarps * kPatch + kBarBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory of the weight-gradient kernel");
 
-// One tile of the work list: its place and its rows [lo, hi), split into k-blocks.
-struct WTile {
-  int e, n0, k0, split;
-  int lo, hi;
-  __device__ __forceinline__ int blocks() const { return (hi - lo + kBK - 1) / kBK; }
-};
-
-// Tiles in groups of 8 along n_out, column by column within a group, so the
+// Tiles go in groups of 8 along n_out, column by column within a group, so the
 // tiles in flight share a few panels of each operand.
-__device__ __forceinline__ WTile wtile(const WgradParams &p, int item) {
+__device__ __forceinline__ WTile look_up(const WgradParams &p, int item) {
   WTile t;
   const int per = p.tn * p.tk;
-  t.split = item % p.splits;
-  const int g = item / p.splits;
+  const int split = item % p.splits, g = item / p.splits;
   t.e = g / per;
+  t.z = split * p.groups + t.e;
   const int tile = g - t.e * per;
   const int band = tile / (8 * p.tk), first = band * 8;
   const int height = min(8, p.tn - first), in = tile - band * 8 * p.tk;
@@ -121,55 +130,53 @@ __device__ __forceinline__ WTile wtile(const WgradParams &p, int item) {
   }
   if (p.splits > 1) {  // whole k-blocks per part
     const int64_t nb = t.blocks();
-    const int a = static_cast<int>(nb * t.split / p.splits), b = static_cast<int>(nb * (t.split + 1) / p.splits);
+    const int a = static_cast<int>(nb * split / p.splits), b = static_cast<int>(nb * (split + 1) / p.splits);
     t.hi = min(t.hi, t.lo + b * kBK);
-    t.lo += a * kBK;
-    if (t.hi < t.lo) t.hi = t.lo;
+    t.lo = min(t.lo + a * kBK, t.hi);
   }
   return t;
 }
 
-// The k-blocks of a pair's whole work list in order: tile by tile, a tile's
-// chunks of kChunk blocks, in each the slices of dY from smallest to largest,
-// in each slice the chunk's blocks.
-struct BlockWalk {
-  WTile t;
-  int item, c, z, b;  // current block: chunk start, slice, block
-  bool done;
-  __device__ __forceinline__ void open(const WgradParams &p, int npairs) {
-    for (; item < p.items; item += npairs) {
-      t = wtile(p, item);
-      if (t.blocks() > 0) {
-        c = 0;
-        b = 0;
-        z = p.slices - 1;
-        return;
-      }
+// A consumer's place in the queue. One lane takes a tile with take(); a warp
+// with take_warp(). False: no more tiles, or a wait gave up.
+struct TileReader {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kQueue) {
+      slot = 0;
+      parity ^= 1u;
     }
-    done = true;
   }
-  __device__ __forceinline__ void start(const WgradParams &p, int pair, int npairs) {
-    item = pair;
-    done = false;
-    open(p, npairs);
+  __device__ __forceinline__ bool take(WgradBarriers *bar, WTile &t, const Waiter &w) {
+    if (!mbar_wait(&bar->qfull[slot], parity, w)) return false;
+    t = bar->queue[slot];
+    mbar_arrive(&bar->qempty[slot]);
+    step();
+    return t.lo >= 0;
   }
-  __device__ __forceinline__ void next(const WgradParams &p, int npairs) {
-    const int nb = t.blocks();
-    if (++b < min(c + kChunk, nb)) return;
-    if (--z >= 0) {
-      b = c;
-      return;
-    }
-    c += kChunk;
-    if (c < nb) {
-      b = c;
-      z = p.slices - 1;
-      return;
-    }
-    item += npairs;
-    open(p, npairs);
+  __device__ __forceinline__ bool take_warp(WgradBarriers *bar, WTile &t, const Waiter &w) {
+    if (!warp_mbar_wait<false>(&bar->qfull[slot], parity, w)) return false;
+    __syncwarp();
+    t = bar->queue[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->qempty[slot]);
+    step();
+    return t.lo >= 0;
   }
 };
+
+// The k-blocks of a tile in order: chunks of kChunk blocks, in each the
+// slices of dY from smallest to largest, in each slice the chunk's blocks.
+template <typename F>
+__device__ __forceinline__ bool for_blocks(const WTile &t, int slices, F &&f) {
+  const int nb = t.blocks();
+  for (int c = 0; c < nb; c += kChunk)
+    for (int z = slices - 1; z >= 0; --z)
+      for (int b = c; b < min(c + kChunk, nb); ++b)
+        if (!f(b, z)) return false;
+  return true;
+}
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int x, int y, uint64_t *bar) {
   asm volatile(
@@ -321,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       mbar_init(&bar->tfull[a], 1);
       mbar_init(&bar->tempty[a], 2 * kSumWarps);
     }
+    for (int q = 0; q < kQueue; ++q) {
+      mbar_init(&bar->qfull[q], 1);
+      mbar_init(&bar->qempty[q], 2 + kSumWarps + (leader ? 1 : 0));
+    }
     mbar_init(&bar->drain, 1);
     bar->abort = 0;
     fence_mbar_init();
@@ -345,22 +356,28 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       int stage = 0;
       uint32_t parity = 0;
       uint32_t issued = 0, last = 0;  // per stage: whether copies were issued, the parity of the last
-      BlockWalk k;
-      for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-        if (!mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) break;
-        mbar_arrive_expect_tx(&bar->full[stage], 2 * kShare);
-        const int x = static_cast<int>(rank) * 128, y = k.t.lo + k.b * kBK;
-        uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
-        tma_load_3d(a, &p.tm_dy, k.t.n0 + x, y, k.z, &bar->full[stage]);
-        tma_load_3d(a + kBoxBytes, &p.tm_dy, k.t.n0 + x + 64, y, k.z, &bar->full[stage]);
-        tma_load_2d(b, &p.tm_x, k.t.k0 + x, y, &bar->full[stage]);
-        tma_load_2d(b + kBoxBytes, &p.tm_x, k.t.k0 + x + 64, y, &bar->full[stage]);
-        issued |= 1u << stage;
-        last = (last & ~(1u << stage)) | (parity << stage);
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1u;
-        }
+      const int x = static_cast<int>(rank) * 128;
+      TileReader tiles;
+      WTile t;
+      while (tiles.take(bar, t, w)) {
+        const bool ok = for_blocks(t, p.slices, [&](int block, int z) {
+          if (!mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) return false;
+          mbar_arrive_expect_tx(&bar->full[stage], 2 * kShare);
+          const int y = t.lo + block * kBK;
+          uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
+          tma_load_3d(a, &p.tm_dy, t.n0 + x, y, z, &bar->full[stage]);
+          tma_load_3d(a + kBoxBytes, &p.tm_dy, t.n0 + x + 64, y, z, &bar->full[stage]);
+          tma_load_2d(b, &p.tm_x, t.k0 + x, y, &bar->full[stage]);
+          tma_load_2d(b + kBoxBytes, &p.tm_x, t.k0 + x + 64, y, &bar->full[stage]);
+          issued |= 1u << stage;
+          last = (last & ~(1u << stage)) | (parity << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1u;
+          }
+          return true;
+        });
+        if (!ok) break;
       }
       if (*abort)
         for (int s = 0; s < kStages; ++s)
@@ -373,26 +390,31 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       const uint64_t desc_a = sw128_mnmajor_desc(smem_u32(sA)), desc_b = sw128_mnmajor_desc(smem_u32(sB));
       int stage = 0, acc = 0;
       uint32_t parity = 0, acc_parity = 0;
-      bool ok = true;
-      for (int item = pair; ok && item < p.items; item += npairs) {
-        const int nb = wtile(p, item).blocks();
+      bool ok = true, seen = false;  // seen: the next stage is known to be ready
+      TileReader tiles;
+      WTile t;
+      while (ok && tiles.take(bar, t, w)) {
+        const int nb = t.blocks();
         for (int c = 0; ok && c < nb; c += kChunk) {
           if (!(ok = mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
-          tc_fence_after();
           const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
           const int n = min(kChunk, nb - c) * p.slices;
           for (int i = 0; i < n; ++i) {
-            if (!(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
+            if (!seen && !(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
             tc_fence_after();
             const uint64_t at = static_cast<uint64_t>(stage * (kShare >> 4));  // addresses are in 16-byte units
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              umma_bf16_pair(d, desc_a + at + k * 128u, desc_b + at + k * 128u, idesc, i > 0 || k > 0);
-            umma_commit_pair_multicast(&bar->empty[stage], 3u);
+            uint64_t *const empty = &bar->empty[stage];
             if (++stage == kStages) {
               stage = 0;
               parity ^= 1u;
             }
+            umma_bf16_pair(d, desc_a + at, desc_b + at, idesc, i > 0);
+            umma_bf16_pair(d, desc_a + at + 128u, desc_b + at + 128u, idesc, 1);
+            // look at the next stage while these run, so that its first MMA follows the last one here at once
+            seen = mbar_try_wait_cluster(&bar->ready[stage], parity);
+            umma_bf16_pair(d, desc_a + at + 256u, desc_b + at + 256u, idesc, 1);
+            umma_bf16_pair(d, desc_a + at + 384u, desc_b + at + 384u, idesc, 1);
+            umma_commit_pair_multicast(empty, 3u);
           }
           if (!ok) break;
           umma_commit_pair_multicast(&bar->tfull[acc], 3u);
@@ -409,26 +431,53 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
     // ---------------------------------------------------- landed stages
     int stage = 0;
     uint32_t parity = 0;
-    BlockWalk k;
-    for (k.start(p, pair, npairs); !k.done; k.next(p, npairs)) {
-      if (!warp_mbar_wait<true>(&bar->full[stage], parity, w)) break;
-      const int left = k.t.hi - k.t.lo - k.b * kBK;
-      if (left < kBK) {  // rows left.. of both boxes of both operands, 8 pieces of 16 bytes each
-        uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
-        for (int i = left * 8 + lane; i < kBK * 8; i += 32) {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(a + i * 16) = zero;
-          *reinterpret_cast<uint4 *>(a + kBoxBytes + i * 16) = zero;
-          *reinterpret_cast<uint4 *>(b + i * 16) = zero;
-          *reinterpret_cast<uint4 *>(b + kBoxBytes + i * 16) = zero;
+    TileReader tiles;
+    WTile t;
+    while (tiles.take_warp(bar, t, w)) {
+      const bool ok = for_blocks(t, p.slices, [&](int block, int) {
+        if (!warp_mbar_wait<true>(&bar->full[stage], parity, w)) return false;
+        const int left = t.hi - t.lo - block * kBK;
+        if (left < kBK) {  // rows left.. of both boxes of both operands, 8 pieces of 16 bytes each
+          uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
+          for (int i = left * 8 + lane; i < kBK * 8; i += 32) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(a + i * 16) = zero;
+            *reinterpret_cast<uint4 *>(a + kBoxBytes + i * 16) = zero;
+            *reinterpret_cast<uint4 *>(b + i * 16) = zero;
+            *reinterpret_cast<uint4 *>(b + kBoxBytes + i * 16) = zero;
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-      }
-      if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
-      if (++stage == kStages) {
-        stage = 0;
-        parity ^= 1u;
+        if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
+        }
+        return true;
+      });
+      if (!ok) break;
+    }
+  } else if (tmem_ok && warp == 3) {
+    // ---------------------------------------------------- the pair's tiles, looked up ahead
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t parity = 0;
+      bool more = true;
+      for (int item = pair; more; item += npairs) {
+        WTile t;
+        more = item < p.items;
+        if (more)
+          t = look_up(p, item);
+        else
+          t.lo = -1;
+        if (!mbar_wait(&bar->qempty[slot], parity ^ 1u, w)) break;
+        bar->queue[slot] = t;
+        mbar_arrive(&bar->qfull[slot]);
+        if (++slot == kQueue) {
+          slot = 0;
+          parity ^= 1u;
+        }
       }
     }
   } else if (tmem_ok && warp >= kSum0) {
@@ -438,8 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
     int acc = 0;
     uint32_t acc_parity = 0;
     bool ok = true;
-    for (int item = pair; ok && item < p.items; item += npairs) {
-      const WTile t = wtile(p, item);
+    TileReader tiles;
+    WTile t;
+    while (ok && tiles.take_warp(bar, t, w)) {
       const int nb = t.blocks();
       if (nb == 0 && p.accumulate && p.splits == 1) continue;
       float sum[128];
@@ -471,15 +521,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       if (!ok) break;
       const int row0 = t.n0 + static_cast<int>(rank) * 128 + quarter * 32, col0 = t.k0 + half * 128;
       if (row0 >= p.n_out) continue;
-      const int z = t.split * p.groups + t.e;
       if (p.store == kStorePlain)
         store_plain(p, t.e, row0, col0, sum, reinterpret_cast<float *>(patch));
       else if (p.splits > 1 || (p.gdtype == kF32 && p.store == kStoreTma))
-        store_tma<false, false>(p, z, row0, col0, sum, patch);
+        store_tma<false, false>(p, t.z, row0, col0, sum, patch);
       else if (p.store == kStoreTmaAdd)
-        store_tma<true, false>(p, z, row0, col0, sum, patch);
+        store_tma<true, false>(p, t.z, row0, col0, sum, patch);
       else
-        store_tma<false, true>(p, z, row0, col0, sum, patch);
+        store_tma<false, true>(p, t.z, row0, col0, sum, patch);
     }
     if (lane == 0) bulk_wait();
   }
