@@ -214,8 +214,10 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // Arrive on a barrier of either CTA of the pair. What it orders are copies
-// that have landed and writes to this CTA's own shared memory that have
-// passed the proxy fence, so the release is at CTA scope.
+// that have landed, writes to this CTA's own shared memory that have passed
+// the proxy fence and TMEM loads that have passed theirs, so the release is
+// at CTA scope (at cluster scope it waits for the warp's other accesses, the
+// stores of the last tile included: 2500 cycles a drain).
 __device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->tempty[acc]), 0));
+        if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->tempty[acc]), 0));
         if (++acc == 2) {
           acc = 0;
           acc_parity ^= 1u;
