@@ -2,12 +2,15 @@
 // gated activation around them (include/ns.h).
 //
 // Element-wise work bound by HBM, so each operator is one pass that reads its
-// inputs and writes its outputs once. A lane holds kLane consecutive values
-// of a row and the lanes of a 32-value block find its largest magnitude by
-// shuffles; the scale is a power of two, so quantising multiplies by an exact
-// factor and rounds once. Two lane widths: 16 values (16-byte accesses of q)
-// when every row allows it, else one value per lane, a block per warp access,
-// which stays coalesced for any pitch and alignment.
+// inputs and writes its outputs once, and what is left is to keep the
+// instructions per element well below what the copies take. A lane holds 8
+// consecutive values of a row and the four lanes of a 32-value block find its
+// largest magnitude by shuffles. The scale is a power of two, so quantising
+// is one fused multiply-add: x * 2^k + 1.5 * 2^23 rounds the exact product
+// half to even and leaves q in the sum's low byte. Rows whose pitch or base
+// does not allow 16-byte accesses take the narrow form: a warp's access is one
+// block, a lane holds one value of each of four blocks, which stays coalesced
+// for any pitch and alignment.
 #include <algorithm>
 
 #include "../../include/ns.h"
@@ -18,6 +21,9 @@ namespace ns {
 namespace {
 
 constexpr int kBlock = 32;  // values per scale
+constexpr int kWide = 8;    // consecutive values per lane where rows are aligned
+constexpr int kNarrow = 4;  // else: values per lane, one of each of as many blocks
+constexpr int kThreads = 256;
 
 struct Held {  // a checkpoint
   int8_t *q;
@@ -31,6 +37,7 @@ struct CkptParams {
   int64_t rows;
   int64_t ld_in, ld_out[3];
   int cols, pitch, scale_pitch;
+  int lanes_log2;      // lanes per row in a block: kThreads >> lanes_log2 rows at a time
   int *status;
 };
 
@@ -41,161 +48,245 @@ __device__ __forceinline__ float up_factor(int e) { return __int_as_float((260 -
 __device__ __forceinline__ float unit_of(int e) {
   return e == 255 ? __int_as_float(0x7fc00000) : __int_as_float((max(e, 7) - 6) << 23);
 }
-__device__ __forceinline__ int quantise(float x, float up) {
-  return max(-127, min(127, __float2int_rn(x * up)));
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a float this size has whole units
+
+template <typename T>
+__device__ __forceinline__ void put(T *at, T v, const void *base, size_t size, int *status) {
+  if (in_bounds(at, sizeof(T), base, size, status)) *at = v;
 }
 
-// Largest magnitude (as float bits; NaN is the largest of all) over the lanes
-// of a block: LANE values per lane, so 32 / LANE neighbouring lanes.
-template <int LANE>
-__device__ __forceinline__ uint32_t block_top(uint32_t top) {
-  if constexpr (LANE == 1) {
-    return __reduce_max_sync(0xffffffffu, top);
-  } else {
+// A lane's values of a row as they were read: wide, kWide from column c on;
+// narrow, columns c, c + 32, ...; zeros beyond the row.
+template <int DT, bool WIDE>
+struct Values {
+  static constexpr int kN = WIDE ? kWide : kNarrow;
+  using E = typename Elem<DT>::T;
+  Pack<DT, kN> v;
+  __device__ __forceinline__ void load(const E *row, int c, int cols, bool here) {
+    if constexpr (WIDE) {
+      if (here) {
+        v.load_stream(row + c);
+      } else {
 #pragma unroll
-    for (int o = 1; o < kBlock / LANE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    return top;
-  }
-}
-
-// The values of one lane quantised and written: x[0..LANE) at row t, columns
-// c.. (values beyond the row are 0 and become the padding bytes).
-template <int LANE>
-__device__ __forceinline__ void hold(const CkptParams &p, const Held &h, int64_t t, int c, float (&x)[LANE]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < LANE; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-  top = block_top<LANE>(top);
-  const int ex = block_exponent(top);
-  const float up = up_factor(ex);
-  Pack<kF32, LANE / 4 + (LANE < 4)> bytes;  // LANE bytes as words
-  int8_t *q8 = reinterpret_cast<int8_t *>(bytes.w);
-#pragma unroll
-  for (int e = 0; e < LANE; ++e) {
-    const int q = ex == 255 ? 0 : quantise(x[e], up);
-    q8[e] = static_cast<int8_t>(q);
-    x[e] = static_cast<float>(q) * unit_of(ex);  // what is held
-  }
-  const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
-  if (c < p.pitch) {
-    int8_t *q = h.q + t * p.pitch + c;
-    if (LANE == 1) {
-      if (in_bounds(q, 1, h.q, qsize, p.status)) *q = q8[0];
+        for (int e = 0; e < kN; ++e) v.set(e, 0.f);
+      }
     } else {
-      bytes.store(reinterpret_cast<float *>(q), h.q, qsize, p.status);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        reinterpret_cast<E *>(v.w)[e] = here && c + e * kBlock < cols ? __ldcs(row + c + e * kBlock) : Elem<DT>::from_f(0.f);
     }
   }
-  const int b = c / kBlock;
-  if (c % kBlock == 0 && b < p.scale_pitch) {
-    uint8_t *s = h.s + t * p.scale_pitch + b;
-    if (in_bounds(s, 1, h.s, ssize, p.status)) *s = c < p.cols ? static_cast<uint8_t>(ex) : 0;
+  // largest magnitude as float bits; NaN is the largest of all
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+    if constexpr (DT == kBF16) {
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) m = __vmaxu2(m, word(i) & 0x7fff7fffu);  // two at a time
+      return max(m & 0xffff0000u, m << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) m = max(m, __float_as_uint(v.get(i)) & 0x7fffffffu);
+      return m;
+    }
   }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    constexpr int kPer = sizeof(v.w[0]) / 4;
+    return reinterpret_cast<const uint32_t *>(&v.w[i / kPer])[i % kPer];
+  }
+};
+
+// The bits whose low byte is q: x in a block whose largest magnitude has the
+// bits `top`. 127.5 units and above would round to 128, and blocks with
+// infinities or NaN hold zeros: both rare, both told by `top`.
+__device__ __forceinline__ bool plain_block(uint32_t top) { return (top & 0x7fffffu) < 0x7f0000u && top < 0x7f800000u; }
+__device__ __forceinline__ uint32_t quantise(float x, float up) { return __float_as_uint(fmaf(x, up, kRound)); }
+__device__ __forceinline__ uint32_t quantise_rare(float x, float up, int ex) {
+  return ex == 255 ? 0u : __float_as_uint(fminf(fmaxf(x * up, -127.f), 127.f) + kRound);
 }
 
-// The values a checkpoint holds at row t, columns c.. (0 beyond the row).
-template <int LANE>
-__device__ __forceinline__ void recall(const CkptParams &p, const Held &h, int64_t t, int c, float (&x)[LANE]) {
-  if (c >= p.cols) {
+// Quantises a lane's values and writes them (with the padding behind the row)
+// where `row`. All lanes of the warp call it.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void hold(const CkptParams &p, const Held &h, int64_t t, int c, bool row, const Values<DT, WIDE> &x) {
+  constexpr int N = Values<DT, WIDE>::kN;
+  const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
+  int8_t *q = h.q + t * p.pitch + c;
+  uint8_t *s = h.s + t * p.scale_pitch + c / kBlock;
+  if constexpr (WIDE) {
+    uint32_t top = x.top();
 #pragma unroll
-    for (int e = 0; e < LANE; ++e) x[e] = 0.f;
-    return;
-  }
-  const float unit = unit_of(h.s[t * p.scale_pitch + c / kBlock]);
-  const int8_t *q = h.q + t * p.pitch + c;
-  if (LANE == 1) {
-    x[0] = static_cast<float>(*q) * unit;
+    for (int o = 1; o < kBlock / N; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int ex = block_exponent(top);
+    const float up = up_factor(ex);
+    uint32_t b[N];
+    if (plain_block(top)) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) b[e] = quantise(x.v.get(e), up);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) b[e] = quantise_rare(x.v.get(e), up, ex);
+    }
+    if (!row) return;
+    if (c < p.pitch) {
+      auto four = [&](int i) {
+        return __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410);
+      };
+      put(reinterpret_cast<uint2 *>(q), make_uint2(four(0), four(4)), h.q, qsize, p.status);
+    }
+    if (c % kBlock == 0 && c / kBlock < p.scale_pitch) put(s, static_cast<uint8_t>(c < p.cols ? ex : 0), h.s, ssize, p.status);
   } else {
-    Pack<kF32, LANE / 4 + (LANE < 4)> bytes;
-    bytes.load(reinterpret_cast<const float *>(q));
-    const int8_t *q8 = reinterpret_cast<const int8_t *>(bytes.w);
 #pragma unroll
-    for (int e = 0; e < LANE; ++e) x[e] = static_cast<float>(q8[e]) * unit;
+    for (int e = 0; e < N; ++e) {
+      const float v = x.v.get(e);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+      const int ex = block_exponent(top), col = c + e * kBlock;
+      const float up = up_factor(ex);
+      const uint32_t b = plain_block(top) ? quantise(v, up) : quantise_rare(v, up, ex);
+      if (row && col < p.pitch) put(q + e * kBlock, static_cast<int8_t>(b), h.q, qsize, p.status);
+      if (row && c % kBlock == e && col / kBlock < p.scale_pitch)  // lane e writes block e's scale
+        put(s + e, static_cast<uint8_t>(col - e < p.cols ? ex : 0), h.s, ssize, p.status);
+    }
   }
 }
 
-template <int DT, int LANE>
-__device__ __forceinline__ void read_row(const void *base, int64_t off, int c, int cols, float (&x)[LANE]) {
-  using P = Pack<DT, LANE>;
-  P v;
-  if (c < cols) v.load_stream(static_cast<const typename P::E *>(base) + off + c);
+// What a checkpoint holds in a lane's columns of row t: the bytes and the scales.
+template <bool WIDE>
+struct HeldValues {
+  static constexpr int kN = WIDE ? kWide : kNarrow;
+  uint32_t w[WIDE ? 2 : 4];
+  int e[WIDE ? 1 : 4];
+  __device__ __forceinline__ void load(const CkptParams &p, const Held &h, int64_t t, int c) {
+    const uint8_t *s = h.s + t * p.scale_pitch + c / kBlock;
+    const int8_t *q = h.q + t * p.pitch + c;
+    if constexpr (WIDE) {
+      e[0] = __ldcs(s);
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(q));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
 #pragma unroll
-  for (int e = 0; e < LANE; ++e) x[e] = c < cols ? v.get(e) : 0.f;
-}
-template <int DT, int LANE>
-__device__ __forceinline__ void write_row(const CkptParams &p, int which, int64_t t, int c, const float (&x)[LANE]) {
-  using P = Pack<DT, LANE>;
-  if (c >= p.cols) return;
-  P v;
+      for (int i = 0; i < kN; ++i)
+        if (c + i * kBlock < p.cols) {
+          e[i] = __ldcs(s + i);
+          w[i] = static_cast<uint8_t>(__ldcs(q + i * kBlock));
+        }
+    }
+  }
+  // the i-th value: (byte + 128) + 2^23 as a float, minus both, in units; exact
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t u = WIDE ? __byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540 + i % 4) : (w[i] ^ 0x80u) | 0x4B000000u;
+    return (__uint_as_float(u) - 8388736.f) * unit_of(e[WIDE ? 0 : i]);
+  }
+};
+
+template <int DT, bool WIDE, int N>
+__device__ __forceinline__ void write_row(const CkptParams &p, int which, int64_t t, int c, const float (&x)[N]) {
+  using E = typename Elem<DT>::T;
+  E *base = static_cast<E *>(p.out[which]);
+  E *to = base + t * p.ld_out[which] + c;
+  const size_t size = static_cast<size_t>((p.rows - 1) * p.ld_out[which] + p.cols) * sizeof(E);
+  if constexpr (WIDE) {
+    Pack<DT, N> v;
 #pragma unroll
-  for (int e = 0; e < LANE; ++e) v.set(e, x[e]);
-  typename P::E *base = static_cast<typename P::E *>(p.out[which]);
-  v.store(base + t * p.ld_out[which] + c, base,
-          static_cast<size_t>((p.rows - 1) * p.ld_out[which] + p.cols) * sizeof(typename P::E), p.status);
+    for (int e = 0; e < N; ++e) v.set(e, x[e]);
+    v.store(to, base, size, p.status);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e * kBlock < p.cols) put(to + e * kBlock, Elem<DT>::from_f(x[e]), base, size, p.status);
+  }
 }
 
+// 1 / (1 + exp(-x)) to a few units in the last place of fp32 (fp32 data), or
+// within |x| of them (bf16 data, far below its rounding)
 template <int DT>
 __device__ __forceinline__ float sigmoid(float x) {
-  return 1.f / (1.f + (DT == kF32 ? expf(-x) : __expf(-x)));
+  return __fdividef(1.f, 1.f + (DT == kF32 ? expf(-x) : __expf(-x)));
 }
 
 enum Op : int { kStore, kLoad, kForward, kBackward };
 
-// One warp per (row, 32 * LANE columns).
-template <int OP, int DT, int LANE>
-__global__ void __launch_bounds__(256) ns_ckpt_kernel(const __grid_constant__ CkptParams p) {
-  const int lane = threadIdx.x & 31;
-  const int span = 32 * LANE;
-  // store and forward also write the padding bytes behind the last column
-  const int extent = OP == kStore || OP == kForward ? max(p.pitch, p.scale_pitch * kBlock) : p.cols;
-  const int per_row = (extent + span - 1) / span;
-  const int64_t items = p.rows * per_row;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t t = it / per_row;
-    const int c = static_cast<int>(it - t * per_row) * span + lane * LANE;
-    if (OP == kStore) {
-      float x[LANE];
-      read_row<DT, LANE>(p.in[0], t * p.ld_in, c, p.cols, x);
-      hold<LANE>(p, p.held[0], t, c, x);
-    } else if (OP == kLoad) {
-      float x[LANE];
-      recall<LANE>(p, p.held[0], t, c, x);
-      write_row<DT, LANE>(p, 0, t, c, x);
-    } else if (OP == kForward) {
-      float g[LANE], u[LANE], h[LANE];
-      read_row<DT, LANE>(p.in[0], t * p.ld_in, c, p.cols, g);
-      read_row<DT, LANE>(p.in[1], t * p.ld_in, c, p.cols, u);
+// A block of threads covers kThreads >> lanes_log2 rows of 1 << lanes_log2
+// lanes, further columns by blockIdx.x, and walks down the rows.
+template <int OP, int DT, bool WIDE>
+__global__ void __launch_bounds__(kThreads) ns_ckpt_kernel(const __grid_constant__ CkptParams p) {
+  using E = typename Elem<DT>::T;
+  constexpr int N = WIDE ? kWide : kNarrow;
+  const int lane = (blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1));
+  const int c = WIDE ? lane * N : (lane / 32) * (32 * N) + lane % 32;
+  const int height = kThreads >> p.lanes_log2;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * height;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < p.rows; t0 += step) {
+    const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
+    const bool row = t < p.rows, here = row && c < p.cols;
+    Values<DT, WIDE> a, b;
+    HeldValues<WIDE> ga, ub;
+    if constexpr (OP != kLoad) a.load(static_cast<const E *>(p.in[0]) + t * p.ld_in, c, p.cols, here);
+    if constexpr (OP == kForward) b.load(static_cast<const E *>(p.in[1]) + t * p.ld_in, c, p.cols, here);
+    if constexpr (OP == kLoad || OP == kBackward)
+      if (here) ga.load(p, p.held[0], t, c);
+    if constexpr (OP == kBackward)
+      if (here) ub.load(p, p.held[1], t, c);
+
+    if constexpr (OP == kStore) hold<DT, WIDE>(p, p.held[0], t, c, row, a);
+    if constexpr (OP == kLoad) {
+      if (here) {
+        float v[N];
 #pragma unroll
-      for (int e = 0; e < LANE; ++e) h[e] = g[e] * sigmoid<DT>(g[e]) * u[e];
-      write_row<DT, LANE>(p, 0, t, c, h);
-      hold<LANE>(p, p.held[0], t, c, g);
-      hold<LANE>(p, p.held[1], t, c, u);
-    } else {
-      float d[LANE], g[LANE], u[LANE], h[LANE];
-      read_row<DT, LANE>(p.in[0], t * p.ld_in, c, p.cols, d);
-      recall<LANE>(p, p.held[0], t, c, g);
-      recall<LANE>(p, p.held[1], t, c, u);
-#pragma unroll
-      for (int e = 0; e < LANE; ++e) {
-        const float s = sigmoid<DT>(g[e]), act = g[e] * s;
-        h[e] = act * u[e];
-        g[e] = d[e] * u[e] * (s * fmaf(g[e], 1.f - s, 1.f));
-        u[e] = d[e] * act;
+        for (int e = 0; e < N; ++e) v[e] = ga.get(e);
+        write_row<DT, WIDE>(p, 0, t, c, v);
       }
-      write_row<DT, LANE>(p, 0, t, c, g);
-      write_row<DT, LANE>(p, 1, t, c, u);
-      if (p.out[2]) write_row<DT, LANE>(p, 2, t, c, h);
+    }
+    if constexpr (OP == kForward) {
+      if (here) {
+        float h[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float g = a.v.get(e);
+          h[e] = g * sigmoid<DT>(g) * b.v.get(e);
+        }
+        write_row<DT, WIDE>(p, 0, t, c, h);
+      }
+      hold<DT, WIDE>(p, p.held[0], t, c, row, a);
+      hold<DT, WIDE>(p, p.held[1], t, c, row, b);
+    }
+    if constexpr (OP == kBackward) {
+      if (here) {
+        float dg[N], du[N], h[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float g = ga.get(e), u = ub.get(e), d = a.v.get(e);
+          const float s = sigmoid<DT>(g), act = g * s;
+          h[e] = act * u;
+          du[e] = d * act;
+          dg[e] = d * u * (s * fmaf(g, 1.f - s, 1.f));
+        }
+        write_row<DT, WIDE>(p, 0, t, c, dg);
+        write_row<DT, WIDE>(p, 1, t, c, du);
+        if (p.out[2]) write_row<DT, WIDE>(p, 2, t, c, h);
+      }
     }
   }
 }
 
-template <int OP, int DT, int LANE>
-int run_one(const CkptParams &p, int sms, cudaStream_t s) {
-  const int span = 32 * LANE;
-  const int64_t extent = std::max<int64_t>(p.pitch, static_cast<int64_t>(p.scale_pitch) * kBlock);
-  const int64_t items = p.rows * ((extent + span - 1) / span);
-  const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, static_cast<int64_t>(sms) * 16));
-  ns_ckpt_kernel<OP, DT, LANE><<<grid, 256, 0, s>>>(p);
+template <int OP, int DT, bool WIDE>
+int run_one(CkptParams p, int sms, cudaStream_t s) {
+  // store and forward also write the padding behind the last column
+  const int64_t extent =
+      OP == kStore || OP == kForward ? std::max<int64_t>(p.pitch, static_cast<int64_t>(p.scale_pitch) * kBlock) : p.cols;
+  // lanes that cover a row; whole warps in the narrow form, whole blocks (4 lanes) in the wide one
+  const int64_t lanes = WIDE ? (extent + kWide - 1) / kWide : (extent + 32 * kNarrow - 1) / (32 * kNarrow) * 32;
+  p.lanes_log2 = WIDE ? 2 : 5;
+  while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < lanes) ++p.lanes_log2;
+  const int64_t gx = (lanes + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
+  const int height = kThreads >> p.lanes_log2;
+  // Blocks beyond the resident ones even out the end; too many repeat the setup: 16384 x 14336 gated, both ways,
+  // 675 us at 32 a SM, 660 at 128, 722 without a limit; 4093 x 6143 narrow store and load 61, 73 and 79. (Two row
+  // steps in flight per thread cost registers: 10 % slower.)
+  const int64_t want = (p.rows + height - 1) / height;
+  const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(sms) * (WIDE ? 128 : 32) / gx);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>({want, most, 65535})), 1);
+  ns_ckpt_kernel<OP, DT, WIDE><<<grid, kThreads, 0, s>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -207,8 +298,8 @@ int ckpt_call(CkptParams &p, int dtype, bool wide, void *stream) {
   p.status = call.status;
   return call.launch(kOpCkpt, [&] {
     if (dtype == NS_BF16)
-      return wide ? run_one<OP, kBF16, 16>(p, call.sms, call.s) : run_one<OP, kBF16, 1>(p, call.sms, call.s);
-    return wide ? run_one<OP, kF32, 16>(p, call.sms, call.s) : run_one<OP, kF32, 1>(p, call.sms, call.s);
+      return wide ? run_one<OP, kBF16, true>(p, call.sms, call.s) : run_one<OP, kBF16, false>(p, call.sms, call.s);
+    return wide ? run_one<OP, kF32, true>(p, call.sms, call.s) : run_one<OP, kF32, false>(p, call.sms, call.s);
   });
 }
 
@@ -249,7 +340,7 @@ extern "C" int ns_ckpt_store(const void *x, int64_t ld_x, int64_t rows, int64_t 
   p.rows = rows;
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(q), static_cast<uint8_t *>(scales)};
-  return ckpt_call<kStore>(p, dtype, cols % 16 == 0 && rows_aligned(x, ld_x, elt, 16), stream);
+  return ckpt_call<kStore>(p, dtype, cols % kWide == 0 && rows_aligned(x, ld_x, elt, kWide), stream);
 }
 
 extern "C" int ns_ckpt_load(const void *q, const void *scales, int64_t rows, int64_t cols, void *out, int64_t ld_out,
@@ -270,7 +361,7 @@ extern "C" int ns_ckpt_load(const void *q, const void *scales, int64_t rows, int
   p.rows = rows;
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(const_cast<void *>(q)), static_cast<uint8_t *>(const_cast<void *>(scales))};
-  return ckpt_call<kLoad>(p, dtype, cols % 16 == 0 && rows_aligned(out, ld_out, elt, 16), stream);
+  return ckpt_call<kLoad>(p, dtype, cols % kWide == 0 && rows_aligned(out, ld_out, elt, kWide), stream);
 }
 
 extern "C" int ns_gated_forward(const void *gate, const void *up, int64_t ld_in, int64_t rows, int64_t cols, void *h,
@@ -304,8 +395,8 @@ extern "C" int ns_gated_forward(const void *gate, const void *up, int64_t ld_in,
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(q_gate), static_cast<uint8_t *>(s_gate)};
   p.held[1] = Held{static_cast<int8_t *>(q_up), static_cast<uint8_t *>(s_up)};
-  const bool wide = cols % 16 == 0 && rows_aligned(gate, ld_in, elt, 16) && rows_aligned(up, ld_in, elt, 16) &&
-                    rows_aligned(h, ld_h, elt, 16);
+  const bool wide = cols % kWide == 0 && rows_aligned(gate, ld_in, elt, kWide) && rows_aligned(up, ld_in, elt, kWide) &&
+                    rows_aligned(h, ld_h, elt, kWide);
   return ckpt_call<kForward>(p, dtype, wide, stream);
 }
 
@@ -343,7 +434,7 @@ extern "C" int ns_gated_backward(const void *dh, int64_t ld_dh, const void *q_ga
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(const_cast<void *>(q_gate)), static_cast<uint8_t *>(const_cast<void *>(s_gate))};
   p.held[1] = Held{static_cast<int8_t *>(const_cast<void *>(q_up)), static_cast<uint8_t *>(const_cast<void *>(s_up))};
-  const bool wide = cols % 16 == 0 && rows_aligned(dh, ld_dh, elt, 16) && rows_aligned(dgate, ld_d, elt, 16) &&
-                    rows_aligned(dup, ld_d, elt, 16) && (!h || rows_aligned(h, ld_h, elt, 16));
+  const bool wide = cols % kWide == 0 && rows_aligned(dh, ld_dh, elt, kWide) && rows_aligned(dgate, ld_d, elt, kWide) &&
+                    rows_aligned(dup, ld_d, elt, kWide) && (!h || rows_aligned(h, ld_h, elt, kWide));
   return ckpt_call<kBackward>(p, dtype, wide, stream);
 }
