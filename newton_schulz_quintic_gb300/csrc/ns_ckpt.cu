@@ -152,7 +152,6 @@ __device__ __forceinline__ void hold(const CkptParams &p, const Held &h, int64_t
 // What a checkpoint holds in a lane's columns of row t: the bytes and the scales.
 template <bool WIDE>
 struct HeldValues {
-  static constexpr int kN = WIDE ? kWide : kNarrow;
   uint32_t w[WIDE ? 2 : 4];
   int e[WIDE ? 1 : 4];
   __device__ __forceinline__ void load(const CkptParams &p, const Held &h, int64_t t, int c) {
@@ -165,7 +164,7 @@ struct HeldValues {
       w[1] = v.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
+      for (int i = 0; i < kNarrow; ++i)
         if (c + i * kBlock < p.cols) {
           e[i] = __ldcs(s + i);
           w[i] = static_cast<uint8_t>(__ldcs(q + i * kBlock));

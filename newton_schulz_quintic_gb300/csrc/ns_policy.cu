@@ -1,11 +1,19 @@
 // ns_policy.cu -- log probabilities of target tokens and the clipped policy
 // loss with a KL term, with the gradient of the logits (include/ns.h).
 //
-// Per row: one pass over the logits keeps each thread's running maximum m and
-// sum of exp(z - m); merged over the CTA they give logp = z[y] - m - log(sum).
+// Per row, with m the largest logit, k = inv_temperature * log2(e) and s = sum
+// of 2^((v - m) k) over the row's logits v: logp = ((v[y] - m) k - log2 s) /
+// log2(e). The difference comes before the factor, so logits up to the type's
+// largest and lowest values do not overflow. Each thread keeps a running
+// maximum and sum; they are merged over the CTA (or over the cluster, where
+// few rows leave SMs idle) in a fixed order.
+//
 // A row's gradient depends on nothing but the row, so the second pass
-// (softmax times the row's coefficient) follows at once. The loss is summed
-// over the rows by one CTA in a fixed order.
+// (softmax times the row's coefficient) follows at once. It is the memory
+// that bounds this: one read and one write of the logits. The second read
+// comes from L2 as long as the rows in flight fit there.
+// The loss is summed over the rows by one CTA in a fixed order.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/ns.h"
@@ -24,26 +32,35 @@ struct PolicyParams {
   int64_t rows, ld, ld_d;
   int vocab;
   float inv_temp, clip_low, clip_high, kl_coef;
+  int cluster;  // CTAs per row
   int *status;
 };
 
-constexpr int kPolicyThreads = 512;
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// (m, s) stands for s * exp(m); m = -inf, s = 0 is nothing.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The largest logit m so far and s = sum of 2^((v - m) k); m = -inf, s = 0 is nothing.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b) {
+__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return MaxSum{m, a.s + b.s};  // nothing yet (or NaN sums, kept)
-  return MaxSum{m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
+  return MaxSum{m, a.s * exp2_fast((a.m - m) * k) + b.s * exp2_fast((b.m - m) * k)};
 }
 
 struct RowResult {
   float logp, kl, loss, slope;
 };
 
-// The row's outputs from its target's z - max and log(sum).
+// The row's outputs from its target's log probability.
 __device__ __forceinline__ RowResult policy_row(const PolicyParams &p, int64_t t, float logp) {
   RowResult r{logp, 0.f, 0.f, 0.f};
   if (!p.weight) return r;
@@ -61,85 +78,136 @@ __device__ __forceinline__ RowResult policy_row(const PolicyParams &p, int64_t t
   return r;
 }
 
+// Largest of a pack's values.
 template <int DT, int VEC>
-__global__ void __launch_bounds__(kPolicyThreads) ns_policy_kernel(const __grid_constant__ PolicyParams p) {
+__device__ __forceinline__ float pack_max(const Pack<DT, VEC> &v) {
+  if constexpr (DT == kBF16 && VEC == 8) {  // two at a time; NaN is passed over here and reaches the sum
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(v.w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    float m = v.get(0);
+#pragma unroll
+    for (int e = 1; e < VEC; ++e) m = fmaxf(m, v.get(e));
+    return m;
+  }
+}
+
+// One row per cluster of p.cluster CTAs (1: no cluster); CTA rank r takes
+// every p.cluster-th stretch of the row.
+template <int DT, int VEC, bool GRAD>
+__global__ void __launch_bounds__(kMaxThreads) ns_policy_kernel(const __grid_constant__ PolicyParams p) {
   using P = Pack<DT, VEC>;
   using E = typename P::E;
-  __shared__ MaxSum part[kPolicyThreads / 32];
+  __shared__ MaxSum part[kMaxThreads / 32];
+  __shared__ MaxSum mine;  // this CTA's share of the row, read by the cluster
   __shared__ MaxSum all;
   __shared__ RowResult res;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = (rank * blockDim.x + threadIdx.x) * VEC, stride = p.cluster * blockDim.x * VEC;
+  const float k = p.inv_temp * kLog2e;
   const size_t dsize = static_cast<size_t>((p.rows - 1) * p.ld_d + p.vocab) * sizeof(E);
-  for (int64_t t = blockIdx.x; t < p.rows; t += gridDim.x) {
+  for (int64_t t = blockIdx.x / p.cluster; t < p.rows; t += gridDim.x / p.cluster) {
     const E *x = static_cast<const E *>(p.logits) + t * p.ld;
-    E *g = p.dlogits ? static_cast<E *>(p.dlogits) + t * p.ld_d : nullptr;
+    E *g = GRAD ? static_cast<E *>(p.dlogits) + t * p.ld_d : nullptr;
     const int y = p.targets.get(t);
-    bool live = y >= 0 && (!p.weight || p.weight[t] != 0.f);
+    bool live = y >= 0 && (!p.weight || p.weight[t] != 0.f);  // the same in every thread of the cluster
     MaxSum a{-INFINITY, 0.f};
     if (live) {
-      for (int c = threadIdx.x * VEC; c < p.vocab; c += kPolicyThreads * VEC) {
+#pragma unroll 4
+      for (int c = first; c < p.vocab; c += stride) {
         P v;
         v.load(x + c);
-        float top = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) top = fmaxf(top, v.get(e) * p.inv_temp);
+        const float top = pack_max<DT, VEC>(v);
         if (top > a.m) {
-          a.s *= __expf(a.m - top);
+          a.s *= exp2_fast((a.m - top) * k);
           a.m = top;
         }
-        // a pack of -inf alone adds exp(-inf - 0) = 0; NaN reaches the sum either way
+        // a pack of -inf alone adds 2^(-inf - 0) = 0; NaN reaches the sum either way
         const float m = a.m == -INFINITY ? 0.f : a.m;
+        float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) a.s += __expf(fmaf(v.get(e), p.inv_temp, -m));
+        for (int e = 0; e < VEC; ++e) s += exp2_fast((v.get(e) - m) * k);
+        a.s += s;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
-        a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
+        a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
       if (lane == 0) part[warp] = a;
       __syncthreads();
+      if (warp == 0) {
+        a = lane < warps ? part[lane] : MaxSum{-INFINITY, 0.f};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
+        if (lane == 0) mine = a;
+      }
+      if (p.cluster > 1) {
+        cluster_sync();
+        if (warp == 0) {
+          MaxSum b{-INFINITY, 0.f};
+          if (lane < p.cluster) {
+            const uint32_t at = mapa_shared(smem_u32(&mine), lane);
+            b.m = __uint_as_float(ld_shared_cluster_u32(at));
+            b.s = __uint_as_float(ld_shared_cluster_u32(at + 4));
+          }
+          a = b;
+#pragma unroll
+          for (int o = kMaxCluster / 2; o > 0; o >>= 1)
+            a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
+        }
+      }
       if (threadIdx.x == 0) {
-        for (int k = 1; k < kPolicyThreads / 32; ++k) a = merge(a, part[k]);
         all = a;
         RowResult r{0.f, 0.f, 0.f, 0.f};
-        if (a.s != 0.f) {  // else every logit is -inf: no distribution
-          const float z = Elem<DT>::to_f(x[y]) * p.inv_temp;
-          r = policy_row(p, t, (z - a.m) - logf(a.s));
-        }
+        if (a.s != 0.f)  // else every logit is -inf: no distribution
+          r = policy_row(p, t, ((Elem<DT>::to_f(x[y]) - a.m) * k - log2f(a.s)) * kLn2);
         res = r;
       }
       __syncthreads();
       a = all;
       if (a.s == 0.f) live = false;
-    } else if (threadIdx.x == 0) {
-      res = RowResult{0.f, 0.f, 0.f, 0.f};
     }
-    if (threadIdx.x == 0) {
-      if (in_bounds(p.logp + t, 4, p.logp, p.rows * 4, p.status)) p.logp[t] = res.logp;
+    if (threadIdx.x == 0 && rank == 0) {
+      const RowResult r = live ? res : RowResult{0.f, 0.f, 0.f, 0.f};
+      if (in_bounds(p.logp + t, 4, p.logp, p.rows * 4, p.status)) p.logp[t] = r.logp;
       if (p.weight) {
-        if (in_bounds(p.kl + t, 4, p.kl, p.rows * 4, p.status)) p.kl[t] = res.kl;
-        p.row_loss[t] = res.loss;
+        if (in_bounds(p.kl + t, 4, p.kl, p.rows * 4, p.status)) p.kl[t] = r.kl;
+        p.row_loss[t] = r.loss;
       }
     }
-    if (g) {
-      const float slope = live ? res.slope : 0.f, scale = live ? -slope / a.s : 0.f;
-      for (int c = threadIdx.x * VEC; c < p.vocab; c += kPolicyThreads * VEC) {
-        P v;
-        if (live) {
-          v.load(x + c);
+    if constexpr (GRAD) {
+      if (live) {
+        const float slope = res.slope, scale = -slope / a.s;
+        const bool in_place = p.dlogits == p.logits;
+        // in place, the target's logit is read by every CTA before any overwrites it
+        if (p.cluster > 1 && in_place) cluster_sync();
+#pragma unroll 4
+        for (int c = first; c < p.vocab; c += stride) {
+          P v;
+          v.load_stream(x + c);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float d = scale * __expf(fmaf(v.get(e), p.inv_temp, -a.m));
-            if (c + e == y) d += slope;
-            v.set(e, d);
+          for (int e = 0; e < VEC; ++e) v.set(e, scale * exp2_fast((v.get(e) - a.m) * k));
+          if (static_cast<unsigned>(y - c) < VEC) {  // the target's pack, again with its 1
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              if (c + e == y) v.set(e, fmaf(scale, exp2_fast((Elem<DT>::to_f(x[y]) - a.m) * k), slope));
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v.set(e, 0.f);
+          v.store_stream(g + c, p.dlogits, dsize, p.status);
         }
-        v.store(g + c, p.dlogits, dsize, p.status);
+      } else {
+        P v;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v.set(e, 0.f);
+        for (int c = first; c < p.vocab; c += stride) v.store_stream(g + c, p.dlogits, dsize, p.status);
       }
     }
-    __syncthreads();  // `all`, `res` and `part` are free for the next row
+    // shared values are free for the next row (in a cluster: once all have read `mine`)
+    if (p.cluster > 1)
+      cluster_sync();
+    else
+      __syncthreads();
   }
 }
 
@@ -158,11 +226,39 @@ __global__ void __launch_bounds__(1024) ns_policy_sum_kernel(const __grid_consta
   }
 }
 
-template <int DT, int VEC>
-int run_policy(const PolicyParams &p, int sms, cudaStream_t s) {
+template <int DT, int VEC, bool GRAD>
+int run_policy(PolicyParams p, int sms, cudaStream_t s) {
   if (p.rows > 0) {
-    const int grid = static_cast<int>(p.rows < sms * 4 ? p.rows : sms * 4);
-    ns_policy_kernel<DT, VEC><<<grid, kPolicyThreads, 0, s>>>(p);
+    constexpr int elt = DT == kBF16 ? 2 : 4;
+    // threads: two packs or more each, down to a warp
+    int threads = kMaxThreads;
+    while (threads > 32 && static_cast<int64_t>(threads) * 2 * VEC > p.vocab) threads /= 2;
+    // few rows: a cluster of CTAs per row while SMs are idle and every thread keeps two packs
+    p.cluster = 1;
+    while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= sms &&
+           static_cast<int64_t>(threads) * p.cluster * 4 * VEC <= p.vocab)
+      p.cluster *= 2;
+    // as many CTAs as are resident, but no more rows in flight than L2 keeps
+    // for the second read (kL2Rows bytes) unless that leaves SMs idle
+    constexpr int64_t kL2Rows = int64_t(80) << 20;
+    int64_t grid = static_cast<int64_t>(sms) * (2048 / threads);
+    if (GRAD) grid = std::min(grid, std::max<int64_t>(sms, kL2Rows / std::max<int64_t>(1, static_cast<int64_t>(p.vocab) * elt)));
+    grid = std::min(grid, p.rows * p.cluster) / p.cluster * p.cluster;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, ns_policy_kernel<DT, VEC, GRAD>, p) != cudaSuccess) {
+      cudaGetLastError();
+      return -1;
+    }
     count_launch();
   }
   if (p.weight) {
@@ -170,6 +266,11 @@ int run_policy(const PolicyParams &p, int sms, cudaStream_t s) {
     count_launch();
   }
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int DT, int VEC>
+int run_policy(const PolicyParams &p, int sms, cudaStream_t s) {
+  return p.dlogits ? run_policy<DT, VEC, true>(p, sms, s) : run_policy<DT, VEC, false>(p, sms, s);
 }
 
 int policy_call(PolicyParams &p, int dtype, void *stream) {

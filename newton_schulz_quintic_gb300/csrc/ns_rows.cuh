@@ -44,6 +44,12 @@ struct Pack {
     for (int i = 0; i < kN; ++i)
       if (in_bounds(reinterpret_cast<const W *>(p) + i, kAcc, base, size, status)) reinterpret_cast<W *>(p)[i] = w[i];
   }
+  // written once and not read again here: first to leave the caches
+  __device__ __forceinline__ void store_stream(E *p, const void *base, size_t size, int *status) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (in_bounds(reinterpret_cast<const W *>(p) + i, kAcc, base, size, status)) __stcs(reinterpret_cast<W *>(p) + i, w[i]);
+  }
 };
 
 // Token ids: int32 or int64; anything outside [0, vocab) becomes -1.

@@ -37,66 +37,64 @@ _PROTOTYPES = {
 }
 _functions: dict = {}
 
+# These calls are short: what Python spends around a kernel counts. The raw
+# handle of the current stream is had without making a Stream object where
+# torch offers that.
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_empty = torch.empty
+
 
 def _function(name):
-    f = _functions.get(name)
-    if f is None:
-        f = getattr(_api.load_library(), name)
-        f.restype, f.argtypes = _i32, _PROTOTYPES[name]
-        _functions[name] = f
+    f = getattr(_api.load_library(), name)
+    f.restype, f.argtypes = _i32, _PROTOTYPES[name]
+    _functions[name] = f
     return f
 
 
 def _call(name, *args) -> None:
-    rc = _function(name)(*args)
+    rc = (_functions.get(name) or _function(name))(*args)
     if rc != 0:
         raise _api.NSError(rc, name)
 
 
-class _On:
-    """The device and stream of a call, current inside the ``with`` block when
-    they are not already (so that what it allocates belongs to that stream)."""
+_HERE = contextlib.nullcontext()
 
-    __slots__ = ("ptr", "_stack")
 
-    def __init__(self, device, stream):
-        self._stack = None
-        if stream is not None or device.index != torch.cuda.current_device():
-            self._stack = contextlib.ExitStack()
-            self._stack.enter_context(torch.cuda.device(device))
-            if stream is not None:
-                self._stack.enter_context(torch.cuda.stream(stream))
-        self.ptr = torch.cuda.current_stream(device).cuda_stream
-
-    def __enter__(self):
-        return self.ptr
-
-    def __exit__(self, *exc):
-        if self._stack is not None:
-            self._stack.close()
-        return False
+def _on(device, stream):
+    """The block in which ``device`` and ``stream`` are torch's current ones, so
+    that what a call allocates belongs to the stream it runs on; inside it
+    _raw_stream(device.index) is the stream's handle."""
+    if stream is None and device.index == _current_device():
+        return _HERE
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
 
 
 def _matrix(t, what, rows=None, cols=None, dtype=None):
     """The row pitch of a 2-D CUDA tensor of a supported type, checked."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be 2-D")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype not in _DTYPE:
-        raise TypeError(f"{what}: unsupported dtype {t.dtype}: use float32 or bfloat16")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, is {t.dtype}")
-    n, m = t.shape
+    kind = t.dtype
+    if kind not in _DTYPE:
+        raise TypeError(f"{what}: unsupported dtype {kind}: use float32 or bfloat16")
+    if dtype is not None and kind != dtype:
+        raise ValueError(f"{what} must be {dtype}, is {kind}")
+    n, m = shape
     if (rows is not None and n != rows) or (cols is not None and m != cols):
         raise ValueError(f"{what} must be {rows if rows is not None else n} x {cols if cols is not None else m}, "
                          f"is {n} x {m}")
-    if n == 0 or m == 0:
-        return m
     s0, s1 = t.stride()
-    if m > 1 and s1 != 1:
+    if s1 != 1 and m > 1 and n > 0:
         raise ValueError(f"{what} must have unit column stride")
-    if n == 1:
+    if n <= 1 or m == 0:
         return m
     if s0 < m:
         raise ValueError(f"{what}: rows must not overlap")
@@ -104,7 +102,7 @@ def _matrix(t, what, rows=None, cols=None, dtype=None):
 
 
 def _vector(t, what, n, dtypes, device):
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{what} must be 1-D of length {n}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
@@ -129,19 +127,19 @@ def embed_lookup(table, ids, scale: float = 1.0, out=None, stream=None):
     dim (given: 2-D, one row per id)."""
     ld = _matrix(table, "table")
     vocab, dim = table.shape
-    flat = ids.reshape(-1)
+    dev, dt = table.device, table.dtype
+    flat = ids if ids.dim() == 1 else ids.reshape(-1)
     n = flat.shape[0]
-    p_ids = _vector(flat, "ids", n, _IDTYPE, table.device)
-    with _On(table.device, stream) as s:
+    p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
+    with _on(dev, stream):
         if out is None:
-            res = torch.empty((*ids.shape, dim), dtype=table.dtype, device=table.device)
-            p_out, ld_out = res.data_ptr(), dim
+            out, ld_out = _empty((*ids.shape, dim), dtype=dt, device=dev), dim
         else:
-            _same_device(table.device, out)
-            res, p_out, ld_out = out, out.data_ptr(), _matrix(out, "out", n, dim, table.dtype)
-        _call("ns_embed_lookup", table.data_ptr(), ld, vocab, dim, p_ids, _IDTYPE[flat.dtype], n, scale, p_out, ld_out,
-              _DTYPE[table.dtype], s)
-    return res
+            _same_device(dev, out)
+            ld_out = _matrix(out, "out", n, dim, dt)
+        _call("ns_embed_lookup", table.data_ptr(), ld, vocab, dim, p_ids, _IDTYPE[flat.dtype], n, scale, out.data_ptr(),
+              ld_out, _DTYPE[dt], _raw_stream(dev.index))
+    return out
 
 
 def embed_grad(dout, ids, vocab: int | None = None, scale: float = 1.0, grad=None, accumulate: bool = False,
@@ -153,22 +151,24 @@ def embed_grad(dout, ids, vocab: int | None = None, scale: float = 1.0, grad=Non
     (default: dout's). Deterministic; returns ``grad``."""
     ld = _matrix(dout, "dout")
     n, dim = dout.shape
-    flat = ids.reshape(-1)
-    p_ids = _vector(flat, "ids", n, _IDTYPE, dout.device)
+    dev = dout.device
+    flat = ids if ids.dim() == 1 else ids.reshape(-1)
+    p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
     if grad is None:
         if accumulate or vocab is None:
             raise ValueError("without grad, give vocab and do not accumulate")
     else:
         if vocab is not None and vocab != grad.shape[0]:
             raise ValueError("grad has another number of rows than vocab")
-        _same_device(dout.device, grad)
+        _same_device(dev, grad)
         ld_grad = _matrix(grad, "grad", None, dim, dtype)
-    with _On(dout.device, stream) as s:
+    with _on(dev, stream):
         if grad is None:
-            grad = torch.empty((int(vocab), dim), dtype=dtype or dout.dtype, device=dout.device)
+            grad = _empty((int(vocab), dim), dtype=dtype or dout.dtype, device=dev)
             ld_grad = _matrix(grad, "grad")
         _call("ns_embed_grad", dout.data_ptr(), ld, p_ids, _IDTYPE[flat.dtype], n, scale, grad.data_ptr(), ld_grad,
-              grad.shape[0], dim, _DTYPE[dout.dtype], _DTYPE[grad.dtype], 1 if accumulate else 0, s)
+              grad.shape[0], dim, _DTYPE[dout.dtype], _DTYPE[grad.dtype], 1 if accumulate else 0,
+              _raw_stream(dev.index))
     return grad
 
 
@@ -179,13 +179,14 @@ def token_logprobs(logits, targets, temperature: float = 1.0, stream=None):
     target is outside the vocabulary (e.g. -100) is masked and gives 0."""
     ld = _matrix(logits, "logits")
     n, vocab = logits.shape
-    p_y = _vector(targets, "targets", n, _IDTYPE, logits.device)
+    dev = logits.device
+    p_y = _vector(targets, "targets", n, _IDTYPE, dev)
     if not temperature > 0:
         raise ValueError("temperature must be positive")
-    with _On(logits.device, stream) as s:
-        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+    with _on(dev, stream):
+        logp = _empty(n, dtype=torch.float32, device=dev)
         _call("ns_token_logprobs", logits.data_ptr(), ld, n, vocab, p_y, _IDTYPE[targets.dtype], 1.0 / temperature,
-              logp.data_ptr(), _DTYPE[logits.dtype], s)
+              logp.data_ptr(), _DTYPE[logits.dtype], _raw_stream(dev.index))
     return logp
 
 
@@ -224,20 +225,26 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
             raise ValueError("dlogits given, but grad is False")
         _same_device(dev, dlogits)
         _matrix(dlogits, "dlogits", n, vocab, logits.dtype)
-    with _On(dev, stream) as s:
+    with _on(dev, stream):
         if grad and dlogits is None:
-            dlogits = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
-        out = torch.empty(2 * n + 1, dtype=torch.float32, device=dev)
-        p = out.data_ptr()
+            dlogits = _empty((n, vocab), dtype=logits.dtype, device=dev)
+        loss = _empty((), dtype=torch.float32, device=dev)
+        logp = _empty(n, dtype=torch.float32, device=dev)
+        kl = _empty(n, dtype=torch.float32, device=dev)
         _call("ns_policy_loss", logits.data_ptr(), ld, n, vocab, p_y, _IDTYPE[targets.dtype], p_old, p_ref, p_adv, p_w,
-              1.0 / temperature, clip_low, clip_high, kl_coef, p + 8 * n, p, p + 4 * n,
-              dlogits.data_ptr() if grad else None, _matrix(dlogits, "dlogits") if grad else 0, _DTYPE[logits.dtype], s)
-    return PolicyLoss(out[2 * n], out[:n], out[n:2 * n], dlogits)
+              1.0 / temperature, clip_low, clip_high, kl_coef, loss.data_ptr(), logp.data_ptr(), kl.data_ptr(),
+              dlogits.data_ptr() if grad else None, _matrix(dlogits, "dlogits") if grad else 0, _DTYPE[logits.dtype],
+              _raw_stream(dev.index))
+    return PolicyLoss(loss, logp, kl, dlogits)
 
 
 # ------------------------------------------------------------------ 8-bit activations
-def _ceil(n, m):
-    return (n + m - 1) // m * m
+def _pitch(cols):
+    return (cols + 15) // 16 * 16
+
+
+def _scale_pitch(cols):
+    return (cols + 127) // 128 * 4
 
 
 class Checkpoint8:
@@ -245,54 +252,88 @@ class Checkpoint8:
     16) and ``scales`` (uint8, one per 32 values, rounded up to 4 a row). The
     format is described at ns_ckpt_store in include/ns.h."""
 
-    __slots__ = ("q", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "device", "_q", "_scales", "_buffer", "_at", "_p_q", "_p_scales")
 
     def __init__(self, q, scales, cols: int):
         rows = q.shape[0]
-        if q.dtype != torch.int8 or q.shape != (rows, _ceil(cols, 16)) or not q.is_contiguous():
-            raise ValueError(f"q must be contiguous int8, {rows} x {_ceil(cols, 16)}")
-        if (scales.dtype != torch.uint8 or scales.shape != (rows, _ceil((cols + 31) // 32, 4))
-                or not scales.is_contiguous()):
-            raise ValueError(f"scales must be contiguous uint8, {rows} x {_ceil((cols + 31) // 32, 4)}")
-        if q.device.type != "cuda" or scales.device != q.device:
+        if q.dtype != torch.int8 or q.shape != (rows, _pitch(cols)) or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous int8, {rows} x {_pitch(cols)}")
+        if scales.dtype != torch.uint8 or scales.shape != (rows, _scale_pitch(cols)) or not scales.is_contiguous():
+            raise ValueError(f"scales must be contiguous uint8, {rows} x {_scale_pitch(cols)}")
+        if not q.is_cuda or scales.device != q.device:
             raise ValueError("q and scales must be CUDA tensors on one device")
-        self.q, self.scales, self.rows, self.cols = q, scales, rows, cols
+        self.rows, self.cols, self.device = rows, cols, q.device
+        self._q, self._scales, self._buffer = q, scales, None
+        self._p_q, self._p_scales = q.data_ptr(), scales.data_ptr()
 
     @classmethod
     def empty(cls, rows: int, cols: int, device):
-        return cls(torch.empty((rows, _ceil(cols, 16)), dtype=torch.int8, device=device),
-                   torch.empty((rows, _ceil((cols + 31) // 32, 4)), dtype=torch.uint8, device=device), cols)
+        """Room for a matrix, in one allocation, uninitialised."""
+        return cls._empties(1, rows, cols, device)[0]
+
+    @classmethod
+    def _empties(cls, count, rows, cols, device):
+        # `count` of them in one allocation, which lives until the last is dropped
+        nq = rows * _pitch(cols)
+        each = (nq + rows * _scale_pitch(cols) + 15) // 16 * 16
+        buffer = _empty(count * each, dtype=torch.uint8, device=device)
+        p = buffer.data_ptr()
+        made = []
+        for k in range(count):
+            self = cls.__new__(cls)
+            self.rows, self.cols, self.device = rows, cols, device
+            self._q = self._scales = None  # views of the buffer, made when asked for
+            self._buffer, self._at = buffer, k * each
+            self._p_q = p + k * each
+            self._p_scales = self._p_q + nq
+            made.append(self)
+        return made
 
     @property
-    def device(self):
-        return self.q.device
+    def q(self):
+        if self._q is None:
+            n, pitch = self.rows, _pitch(self.cols)
+            self._q = self._buffer[self._at:self._at + n * pitch].view(torch.int8).view(n, pitch)
+        return self._q
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            n, pitch = self.rows, _scale_pitch(self.cols)
+            at = self._at + n * _pitch(self.cols)
+            self._scales = self._buffer[at:at + n * pitch].view(n, pitch)
+        return self._scales
 
     def nbytes(self) -> int:
-        return self.q.numel() + self.scales.numel()
+        return self.rows * (_pitch(self.cols) + _scale_pitch(self.cols))
 
 
 def checkpoint_store(x, stream=None) -> Checkpoint8:
     """Hold a 2-D tensor in 8 bits (ns_ckpt_store)."""
     ld = _matrix(x, "x")
     rows, cols = x.shape
-    with _On(x.device, stream) as s:
-        ck = Checkpoint8.empty(rows, cols, x.device)
-        _call("ns_ckpt_store", x.data_ptr(), ld, rows, cols, ck.q.data_ptr(), ck.scales.data_ptr(), _DTYPE[x.dtype], s)
+    dev = x.device
+    with _on(dev, stream):
+        ck = Checkpoint8.empty(rows, cols, dev)
+        _call("ns_ckpt_store", x.data_ptr(), ld, rows, cols, ck._p_q, ck._p_scales, _DTYPE[x.dtype],
+              _raw_stream(dev.index))
     return ck
 
 
 def checkpoint_load(ck: Checkpoint8, dtype=torch.bfloat16, out=None, stream=None):
     """The values that a checkpoint holds (ns_ckpt_load)."""
+    dev = ck.device
+    ld = ck.cols
     if out is not None:
-        _same_device(ck.device, out)
-        _matrix(out, "out", ck.rows, ck.cols)
+        _same_device(dev, out)
+        ld = _matrix(out, "out", ck.rows, ck.cols)
     elif dtype not in _DTYPE:
         raise TypeError(f"unsupported dtype {dtype}: use float32 or bfloat16")
-    with _On(ck.device, stream) as s:
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((ck.rows, ck.cols), dtype=dtype, device=ck.device)
-        _call("ns_ckpt_load", ck.q.data_ptr(), ck.scales.data_ptr(), ck.rows, ck.cols, out.data_ptr(),
-              _matrix(out, "out"), _DTYPE[out.dtype], s)
+            out = _empty((ck.rows, ck.cols), dtype=dtype, device=dev)
+        _call("ns_ckpt_load", ck._p_q, ck._p_scales, ck.rows, ck.cols, out.data_ptr(), ld, _DTYPE[out.dtype],
+              _raw_stream(dev.index))
     return out
 
 
@@ -303,17 +344,17 @@ def gated_forward(gate, up, out=None, stream=None):
     checkpoint of gate, checkpoint of up)."""
     ld = _matrix(gate, "gate")
     rows, cols = gate.shape
-    ld_up = _matrix(up, "up", rows, cols, gate.dtype)
-    _same_device(gate.device, up, out)
-    if ld_up != ld:
+    dev, dt = gate.device, gate.dtype
+    if _matrix(up, "up", rows, cols, dt) != ld:
         raise ValueError("gate and up must have the same row stride")
-    with _On(gate.device, stream) as s:
+    _same_device(dev, up, out)
+    ld_out = cols if out is None else _matrix(out, "out", rows, cols, dt)
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device)
-        a, b = Checkpoint8.empty(rows, cols, gate.device), Checkpoint8.empty(rows, cols, gate.device)
-        _call("ns_gated_forward", gate.data_ptr(), up.data_ptr(), ld, rows, cols, out.data_ptr(),
-              _matrix(out, "out", rows, cols, gate.dtype), a.q.data_ptr(), a.scales.data_ptr(), b.q.data_ptr(),
-              b.scales.data_ptr(), _DTYPE[gate.dtype], s)
+            out = _empty((rows, cols), dtype=dt, device=dev)
+        a, b = Checkpoint8._empties(2, rows, cols, dev)
+        _call("ns_gated_forward", gate.data_ptr(), up.data_ptr(), ld, rows, cols, out.data_ptr(), ld_out, a._p_q,
+              a._p_scales, b._p_q, b._p_scales, _DTYPE[dt], _raw_stream(dev.index))
     return out, a, b
 
 
@@ -324,20 +365,21 @@ def gated_backward(dh, ck_gate: Checkpoint8, ck_up: Checkpoint8, recompute: bool
     again, the input of the next layer's weight gradient (None unless
     ``recompute``)."""
     rows, cols = ck_gate.rows, ck_gate.cols
+    dev, dt = dh.device, dh.dtype
     ld = _matrix(dh, "dh", rows, cols)
-    if (ck_up.rows, ck_up.cols) != (rows, cols):
+    if ck_up.rows != rows or ck_up.cols != cols:
         raise ValueError("the checkpoints of gate and up must have one shape")
-    _same_device(dh.device, ck_gate, ck_up, dgu)
-    if dgu is not None:
-        _matrix(dgu, "dgu", rows, 2 * cols, dh.dtype)
-    with _On(dh.device, stream) as s:
+    _same_device(dev, ck_gate, ck_up, dgu)
+    ld_d = 2 * cols if dgu is None else _matrix(dgu, "dgu", rows, 2 * cols, dt)
+    code = _DTYPE[dt]
+    with _on(dev, stream):
         if dgu is None:
-            dgu = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dh.device)
-        h = torch.empty((rows, cols), dtype=dh.dtype, device=dh.device) if recompute else None
+            dgu = _empty((rows, 2 * cols), dtype=dt, device=dev)
+        h = _empty((rows, cols), dtype=dt, device=dev) if recompute else None
         p = dgu.data_ptr()
-        _call("ns_gated_backward", dh.data_ptr(), ld, ck_gate.q.data_ptr(), ck_gate.scales.data_ptr(),
-              ck_up.q.data_ptr(), ck_up.scales.data_ptr(), rows, cols, p, p + cols * dgu.element_size(),
-              _matrix(dgu, "dgu"), h.data_ptr() if recompute else None, cols, _DTYPE[dh.dtype], s)
+        _call("ns_gated_backward", dh.data_ptr(), ld, ck_gate._p_q, ck_gate._p_scales, ck_up._p_q, ck_up._p_scales,
+              rows, cols, p, p + cols * (2 if code else 4), ld_d, h.data_ptr() if recompute else None, cols, code,
+              _raw_stream(dev.index))
     return dgu, h
 
 
@@ -351,27 +393,31 @@ def checkpoint_wgrad(dy, ck: Checkpoint8, offsets=None, grad=None, accumulate: b
     matrices are what muon_update_batched takes."""
     ld = _matrix(dy, "dy", ck.rows)
     rows, n_out = dy.shape
-    _same_device(dy.device, ck, offsets, grad)
+    dev, dt = dy.device, dy.dtype
+    _same_device(dev, ck, offsets, grad)
     groups = 1
     p_off = None
     if offsets is not None:
         groups = offsets.shape[0] - 1
         if groups < 0:
             raise ValueError("offsets must have at least one entry")
-        p_off = _vector(offsets, "offsets", groups + 1, (torch.int32,), dy.device)
+        p_off = _vector(offsets, "offsets", groups + 1, (torch.int32,), dev)
     if grad is None:
         if accumulate:
             raise ValueError("accumulate needs grad")
-        if dtype is not None and dtype not in _DTYPE:
+        if dtype is None:
+            dtype = dt
+        elif dtype not in _DTYPE:
             raise TypeError(f"unsupported dtype {dtype}: use float32 or bfloat16")
     else:
         if grad.shape != (groups, n_out, ck.cols) or not grad.is_contiguous():
             raise ValueError(f"grad must be contiguous, {groups} x {n_out} x {ck.cols}")
         if grad.dtype not in _DTYPE or (dtype is not None and grad.dtype != dtype):
             raise TypeError(f"grad: unsupported dtype {grad.dtype}")
-    with _On(dy.device, stream) as s:
+        dtype = grad.dtype
+    with _on(dev, stream):
         if grad is None:
-            grad = torch.empty((groups, n_out, ck.cols), dtype=dtype or dy.dtype, device=dy.device)
-        _call("ns_ckpt_wgrad", dy.data_ptr(), ld, rows, n_out, ck.q.data_ptr(), ck.scales.data_ptr(), ck.cols, p_off,
-              groups, grad.data_ptr(), _DTYPE[dy.dtype], _DTYPE[grad.dtype], 1 if accumulate else 0, s)
+            grad = _empty((groups, n_out, ck.cols), dtype=dtype, device=dev)
+        _call("ns_ckpt_wgrad", dy.data_ptr(), ld, rows, n_out, ck._p_q, ck._p_scales, ck.cols, p_off, groups,
+              grad.data_ptr(), _DTYPE[dt], _DTYPE[dtype], 1 if accumulate else 0, _raw_stream(dev.index))
     return grad
