@@ -2,17 +2,24 @@
 // loss with a KL term, with the gradient of the logits (include/ns.h).
 //
 // Per row, with m the largest logit, k = inv_temperature * log2(e) and s = sum
-// of 2^((v - m) k) over the row's logits v: logp = ((v[y] - m) k - log2 s) /
-// log2(e). The difference comes before the factor, so logits up to the type's
-// largest and lowest values do not overflow. Each thread keeps a running
-// maximum and sum; they are merged over the CTA (or over the cluster, where
-// few rows leave SMs idle) in a fixed order.
+// of 2^(v k - m k) over the row's logits v: logp = (v[y] k - m k - log2 s) /
+// log2(e). A row's gradient depends on nothing but the row, so it follows at
+// once: softmax times the row's coefficient.
 //
-// A row's gradient depends on nothing but the row, so the second pass
-// (softmax times the row's coefficient) follows at once. It is the memory
-// that bounds this: one read and one write of the logits. The second read
-// comes from L2 as long as the rows in flight fit there.
-// The loss is summed over the rows by one CTA in a fixed order.
+// One CTA per row (a cluster of up to 8 where few rows leave SMs idle), in two
+// passes. What bounds this is one read and one write of the logits: the
+// second read comes from L2, since no more rows are in flight than fit there.
+// That leaves the instructions per element: packed maxima and pairs of fp32
+// operations, about 4 a pass. (Measured at 8192 x 131072 bf16, a quarter of
+// the rows masked: 17 instructions an element, 800 us; the row held in the
+// registers of 8 CTAs, one read, but a cluster barrier a row: 1160 us.)
+//
+// Packs of 16 bytes sit on 16-byte boundaries whatever a row's own alignment
+// is; the ragged ends go element by element, and so does a gradient whose
+// rows lie differently on those boundaries than the logits'. All sums run in
+// a fixed order that depends on the logits' shape and alignment alone, so log
+// probabilities are the same bits with and without a gradient; the loss is
+// summed over the rows by one CTA.
 #include <algorithm>
 #include <cmath>
 
@@ -33,12 +40,14 @@ struct PolicyParams {
   int vocab;
   float inv_temp, clip_low, clip_high, kl_coef;
   int cluster;  // CTAs per row
+  int packed;   // the gradient's rows take the packs that the logits' rows are read in
   int *status;
 };
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLargest = 3.402823466e38f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -46,90 +55,206 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// The largest logit m so far and s = sum of 2^((v - m) k); m = -inf, s = 0 is nothing.
+// Factor and offset with which a logit v becomes the exponent v k - m k. Where
+// m k overflows, distinct logits of that size differ by more than 2^100 in the
+// exponent, and by more than 2^35 with k's power of two times 2^-64, which does
+// not overflow and whose products are exact: the powers are 0 or 1 either way.
+// m = -inf: nothing but -inf so far, whose powers are 0.
+struct Scale {
+  float k, mk;
+  bool plain;
+  __device__ __forceinline__ Scale(float m, float factor) {
+    mk = __fmul_rn(m, factor);
+    plain = fabsf(mk) <= kLargest;
+    k = factor;
+    if (!plain) {
+      k = __uint_as_float(__float_as_uint(factor) & 0x7f800000u) * 5.421010862427522e-20f;
+      mk = m == -INFINITY ? 0.f : __fmul_rn(m, k);
+    }
+  }
+  __device__ __forceinline__ float power(float v) const { return exp2_fast(fmaf(v, k, -mk)); }
+};
+
+// The largest logit m so far and s = sum of the powers relative to it; m = -inf, s = 0 is nothing.
 struct MaxSum {
   float m, s;
 };
+// (Products and sums that a compiler may contract one way here and another
+// way there are written out, so that every instance of the kernel rounds alike.)
+// What a sum relative to `from` is multiplied by to be relative to m >= from.
+__device__ __forceinline__ float rebase(float from, float m, float k) {
+  if (from == m) return 1.f;
+  const float mk = __fmul_rn(m, k);
+  return fabsf(mk) <= kLargest ? exp2_fast(fmaf(from, k, -mk)) : 0.f;
+}
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return MaxSum{m, a.s + b.s};  // nothing yet (or NaN sums, kept)
-  return MaxSum{m, a.s * exp2_fast((a.m - m) * k) + b.s * exp2_fast((b.m - m) * k)};
+  return MaxSum{m, fmaf(a.s, rebase(a.m, m, k), __fmul_rn(b.s, rebase(b.m, m, k)))};
 }
 
+struct RowInputs {
+  float old_logp, ref_logp, advantage, weight;
+};
 struct RowResult {
   float logp, kl, loss, slope;
 };
 
-// The row's outputs from its target's log probability.
-__device__ __forceinline__ RowResult policy_row(const PolicyParams &p, int64_t t, float logp) {
-  RowResult r{logp, 0.f, 0.f, 0.f};
+__device__ __forceinline__ RowInputs row_inputs(const PolicyParams &p, int64_t t) {
+  RowInputs r{0.f, 0.f, 0.f, 0.f};
   if (!p.weight) return r;
-  const float adv = p.advantage[t], w = p.weight[t];
-  const float ratio = p.old_logp ? expf(logp - p.old_logp[t]) : 1.f;
-  const float a = ratio * adv, b = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * adv;
-  float slope = a <= b ? -a : 0.f;
-  if (p.ref_logp) {
-    const float d = p.ref_logp[t] - logp, e = expm1f(d);
-    r.kl = e - d;
-    slope -= p.kl_coef * e;
-  }
-  r.loss = w * (p.kl_coef * r.kl - fminf(a, b));
-  r.slope = w * slope * p.inv_temp;
+  r.weight = p.weight[t];
+  r.advantage = p.advantage[t];
+  if (p.old_logp) r.old_logp = p.old_logp[t];
+  if (p.ref_logp) r.ref_logp = p.ref_logp[t];
   return r;
 }
 
-// Largest of a pack's values.
-template <int DT, int VEC>
-__device__ __forceinline__ float pack_max(const Pack<DT, VEC> &v) {
-  if constexpr (DT == kBF16 && VEC == 8) {  // two at a time; NaN is passed over here and reaches the sum
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(v.w);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-  } else {
-    float m = v.get(0);
-#pragma unroll
-    for (int e = 1; e < VEC; ++e) m = fmaxf(m, v.get(e));
-    return m;
+// The row's outputs from its target's log probability.
+__device__ __forceinline__ RowResult policy_row(const PolicyParams &p, const RowInputs &in, float logp) {
+  RowResult r{logp, 0.f, 0.f, 0.f};
+  if (!p.weight) return r;
+  const float ratio = p.old_logp ? expf(logp - in.old_logp) : 1.f;
+  const float a = ratio * in.advantage, b = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * in.advantage;
+  float slope = a <= b ? -a : 0.f;
+  if (p.ref_logp) {
+    const float d = in.ref_logp - logp, e = expm1f(d);
+    r.kl = e - d;
+    slope -= p.kl_coef * e;
+  }
+  r.loss = in.weight * (p.kl_coef * r.kl - fminf(a, b));
+  r.slope = in.weight * slope * p.inv_temp;
+  return r;
+}
+
+// Writes a row's scalars.
+__device__ __forceinline__ void write_result(const PolicyParams &p, int64_t t, const RowResult &r) {
+  if (in_bounds(p.logp + t, 4, p.logp, p.rows * 4, p.status)) p.logp[t] = r.logp;
+  if (p.weight) {
+    if (in_bounds(p.kl + t, 4, p.kl, p.rows * 4, p.status)) p.kl[t] = r.kl;
+    p.row_loss[t] = r.loss;
   }
 }
 
-// One row per cluster of p.cluster CTAs (1: no cluster); CTA rank r takes
-// every p.cluster-th stretch of the row.
-template <int DT, int VEC, bool GRAD>
-__global__ void __launch_bounds__(kMaxThreads) ns_policy_kernel(const __grid_constant__ PolicyParams p) {
-  using P = Pack<DT, VEC>;
-  using E = typename P::E;
+// 16 bytes of a row.
+template <int DT>
+struct RowPack {
+  static constexpr int VEC = DT == kBF16 ? 8 : 4;
+  using E = typename Elem<DT>::T;
+  Pack<DT, VEC> v;
+  // its i-th pair of values
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(v.w);
+    if constexpr (DT == kBF16)
+      return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ void set_pair(int i, float2 x) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(v.w);
+    if constexpr (DT == kBF16) {
+      const __nv_bfloat162 b = __float22bfloat162_rn(x);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+      w[2 * i] = __float_as_uint(x.x);
+      w[2 * i + 1] = __float_as_uint(x.y);
+    }
+  }
+  // largest value; NaN is passed over here and reaches the sum
+  __device__ __forceinline__ float top() const {
+    if constexpr (DT == kBF16) {
+      const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(v.w);
+      const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      return fmaxf(fmaxf(v.get(0), v.get(1)), fmaxf(v.get(2), v.get(3)));
+    }
+  }
+  __device__ __forceinline__ float2 powers(int i, const Scale &f) const {
+    const float2 x = __ffma2_rn(pair(i), make_float2(f.k, f.k), make_float2(-f.mk, -f.mk));
+    return make_float2(exp2_fast(x.x), exp2_fast(x.y));
+  }
+};
+
+// A row as its packs: `count` of them, the first starting `phase` elements
+// before the row. Packs [full0, full1) lie in it whole; the one before and
+// the one after, if any, are its ragged ends.
+struct RowPacks {
+  int phase, full0, full1;
+  template <int DT>
+  static __device__ __forceinline__ RowPacks of(const void *row, int vocab) {
+    constexpr int VEC = RowPack<DT>::VEC;
+    RowPacks r;
+    r.phase = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / (16 / VEC));
+    r.full0 = r.phase ? 1 : 0;
+    r.full1 = (vocab + r.phase) / VEC;  // may be below full0: a row inside one pack
+    return r;
+  }
+};
+
+constexpr int kAhead = 4;  // packs in flight per thread
+
+template <int DT, bool GRAD>
+__global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_constant__ PolicyParams p) {
+  using RP = RowPack<DT>;
+  using E = typename RP::E;
+  constexpr int VEC = RP::VEC;
   __shared__ MaxSum part[kMaxThreads / 32];
   __shared__ MaxSum mine;  // this CTA's share of the row, read by the cluster
   __shared__ MaxSum all;
   __shared__ RowResult res;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int first = (rank * blockDim.x + threadIdx.x) * VEC, stride = p.cluster * blockDim.x * VEC;
+  const int first = rank * blockDim.x + threadIdx.x, stride = p.cluster * blockDim.x;
   const float k = p.inv_temp * kLog2e;
   const size_t dsize = static_cast<size_t>((p.rows - 1) * p.ld_d + p.vocab) * sizeof(E);
   for (int64_t t = blockIdx.x / p.cluster; t < p.rows; t += gridDim.x / p.cluster) {
     const E *x = static_cast<const E *>(p.logits) + t * p.ld;
-    E *g = GRAD ? static_cast<E *>(p.dlogits) + t * p.ld_d : nullptr;
+    const RowPacks packs = RowPacks::of<DT>(x, p.vocab);
+    const E *base = x - packs.phase;  // pack j is base + j * VEC
+    // the two ragged ends, at most VEC - 1 elements each: thread 0's and thread 1's
+    int edge0 = 0, edge1 = 0;
+    if (first == 0) {
+      edge1 = min(p.vocab, packs.full0 * VEC - packs.phase);
+    } else if (first == 1) {
+      edge0 = max(packs.full1 * VEC - packs.phase, min(p.vocab, packs.full0 * VEC - packs.phase));
+      edge1 = p.vocab;
+    }
     const int y = p.targets.get(t);
     bool live = y >= 0 && (!p.weight || p.weight[t] != 0.f);  // the same in every thread of the cluster
     MaxSum a{-INFINITY, 0.f};
     if (live) {
-#pragma unroll 4
-      for (int c = first; c < p.vocab; c += stride) {
-        P v;
-        v.load(x + c);
-        const float top = pack_max<DT, VEC>(v);
-        if (top > a.m) {
-          a.s *= exp2_fast((a.m - top) * k);
-          a.m = top;
-        }
-        // a pack of -inf alone adds 2^(-inf - 0) = 0; NaN reaches the sum either way
-        const float m = a.m == -INFINITY ? 0.f : a.m;
-        float s = 0.f;
+      RowInputs in;
+      float target = 0.f;
+      if (threadIdx.x == 0) {  // asked for now, needed after the reduction
+        in = row_inputs(p, t);
+        target = Elem<DT>::to_f(x[y]);
+      }
+      Scale f(-INFINITY, k);
+      auto raise = [&](float top) {  // a new largest logit
+        a.s = __fmul_rn(a.s, rebase(a.m, top, k));
+        a.m = top;
+        f = Scale(top, k);
+      };
+      for (int j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride) {
+        RP v[kAhead];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += exp2_fast((v.get(e) - m) * k);
-        a.s += s;
+        for (int u = 0; u < kAhead; ++u)
+          if (j0 + u * stride < packs.full1) v[u].v.load(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (j0 + u * stride >= packs.full1) break;
+          const float top = v[u].top();
+          if (top > a.m) raise(top);
+          float2 s = v[u].powers(0, f);
+#pragma unroll
+          for (int i = 1; i < VEC / 2; ++i) s = __fadd2_rn(s, v[u].powers(i, f));
+          a.s = __fadd_rn(a.s, __fadd_rn(s.x, s.y));
+        }
+      }
+      for (int c = edge0; c < edge1; ++c) {
+        const float v = Elem<DT>::to_f(x[c]);
+        if (v > a.m) raise(v);
+        a.s = __fadd_rn(a.s, f.power(v));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
@@ -139,20 +264,19 @@ __global__ void __launch_bounds__(kMaxThreads) ns_policy_kernel(const __grid_con
       if (warp == 0) {
         a = lane < warps ? part[lane] : MaxSum{-INFINITY, 0.f};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = kMaxThreads / 64; o > 0; o >>= 1)
           a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
         if (lane == 0) mine = a;
       }
       if (p.cluster > 1) {
         cluster_sync();
         if (warp == 0) {
-          MaxSum b{-INFINITY, 0.f};
+          a = MaxSum{-INFINITY, 0.f};
           if (lane < p.cluster) {
             const uint32_t at = mapa_shared(smem_u32(&mine), lane);
-            b.m = __uint_as_float(ld_shared_cluster_u32(at));
-            b.s = __uint_as_float(ld_shared_cluster_u32(at + 4));
+            a.m = __uint_as_float(ld_shared_cluster_u32(at));
+            a.s = __uint_as_float(ld_shared_cluster_u32(at + 4));
           }
-          a = b;
 #pragma unroll
           for (int o = kMaxCluster / 2; o > 0; o >>= 1)
             a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
@@ -161,46 +285,76 @@ __global__ void __launch_bounds__(kMaxThreads) ns_policy_kernel(const __grid_con
       if (threadIdx.x == 0) {
         all = a;
         RowResult r{0.f, 0.f, 0.f, 0.f};
-        if (a.s != 0.f)  // else every logit is -inf: no distribution
-          r = policy_row(p, t, ((Elem<DT>::to_f(x[y]) - a.m) * k - log2f(a.s)) * kLn2);
+        if (a.s != 0.f) {  // else every logit is -inf: no distribution
+          const Scale f(a.m, k);
+          const float z = f.plain ? fmaf(target, k, -f.mk) : (target - a.m) * k;
+          r = policy_row(p, in, (z - log2f(a.s)) * kLn2);
+        }
         res = r;
+        if (rank == 0) write_result(p, t, r);
       }
       __syncthreads();
       a = all;
       if (a.s == 0.f) live = false;
-    }
-    if (threadIdx.x == 0 && rank == 0) {
-      const RowResult r = live ? res : RowResult{0.f, 0.f, 0.f, 0.f};
-      if (in_bounds(p.logp + t, 4, p.logp, p.rows * 4, p.status)) p.logp[t] = r.logp;
-      if (p.weight) {
-        if (in_bounds(p.kl + t, 4, p.kl, p.rows * 4, p.status)) p.kl[t] = r.kl;
-        p.row_loss[t] = r.loss;
-      }
+    } else if (threadIdx.x == 0 && rank == 0) {
+      write_result(p, t, RowResult{0.f, 0.f, 0.f, 0.f});
     }
     if constexpr (GRAD) {
+      E *g = static_cast<E *>(p.dlogits) + t * p.ld_d;
+      E *gbase = g - packs.phase;
+      // in place, every CTA has read the target's logit before any overwrites it
+      if (live && p.cluster > 1 && p.dlogits == p.logits) cluster_sync();
+      const float slope = live ? res.slope : 0.f, scale = live ? -slope / a.s : 0.f;
+      const Scale f(a.m, k);
+      auto put = [&](int j, const RP &v) {
+        if (p.packed) {
+          v.v.store_stream(gbase + static_cast<int64_t>(j) * VEC, p.dlogits, dsize, p.status);
+        } else {
+          E *to = gbase + static_cast<int64_t>(j) * VEC;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (in_bounds(to + e, sizeof(E), p.dlogits, dsize, p.status)) to[e] = reinterpret_cast<const E *>(v.v.w)[e];
+        }
+      };
+      auto put_one = [&](int c, float v) {
+        if (in_bounds(g + c, sizeof(E), p.dlogits, dsize, p.status)) g[c] = Elem<DT>::from_f(v);
+      };
       if (live) {
-        const float slope = res.slope, scale = -slope / a.s;
-        const bool in_place = p.dlogits == p.logits;
-        // in place, the target's logit is read by every CTA before any overwrites it
-        if (p.cluster > 1 && in_place) cluster_sync();
-#pragma unroll 4
-        for (int c = first; c < p.vocab; c += stride) {
-          P v;
-          v.load_stream(x + c);
+        const float2 scale2 = make_float2(scale, scale);
+        const int target_pack = (y + packs.phase) / VEC;
+        for (int j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride) {
+          RP v[kAhead];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v.set(e, scale * exp2_fast((v.get(e) - a.m) * k));
-          if (static_cast<unsigned>(y - c) < VEC) {  // the target's pack, again with its 1
+          for (int u = 0; u < kAhead; ++u)
+            if (j0 + u * stride < packs.full1) v[u].v.load_stream(base + static_cast<int64_t>(j0 + u * stride) * VEC);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (c + e == y) v.set(e, fmaf(scale, exp2_fast((Elem<DT>::to_f(x[y]) - a.m) * k), slope));
+          for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u * stride;
+            if (j >= packs.full1) break;
+            if (j != target_pack) {
+#pragma unroll
+              for (int i = 0; i < VEC / 2; ++i) v[u].set_pair(i, __fmul2_rn(scale2, v[u].powers(i, f)));
+            } else {
+              const int at = y + packs.phase - j * VEC;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float d = scale * f.power(v[u].v.get(e));
+                v[u].v.set(e, e == at ? d + slope : d);
+              }
+            }
+            put(j, v[u]);
           }
-          v.store_stream(g + c, p.dlogits, dsize, p.status);
+        }
+        for (int c = edge0; c < edge1; ++c) {
+          const float d = scale * f.power(Elem<DT>::to_f(x[c]));
+          put_one(c, c == y ? d + slope : d);
         }
       } else {
-        P v;
+        RP v;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v.set(e, 0.f);
-        for (int c = first; c < p.vocab; c += stride) v.store_stream(g + c, p.dlogits, dsize, p.status);
+        for (int i = 0; i < VEC / 2; ++i) v.set_pair(i, make_float2(0.f, 0.f));
+        for (int j = packs.full0 + first; j < packs.full1; j += stride) put(j, v);
+        for (int c = edge0; c < edge1; ++c) put_one(c, 0.f);
       }
     }
     // shared values are free for the next row (in a cluster: once all have read `mine`)
@@ -226,69 +380,67 @@ __global__ void __launch_bounds__(1024) ns_policy_sum_kernel(const __grid_consta
   }
 }
 
-template <int DT, int VEC, bool GRAD>
-int run_policy(PolicyParams p, int sms, cudaStream_t s) {
-  if (p.rows > 0) {
-    constexpr int elt = DT == kBF16 ? 2 : 4;
-    // threads: two packs or more each, down to a warp
-    int threads = kMaxThreads;
-    while (threads > 32 && static_cast<int64_t>(threads) * 2 * VEC > p.vocab) threads /= 2;
-    // few rows: a cluster of CTAs per row while SMs are idle and every thread keeps two packs
-    p.cluster = 1;
-    while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= sms &&
-           static_cast<int64_t>(threads) * p.cluster * 4 * VEC <= p.vocab)
-      p.cluster *= 2;
-    // as many CTAs as are resident, but no more rows in flight than L2 keeps
-    // for the second read (kL2Rows bytes) unless that leaves SMs idle
-    constexpr int64_t kL2Rows = int64_t(80) << 20;
-    int64_t grid = static_cast<int64_t>(sms) * (2048 / threads);
-    if (GRAD) grid = std::min(grid, std::max<int64_t>(sms, kL2Rows / std::max<int64_t>(1, static_cast<int64_t>(p.vocab) * elt)));
-    grid = std::min(grid, p.rows * p.cluster) / p.cluster * p.cluster;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, ns_policy_kernel<DT, VEC, GRAD>, p) != cudaSuccess) {
-      cudaGetLastError();
-      return -1;
-    }
-    count_launch();
+template <int DT, bool GRAD>
+int run_rows(PolicyParams p, int sms, cudaStream_t s) {
+  constexpr int elt = DT == kBF16 ? 2 : 4, VEC = 16 / elt;
+  p.packed = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) % 16 == 0) &&
+             (p.ld_d - p.ld) * elt % 16 == 0;
+  // threads: kAhead packs each where the row has them, down to a warp
+  int threads = kMaxThreads;
+  while (threads > 32 && static_cast<int64_t>(threads) * kAhead * VEC > p.vocab) threads /= 2;
+  // few rows: a cluster of CTAs per row while SMs are idle and threads keep kAhead packs
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= sms &&
+         static_cast<int64_t>(threads) * p.cluster * 2 * kAhead * VEC <= p.vocab)
+    p.cluster *= 2;
+  // as many CTAs as are resident, but with a gradient no more rows in flight
+  // than L2 keeps for the second read, unless that leaves SMs idle
+  constexpr int64_t kL2Rows = int64_t(80) << 20;
+  int64_t grid = static_cast<int64_t>(sms) * 2 * (kMaxThreads / threads);
+  if (GRAD) grid = std::min(grid, std::max<int64_t>(sms, kL2Rows / (static_cast<int64_t>(p.vocab) * elt + 1)));
+  grid = std::max<int64_t>(1, std::min(grid / p.cluster, p.rows)) * p.cluster;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, ns_policy_kernel<DT, GRAD>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
   }
-  if (p.weight) {
-    ns_policy_sum_kernel<<<1, 1024, 0, s>>>(p);
-    count_launch();
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  count_launch();
+  return 0;
 }
 
-template <int DT, int VEC>
+template <int DT>
 int run_policy(const PolicyParams &p, int sms, cudaStream_t s) {
-  return p.dlogits ? run_policy<DT, VEC, true>(p, sms, s) : run_policy<DT, VEC, false>(p, sms, s);
+  int rc = 0;
+  if (p.rows > 0) rc = p.dlogits ? run_rows<DT, true>(p, sms, s) : run_rows<DT, false>(p, sms, s);
+  if (rc == 0 && p.weight) {
+    ns_policy_sum_kernel<<<1, 1024, 0, s>>>(p);
+    count_launch();
+    rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
+  }
+  return rc;
 }
 
 int policy_call(PolicyParams &p, int dtype, void *stream) {
   OpCall call(stream);
   if (call.rc) return call.rc;
   p.status = call.status;
-  const int elt = dtype == NS_BF16 ? 2 : 4;
   if (p.weight) {
     uint8_t *ws = nullptr;
     if (const int rc = call.workspace(kSlotPolicy, static_cast<size_t>(p.rows) * 4, &ws)) return rc;
     p.row_loss = reinterpret_cast<float *>(ws);
   }
-  const int vec = 16 / elt;
-  const bool wide = p.vocab % vec == 0 && rows_aligned(p.logits, p.ld, elt, vec) &&
-                    (!p.dlogits || rows_aligned(p.dlogits, p.ld_d, elt, vec));
   return call.launch(kOpPolicy, [&] {
-    if (dtype == NS_BF16) return wide ? run_policy<kBF16, 8>(p, call.sms, call.s) : run_policy<kBF16, 1>(p, call.sms, call.s);
-    return wide ? run_policy<kF32, 4>(p, call.sms, call.s) : run_policy<kF32, 1>(p, call.sms, call.s);
+    return dtype == NS_BF16 ? run_policy<kBF16>(p, call.sms, call.s) : run_policy<kF32>(p, call.sms, call.s);
   });
 }
 
