@@ -7,12 +7,16 @@
 // once: softmax times the row's coefficient.
 //
 // One CTA per row (a cluster of up to 8 where few rows leave SMs idle), in two
-// passes. What bounds this is one read and one write of the logits: the
-// second read comes from L2, since no more rows are in flight than fit there.
-// That leaves the instructions per element: packed maxima and pairs of fp32
-// operations, about 4 a pass. (Measured at 8192 x 131072 bf16, a quarter of
-// the rows masked: 17 instructions an element, 800 us; the row held in the
-// registers of 8 CTAs, one read, but a cluster barrier a row: 1160 us.)
+// passes. What bounds this is one read and one write of the logits: between
+// the passes a row stays in shared memory as far as that goes (110 KB a CTA,
+// two CTAs an SM) and in L2 beyond. That leaves the instructions per element:
+// packed maxima and pairs of fp32 operations. Measured at 8192 x 131072 bf16
+// with a quarter of the rows masked: 665 us, 85 % of the copy bandwidth (565
+// us). On the way there: separate fp32 operations 800 us; CTAs that walk over
+// the rows in a fixed stride 754 us, because masked rows are cheap and leave
+// some CTAs with more work, where the block scheduler hands rows out as CTAs
+// finish; and a row held in the registers of 8 CTAs, 1160 us, a cluster
+// barrier a row.
 //
 // Packs of 16 bytes sit on 16-byte boundaries whatever a row's own alignment
 // is; the ragged ends go element by element, and so does a gradient whose
@@ -40,12 +44,14 @@ struct PolicyParams {
   int vocab;
   float inv_temp, clip_low, clip_high, kl_coef;
   int cluster;  // CTAs per row
+  int kept;     // packs per thread that stay in shared memory between the passes
   int packed;   // the gradient's rows take the packs that the logits' rows are read in
   int *status;
 };
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxCluster = 8;
+constexpr int64_t kKeepBytes = 216 * 1024;  // shared memory of an SM for rows kept between the passes
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kLargest = 3.402823466e38f;
 
@@ -198,6 +204,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
   using RP = RowPack<DT>;
   using E = typename RP::E;
   constexpr int VEC = RP::VEC;
+  extern __shared__ uint4 keep[];  // [pack][thread]
   __shared__ MaxSum part[kMaxThreads / 32];
   __shared__ MaxSum mine;  // this CTA's share of the row, read by the cluster
   __shared__ MaxSum all;
@@ -207,162 +214,164 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
   const int first = rank * blockDim.x + threadIdx.x, stride = p.cluster * blockDim.x;
   const float k = p.inv_temp * kLog2e;
   const size_t dsize = static_cast<size_t>((p.rows - 1) * p.ld_d + p.vocab) * sizeof(E);
-  for (int64_t t = blockIdx.x / p.cluster; t < p.rows; t += gridDim.x / p.cluster) {
-    const E *x = static_cast<const E *>(p.logits) + t * p.ld;
-    const RowPacks packs = RowPacks::of<DT>(x, p.vocab);
-    const E *base = x - packs.phase;  // pack j is base + j * VEC
-    // the two ragged ends, at most VEC - 1 elements each: thread 0's and thread 1's
-    int edge0 = 0, edge1 = 0;
-    if (first == 0) {
-      edge1 = min(p.vocab, packs.full0 * VEC - packs.phase);
-    } else if (first == 1) {
-      edge0 = max(packs.full1 * VEC - packs.phase, min(p.vocab, packs.full0 * VEC - packs.phase));
-      edge1 = p.vocab;
+  const int64_t t = blockIdx.x / p.cluster;
+  const E *x = static_cast<const E *>(p.logits) + t * p.ld;
+  const RowPacks packs = RowPacks::of<DT>(x, p.vocab);
+  const E *base = x - packs.phase;  // pack j is base + j * VEC
+  // the two ragged ends, at most VEC - 1 elements each: thread 0's and thread 1's
+  int edge0 = 0, edge1 = 0;
+  if (first == 0) {
+    edge1 = min(p.vocab, packs.full0 * VEC - packs.phase);
+  } else if (first == 1) {
+    edge0 = max(packs.full1 * VEC - packs.phase, min(p.vocab, packs.full0 * VEC - packs.phase));
+    edge1 = p.vocab;
+  }
+  const int y = p.targets.get(t);
+  bool live = y >= 0 && (!p.weight || p.weight[t] != 0.f);  // the same in every thread of the cluster
+  MaxSum a{-INFINITY, 0.f};
+  if (live) {
+    RowInputs in;
+    float target = 0.f;
+    if (threadIdx.x == 0) {  // asked for now, needed after the reduction
+      in = row_inputs(p, t);
+      target = Elem<DT>::to_f(x[y]);
     }
-    const int y = p.targets.get(t);
-    bool live = y >= 0 && (!p.weight || p.weight[t] != 0.f);  // the same in every thread of the cluster
-    MaxSum a{-INFINITY, 0.f};
-    if (live) {
-      RowInputs in;
-      float target = 0.f;
-      if (threadIdx.x == 0) {  // asked for now, needed after the reduction
-        in = row_inputs(p, t);
-        target = Elem<DT>::to_f(x[y]);
+    Scale f(-INFINITY, k);
+    auto raise = [&](float top) {  // a new largest logit
+      a.s = __fmul_rn(a.s, rebase(a.m, top, k));
+      a.m = top;
+      f = Scale(top, k);
+    };
+    for (int n = 0, j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride, n += kAhead) {
+      RP v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j0 + u * stride < packs.full1) v[u].v.load(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (j0 + u * stride >= packs.full1) break;
+        if (GRAD && n < p.kept) keep[(n + u) * blockDim.x + threadIdx.x] = v[u].v.w[0];
+        const float top = v[u].top();
+        if (top > a.m) raise(top);
+        float2 s = v[u].powers(0, f);
+#pragma unroll
+        for (int i = 1; i < VEC / 2; ++i) s = __fadd2_rn(s, v[u].powers(i, f));
+        a.s = __fadd_rn(a.s, __fadd_rn(s.x, s.y));
       }
-      Scale f(-INFINITY, k);
-      auto raise = [&](float top) {  // a new largest logit
-        a.s = __fmul_rn(a.s, rebase(a.m, top, k));
-        a.m = top;
-        f = Scale(top, k);
-      };
-      for (int j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride) {
-        RP v[kAhead];
+    }
+    for (int c = edge0; c < edge1; ++c) {
+      const float v = Elem<DT>::to_f(x[c]);
+      if (v > a.m) raise(v);
+      a.s = __fadd_rn(a.s, f.power(v));
+    }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (j0 + u * stride < packs.full1) v[u].v.load(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+    for (int o = 16; o > 0; o >>= 1)
+      a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
+    if (lane == 0) part[warp] = a;
+    __syncthreads();
+    if (warp == 0) {
+      a = lane < warps ? part[lane] : MaxSum{-INFINITY, 0.f};
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (j0 + u * stride >= packs.full1) break;
-          const float top = v[u].top();
-          if (top > a.m) raise(top);
-          float2 s = v[u].powers(0, f);
-#pragma unroll
-          for (int i = 1; i < VEC / 2; ++i) s = __fadd2_rn(s, v[u].powers(i, f));
-          a.s = __fadd_rn(a.s, __fadd_rn(s.x, s.y));
-        }
-      }
-      for (int c = edge0; c < edge1; ++c) {
-        const float v = Elem<DT>::to_f(x[c]);
-        if (v > a.m) raise(v);
-        a.s = __fadd_rn(a.s, f.power(v));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
+      for (int o = kMaxThreads / 64; o > 0; o >>= 1)
         a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
-      if (lane == 0) part[warp] = a;
-      __syncthreads();
-      if (warp == 0) {
-        a = lane < warps ? part[lane] : MaxSum{-INFINITY, 0.f};
-#pragma unroll
-        for (int o = kMaxThreads / 64; o > 0; o >>= 1)
-          a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
-        if (lane == 0) mine = a;
-      }
-      if (p.cluster > 1) {
-        cluster_sync();
-        if (warp == 0) {
-          a = MaxSum{-INFINITY, 0.f};
-          if (lane < p.cluster) {
-            const uint32_t at = mapa_shared(smem_u32(&mine), lane);
-            a.m = __uint_as_float(ld_shared_cluster_u32(at));
-            a.s = __uint_as_float(ld_shared_cluster_u32(at + 4));
-          }
-#pragma unroll
-          for (int o = kMaxCluster / 2; o > 0; o >>= 1)
-            a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
-        }
-      }
-      if (threadIdx.x == 0) {
-        all = a;
-        RowResult r{0.f, 0.f, 0.f, 0.f};
-        if (a.s != 0.f) {  // else every logit is -inf: no distribution
-          const Scale f(a.m, k);
-          const float z = f.plain ? fmaf(target, k, -f.mk) : (target - a.m) * k;
-          r = policy_row(p, in, (z - log2f(a.s)) * kLn2);
-        }
-        res = r;
-        if (rank == 0) write_result(p, t, r);
-      }
-      __syncthreads();
-      a = all;
-      if (a.s == 0.f) live = false;
-    } else if (threadIdx.x == 0 && rank == 0) {
-      write_result(p, t, RowResult{0.f, 0.f, 0.f, 0.f});
+      if (lane == 0) mine = a;
     }
-    if constexpr (GRAD) {
-      E *g = static_cast<E *>(p.dlogits) + t * p.ld_d;
-      E *gbase = g - packs.phase;
-      // in place, every CTA has read the target's logit before any overwrites it
-      if (live && p.cluster > 1 && p.dlogits == p.logits) cluster_sync();
-      const float slope = live ? res.slope : 0.f, scale = live ? -slope / a.s : 0.f;
-      const Scale f(a.m, k);
-      auto put = [&](int j, const RP &v) {
-        if (p.packed) {
-          v.v.store_stream(gbase + static_cast<int64_t>(j) * VEC, p.dlogits, dsize, p.status);
-        } else {
-          E *to = gbase + static_cast<int64_t>(j) * VEC;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (in_bounds(to + e, sizeof(E), p.dlogits, dsize, p.status)) to[e] = reinterpret_cast<const E *>(v.v.w)[e];
+    if (p.cluster > 1) {
+      cluster_sync();
+      if (warp == 0) {
+        a = MaxSum{-INFINITY, 0.f};
+        if (lane < p.cluster) {
+          const uint32_t at = mapa_shared(smem_u32(&mine), lane);
+          a.m = __uint_as_float(ld_shared_cluster_u32(at));
+          a.s = __uint_as_float(ld_shared_cluster_u32(at + 4));
         }
-      };
-      auto put_one = [&](int c, float v) {
-        if (in_bounds(g + c, sizeof(E), p.dlogits, dsize, p.status)) g[c] = Elem<DT>::from_f(v);
-      };
-      if (live) {
-        const float2 scale2 = make_float2(scale, scale);
-        const int target_pack = (y + packs.phase) / VEC;
-        for (int j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride) {
-          RP v[kAhead];
+#pragma unroll
+        for (int o = kMaxCluster / 2; o > 0; o >>= 1)
+          a = merge(a, MaxSum{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, k);
+      }
+    }
+    if (threadIdx.x == 0) {
+      all = a;
+      RowResult r{0.f, 0.f, 0.f, 0.f};
+      if (a.s != 0.f) {  // else every logit is -inf: no distribution
+        const Scale f(a.m, k);
+        const float z = f.plain ? fmaf(target, k, -f.mk) : (target - a.m) * k;
+        r = policy_row(p, in, (z - log2f(a.s)) * kLn2);
+      }
+      res = r;
+      if (rank == 0) write_result(p, t, r);
+    }
+    __syncthreads();
+    a = all;
+    if (a.s == 0.f) live = false;
+  } else if (threadIdx.x == 0 && rank == 0) {
+    write_result(p, t, RowResult{0.f, 0.f, 0.f, 0.f});
+  }
+  if constexpr (GRAD) {
+    E *g = static_cast<E *>(p.dlogits) + t * p.ld_d;
+    E *gbase = g - packs.phase;
+    // in place, every CTA has read the target's logit before any overwrites it
+    if (live && p.cluster > 1 && p.dlogits == p.logits) cluster_sync();
+    const float slope = live ? res.slope : 0.f, scale = live ? -slope / a.s : 0.f;
+    const Scale f(a.m, k);
+    auto put = [&](int j, const RP &v) {
+      if (p.packed) {
+        v.v.store_stream(gbase + static_cast<int64_t>(j) * VEC, p.dlogits, dsize, p.status);
+      } else {
+        E *to = gbase + static_cast<int64_t>(j) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (in_bounds(to + e, sizeof(E), p.dlogits, dsize, p.status)) to[e] = reinterpret_cast<const E *>(v.v.w)[e];
+      }
+    };
+    auto put_one = [&](int c, float v) {
+      if (in_bounds(g + c, sizeof(E), p.dlogits, dsize, p.status)) g[c] = Elem<DT>::from_f(v);
+    };
+    if (live) {
+      const float2 scale2 = make_float2(scale, scale);
+      const int target_pack = (y + packs.phase) / VEC;
+      for (int n = 0, j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride, n += kAhead) {
+        RP v[kAhead];
+        if (n < p.kept) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (j0 + u * stride < packs.full1) v[u].v.w[0] = keep[(n + u) * blockDim.x + threadIdx.x];
+        } else {
 #pragma unroll
           for (int u = 0; u < kAhead; ++u)
             if (j0 + u * stride < packs.full1) v[u].v.load_stream(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+        }
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            const int j = j0 + u * stride;
-            if (j >= packs.full1) break;
-            if (j != target_pack) {
+        for (int u = 0; u < kAhead; ++u) {
+          const int j = j0 + u * stride;
+          if (j >= packs.full1) break;
+          if (j != target_pack) {
 #pragma unroll
-              for (int i = 0; i < VEC / 2; ++i) v[u].set_pair(i, __fmul2_rn(scale2, v[u].powers(i, f)));
-            } else {
-              const int at = y + packs.phase - j * VEC;
+            for (int i = 0; i < VEC / 2; ++i) v[u].set_pair(i, __fmul2_rn(scale2, v[u].powers(i, f)));
+          } else {
+            const int at = y + packs.phase - j * VEC;
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                const float d = scale * f.power(v[u].v.get(e));
-                v[u].v.set(e, e == at ? d + slope : d);
-              }
+            for (int e = 0; e < VEC; ++e) {
+              const float d = scale * f.power(v[u].v.get(e));
+              v[u].v.set(e, e == at ? d + slope : d);
             }
-            put(j, v[u]);
           }
+          put(j, v[u]);
         }
-        for (int c = edge0; c < edge1; ++c) {
-          const float d = scale * f.power(Elem<DT>::to_f(x[c]));
-          put_one(c, c == y ? d + slope : d);
-        }
-      } else {
-        RP v;
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) v.set_pair(i, make_float2(0.f, 0.f));
-        for (int j = packs.full0 + first; j < packs.full1; j += stride) put(j, v);
-        for (int c = edge0; c < edge1; ++c) put_one(c, 0.f);
       }
+      for (int c = edge0; c < edge1; ++c) {
+        const float d = scale * f.power(Elem<DT>::to_f(x[c]));
+        put_one(c, c == y ? d + slope : d);
+      }
+    } else {
+      RP v;
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) v.set_pair(i, make_float2(0.f, 0.f));
+      for (int j = packs.full0 + first; j < packs.full1; j += stride) put(j, v);
+      for (int c = edge0; c < edge1; ++c) put_one(c, 0.f);
     }
-    // shared values are free for the next row (in a cluster: once all have read `mine`)
-    if (p.cluster > 1)
-      cluster_sync();
-    else
-      __syncthreads();
   }
+  if (p.cluster > 1) cluster_sync();  // no CTA leaves while another may read its share
 }
 
 // loss = sum of the rows' losses: one CTA, each thread a fixed stride, then a
@@ -385,31 +394,39 @@ int run_rows(PolicyParams p, int sms, cudaStream_t s) {
   constexpr int elt = DT == kBF16 ? 2 : 4, VEC = 16 / elt;
   p.packed = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) % 16 == 0) &&
              (p.ld_d - p.ld) * elt % 16 == 0;
-  // threads: kAhead packs each where the row has them, down to a warp
+  // Threads: 16 packs each where the row has them, down to a warp; fewer, and
+  // so more rows at a time on an SM, beat more threads a row (8192 x 32000
+  // bf16: 205 us, 225 with 8 packs each, 260 with 4).
   int threads = kMaxThreads;
-  while (threads > 32 && static_cast<int64_t>(threads) * kAhead * VEC > p.vocab) threads /= 2;
+  while (threads > 32 && static_cast<int64_t>(threads) * 4 * kAhead * VEC > p.vocab) threads /= 2;
   // few rows: a cluster of CTAs per row while SMs are idle and threads keep kAhead packs
   p.cluster = 1;
   while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= sms &&
          static_cast<int64_t>(threads) * p.cluster * 2 * kAhead * VEC <= p.vocab)
     p.cluster *= 2;
-  // as many CTAs as are resident, but with a gradient no more rows in flight
-  // than L2 keeps for the second read, unless that leaves SMs idle
-  constexpr int64_t kL2Rows = int64_t(80) << 20;
-  int64_t grid = static_cast<int64_t>(sms) * 2 * (kMaxThreads / threads);
-  if (GRAD) grid = std::min(grid, std::max<int64_t>(sms, kL2Rows / (static_cast<int64_t>(p.vocab) * elt + 1)));
-  grid = std::max<int64_t>(1, std::min(grid / p.cluster, p.rows)) * p.cluster;
+  // shared memory for what is read twice: the row's packs, or an equal share of the SM
+  int smem = 0;
+  if (GRAD) {
+    const int64_t step = static_cast<int64_t>(threads) * 16 * kAhead;  // bytes of kAhead packs of every thread
+    const int64_t row = (static_cast<int64_t>(p.vocab) * elt / p.cluster + step - 1) / step * step;
+    const int64_t share = kKeepBytes * threads / (2 * kMaxThreads) / step * step;
+    smem = static_cast<int>(std::min(row, share));
+    p.kept = static_cast<int>(smem / step) * kAhead;
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows * p.cluster), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  static SmemOptIn opt_in;
+  if (smem > 0 && opt_in.ensure(reinterpret_cast<const void *>(ns_policy_kernel<DT, GRAD>), smem)) return -1;
   if (cudaLaunchKernelEx(&cfg, ns_policy_kernel<DT, GRAD>, p) != cudaSuccess) {
     cudaGetLastError();
     return -1;
