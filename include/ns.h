@@ -221,7 +221,7 @@ int ns_embed_lookup(const void *table, int64_t ld_table, int64_t vocab, int64_t 
  *   NS_BF16, whatever dtype is).
  * Sums run in fp32 over the positions in a fixed order and are rounded once.
  * Ids outside [0, vocab) have no gradient; their rows of dOut are not read.
- * count <= 2^30, vocab < 2^31 - 1, count * dim below 2^43.
+ * count <= 2^30, vocab < 2^31 - 1, dim <= 2^24, count * dim below 2^43.
  */
 int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids, int id_type, int64_t count, float scale,
                   void *grad, int64_t ld_grad, int64_t vocab, int64_t dim, int dtype, int grad_dtype, int accumulate,

@@ -3,17 +3,23 @@
 //
 // The gradient is a sum over positions grouped by token id. Atomic adds into
 // the table would make the sums depend on the schedule (and serialise on the
-// few very frequent ids of real text), so the positions are sorted by id
-// first, stably, and each id's rows are added in the order of their
-// positions:
-//   sort      one cluster of 8 CTAs, a stable radix sort of (id, position);
-//             padding ids sort to the end;
-//   segments  the sorted list in fixed pieces of kSeg positions, one piece and
-//             column range per CTA, whatever the ids are: a run of equal ids
-//             inside a piece is written to the table, the parts of a run
-//             that crosses piece borders go to scratch as fp32 sums;
-//   joins     adds the parts of each crossing run in piece order;
-//   zeros     (not accumulating) the rows no id points to.
+// few very frequent ids of real text), so each id's rows are added in the
+// order of their positions.
+//   few positions (kDirect): one launch. A CTA per position and column range
+//     finds the positions with the same id in the list itself; the first of
+//     them adds them all.
+//   else: sort      one cluster of 8 CTAs, a stable radix sort of (id,
+//                   position); padding ids sort to the end;
+//         segments  the sorted list in fixed pieces of kSeg positions, one
+//                   piece and column range per CTA, whatever the ids are: a
+//                   run of equal ids inside a piece is written to the table,
+//                   the parts of a run that crosses piece borders go to
+//                   scratch as fp32 sums;
+//         joins     adds the parts of each crossing run in piece order.
+// Not accumulating, the rows that no id points to are cleared by the other
+// CTAs of the first launch, which find them from the ids directly (a bitmap of
+// their rows): most of the bytes of a large vocabulary, written while the sort
+// (25 us for 32768 ids) runs beside them.
 #include <algorithm>
 
 #include "../../include/ns.h"
@@ -70,6 +76,56 @@ __global__ void __launch_bounds__(256) ns_embed_lookup_kernel(const __grid_const
   }
 }
 
+// ------------------------------------------------------------------ absent rows
+struct ZeroParams {
+  Ids ids;
+  int n;
+  uint8_t *grad;
+  int64_t ld_bytes;
+  int row_bytes;
+  size_t size;
+  int *status;
+};
+
+constexpr int kZeroRows = 16384;  // rows of a bitmap
+struct Bitmap {
+  uint32_t w[kZeroRows / 32];
+};
+
+// The calling CTA, `part` of `parts`, clears those rows of its share of the
+// table that no id points to.
+__device__ __forceinline__ void zero_absent(const ZeroParams &p, Bitmap &seen, int part, int parts) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t vocab = p.ids.vocab;
+  const int64_t r0 = vocab * part / parts, r1 = vocab * (part + 1) / parts;
+  for (int64_t a = r0; a < r1; a += kZeroRows) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), r1 - a));
+    for (int i = threadIdx.x; i < kZeroRows / 32; i += blockDim.x) seen.w[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
+      const int64_t d = p.ids.get(i) - a;
+      if (d >= 0 && d < rows) atomicOr(&seen.w[d >> 5], 1u << (d & 31));
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += warps) {
+      if ((seen.w[r >> 5] >> (r & 31)) & 1u) continue;
+      // 2- or 4-byte elements up to a 16-byte boundary, whole 16-byte words, the rest
+      uint8_t *row = p.grad + (a + r) * p.ld_bytes, *end = row + p.row_bytes;
+      uint8_t *lo = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(row) + 15) & ~uintptr_t(15));
+      uint8_t *hi = reinterpret_cast<uint8_t *>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+      if (lo > hi) lo = hi = end;
+      for (uint8_t *at = lo + lane * 16; at < hi; at += 512)
+        if (in_bounds(at, 16, p.grad, p.size, p.status)) __stcs(reinterpret_cast<uint4 *>(at), make_uint4(0, 0, 0, 0));
+      for (uint8_t *at = row + lane * 2; at < lo; at += 64)
+        if (in_bounds(at, 2, p.grad, p.size, p.status)) *reinterpret_cast<uint16_t *>(at) = 0;
+      for (uint8_t *at = hi + lane * 2; at < end; at += 64)
+        if (in_bounds(at, 2, p.grad, p.size, p.status)) *reinterpret_cast<uint16_t *>(at) = 0;
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------ sort
 constexpr int kSortCluster = 8;
 constexpr int kSortThreads = 1024;
@@ -92,7 +148,14 @@ struct SortParams {
 // gives each CTA where its keys of each digit go; then the share is ranked
 // tile by tile: within a warp by matching digits, across warps by a prefix
 // over the warps' counts, so equal digits keep their order.
-__global__ void __launch_bounds__(kSortThreads) ns_embed_sort_kernel(const __grid_constant__ SortParams p) {
+// The clusters behind the first one clear the absent rows.
+__global__ void __launch_bounds__(kSortThreads)
+    ns_embed_sort_kernel(const __grid_constant__ SortParams p, const __grid_constant__ ZeroParams zero) {
+  if (blockIdx.x >= kSortCluster) {
+    __shared__ Bitmap seen;
+    zero_absent(zero, seen, blockIdx.x - kSortCluster, gridDim.x - kSortCluster);
+    return;
+  }
   __shared__ int hist[kSortBins];
   __shared__ int base[kSortBins];
   __shared__ int wsum[kSortWarps];
@@ -194,9 +257,10 @@ __global__ void __launch_bounds__(kSortThreads) ns_embed_sort_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ segment sums
-constexpr int kSeg = 32;         // sorted positions per piece
+constexpr int kSeg = 64;         // sorted positions per piece (32: joins of a frequent id take 6 us more at 32768 ids)
 constexpr int kSegThreads = 128;
 constexpr int kSegAhead = 8;     // rows in flight per thread
+constexpr int kJoinAhead = 16;   // parts in flight per thread
 
 struct GradParams {
   const void *dout;
@@ -286,54 +350,102 @@ __global__ void __launch_bounds__(kSegThreads) ns_embed_joins_kernel(const __gri
   const int id = p.keys[last];
   if (id >= p.vocab || p.keys[last + 1] != id) return;              // nothing leaves
   if (b > 0 && p.keys[b * kSeg] == id && p.keys[b * kSeg - 1] == id) return;  // began earlier
+  // pieces b + 1 .. q begin with it: the CTA looks at kSegThreads of them at a time
+  int q = b;
+  for (int more = kSegThreads; more == kSegThreads;) {
+    const int64_t i = static_cast<int64_t>(q + 1 + static_cast<int>(threadIdx.x)) * kSeg;
+    more = __syncthreads_count(i < p.n && p.keys[i] == id);
+    q += more;
+  }
   const int c = ((blockIdx.x - b * p.chunks) * kSegThreads + threadIdx.x) * VEC;
   if (c >= p.dim) return;
-  // pieces b + 1 .. q hold it: q is where its last position lies
-  int lo = last + 1, hi = p.n;  // keys[lo] == id; hi: the first known not to be
-  while (lo + 1 < hi) {
-    const int m = lo + (hi - lo) / 2;
-    if (p.keys[m] == id) lo = m; else hi = m;
-  }
-  const int q = lo / kSeg;
   const float *parts = p.parts + static_cast<int64_t>(b) * 2 * p.dim_pad + c;
   float sum[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sum[e] = parts[p.dim_pad + e];
-  for (int k = b + 1; k <= q; ++k) {
-    parts += 2 * p.dim_pad;
+  for (int k0 = b + 1; k0 <= q; k0 += kJoinAhead) {
+    float v[kJoinAhead][VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[e] += parts[e];
+    for (int k = 0; k < kJoinAhead; ++k) {
+      const float *at = parts + static_cast<int64_t>(min(k0 + k, q) - b) * 2 * p.dim_pad;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[k][e] = at[e];  // parts are 16-byte aligned: one access
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k)
+      if (k0 + k <= q) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] += v[k][e];
+      }
   }
   write_row<GT, VEC>(p, id, c, sum);
 }
 
-// Rows without an id: a warp looks its 32 rows up in the sorted keys, a lane
-// each, and clears those that are absent.
-template <int GT, int VEC>
-__global__ void __launch_bounds__(256) ns_embed_zeros_kernel(const __grid_constant__ GradParams p) {
-  using P = Pack<GT, VEC>;
+// ------------------------------------------------------------------ few positions
+constexpr int kDirect = 1024;  // positions at most (the words of a list of matches are one per lane)
+
+// CTAs [0, n * chunks): position t and a column range. The first position of
+// an id adds the rows of all its positions; the list of them is a bitmap, so
+// they come in order. The CTAs behind clear the absent rows.
+template <int DT, int GT, int VEC>
+__global__ void __launch_bounds__(kSegThreads)
+    ns_embed_direct_kernel(const __grid_constant__ GradParams p, const __grid_constant__ ZeroParams zero) {
+  using P = Pack<DT, VEC>;
   using E = typename P::E;
-  const int lane = threadIdx.x & 31;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 32;
-  if (r0 >= p.vocab) return;
-  const int row = static_cast<int>(r0) + lane;
-  int a = 0, b = p.n;
-  while (a < b) {
-    const int m = (a + b) >> 1;
-    if (p.keys[m] < row) a = m + 1; else b = m;
+  const int work = p.n * p.chunks;
+  if (blockIdx.x >= work) {
+    __shared__ Bitmap seen;
+    zero_absent(zero, seen, blockIdx.x - work, gridDim.x - work);
+    return;
   }
-  const bool absent = row < p.vocab && (a >= p.n || p.keys[a] != row);
-  uint32_t todo = __ballot_sync(0xffffffffu, absent);
-  P z;
+  __shared__ uint32_t match[kDirect / 32];
+  const int t = blockIdx.x / p.chunks, chunk = blockIdx.x - t * p.chunks;
+  const int id = zero.ids.get(t);
+  if (id < 0) return;
+  bool earlier = false;
+  for (int i = threadIdx.x; i < kDirect; i += kSegThreads) {  // whole warps, a word each
+    const bool same = i < p.n && zero.ids.get(i) == id;
+    const uint32_t word = __ballot_sync(0xffffffffu, same);
+    if ((threadIdx.x & 31) == 0) match[i >> 5] = word;
+    earlier |= same && i < t;
+  }
+  if (__syncthreads_or(earlier)) return;
+  const int c = (chunk * kSegThreads + threadIdx.x) * VEC;
+  if (c >= p.dim) return;
+  float sum[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) z.set(e, 0.f);
-  const size_t size = static_cast<size_t>((p.vocab - 1) * p.ld_grad + p.dim) * sizeof(E);
-  while (todo) {
-    const int k = __ffs(todo) - 1;
-    todo &= todo - 1;
-    E *g = static_cast<E *>(p.grad) + (r0 + k) * p.ld_grad;
-    for (int c = lane * VEC; c < p.dim; c += 32 * VEC) z.store(g + c, p.grad, size, p.status);
+  for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
+  const E *src = static_cast<const E *>(p.dout) + c;
+  int word = t >> 5;
+  uint32_t left = match[word];
+  const int words = (p.n + 31) >> 5;
+  auto next = [&] {  // the next position with this id, -1 behind the last
+    while (left == 0) {
+      if (++word >= words) return -1;
+      left = match[word];
+    }
+    const int i = (word << 5) + __ffs(left) - 1;
+    left &= left - 1;
+    return i;
+  };
+  for (int i = next(); i >= 0;) {
+    P v[kSegAhead];
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < kSegAhead; ++k)
+      if (i >= 0) {
+        v[k].load_stream(src + static_cast<int64_t>(i) * p.ld_dout);
+        ++count;
+        i = next();
+      }
+#pragma unroll
+    for (int k = 0; k < kSegAhead; ++k)
+      if (k < count) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] += v[k].get(e);
+      }
   }
+  write_row<GT, VEC>(p, id, c, sum);
 }
 
 template <int DT, int VEC>
@@ -346,19 +458,32 @@ int run_lookup(const LookupParams &p, int sms, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-int run_sort(const SortParams &p, cudaStream_t s) {
+int run_sort(const SortParams &p, const ZeroParams &zero, bool clear, int dev, int sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kSortCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(kSortCluster, 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, ns_embed_sort_kernel, p) != cudaSuccess) {
+  int clusters = 1;
+  if (clear) {  // as many clusters as are resident at once: every one looks through the ids first
+    static int resident[64] = {};
+    int &n = resident[dev & 63];
+    if (n == 0) {
+      cfg.gridDim = dim3(sms / kSortCluster * kSortCluster, 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&n, ns_embed_sort_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+    }
+    clusters = std::max(2, n);
+  }
+  cfg.gridDim = dim3(kSortCluster * clusters, 1, 1);
+  if (cudaLaunchKernelEx(&cfg, ns_embed_sort_kernel, p, zero) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -367,22 +492,34 @@ int run_sort(const SortParams &p, cudaStream_t s) {
 }
 
 template <int DT, int GT, int VEC>
-int run_grad(const GradParams &p, cudaStream_t s) {
-  const int per = kSegThreads * VEC;
-  GradParams q = p;
-  q.chunks = (p.dim + per - 1) / per;
-  if (static_cast<int64_t>(p.pieces) * q.chunks > INT32_MAX) return -1;
-  if (p.n > 0) {
-    ns_embed_segments_kernel<DT, GT, VEC><<<p.pieces * q.chunks, kSegThreads, 0, s>>>(q);
-    count_launch();
-    ns_embed_joins_kernel<GT, VEC><<<p.pieces * q.chunks, kSegThreads, 0, s>>>(q);
-    count_launch();
-  }
-  if (!p.accumulate) {
-    ns_embed_zeros_kernel<GT, VEC><<<static_cast<int>((p.vocab + 255ll) / 256), 256, 0, s>>>(p);
-    count_launch();
-  }
+int run_direct(const GradParams &p, const ZeroParams &zero, int sms, cudaStream_t s) {
+  // the rows to clear: one CTA each for 64 KB, four per SM at most
+  const int64_t clear = p.accumulate ? 0 : (static_cast<int64_t>(p.vocab) * zero.row_bytes + 65535) / 65536;
+  const int64_t grid = static_cast<int64_t>(p.n) * p.chunks + std::min<int64_t>(clear, sms * 4);
+  ns_embed_direct_kernel<DT, GT, VEC><<<static_cast<int>(grid), kSegThreads, 0, s>>>(p, zero);
+  count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int DT, int GT, int VEC>
+int run_segments(const GradParams &p, cudaStream_t s) {
+  ns_embed_segments_kernel<DT, GT, VEC><<<p.pieces * p.chunks, kSegThreads, 0, s>>>(p);
+  count_launch();
+  constexpr int kJoin = VEC == 1 ? 1 : 4;  // a 16-byte word of the fp32 parts
+  GradParams j = p;
+  j.chunks = (p.dim + kSegThreads * kJoin - 1) / (kSegThreads * kJoin);
+  ns_embed_joins_kernel<GT, kJoin><<<p.pieces * j.chunks, kSegThreads, 0, s>>>(j);
+  count_launch();
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int DT, int GT>
+int run_grad(GradParams p, const ZeroParams &zero, bool wide, int sms, cudaStream_t s) {
+  constexpr int VEC = DT == kBF16 ? 8 : 4;
+  const int per = kSegThreads * (wide ? VEC : 1);
+  p.chunks = (p.dim + per - 1) / per;
+  if (p.n <= kDirect) return wide ? run_direct<DT, GT, VEC>(p, zero, sms, s) : run_direct<DT, GT, 1>(p, zero, sms, s);
+  return wide ? run_segments<DT, GT, VEC>(p, s) : run_segments<DT, GT, 1>(p, s);
 }
 
 }  // namespace
@@ -423,7 +560,7 @@ extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids,
       (id_type != NS_I32 && id_type != NS_I64) || (accumulate != 0 && accumulate != 1))
     return NS_EINVAL;
   if (bad_shape(vocab, dim, ld_grad) || bad_shape(count, dim, ld_dout) || vocab >= INT32_MAX) return NS_EINVAL;
-  if (count > (1 << 30) || (count / kSeg + 1) * (dim / kSegThreads + 1) > INT32_MAX) return NS_EINVAL;
+  if (count > (1 << 30) || dim > (1 << 24) || (count / kSeg + 1) * (dim / kSegThreads + 1) > INT32_MAX) return NS_EINVAL;
   if (vocab == 0 || dim == 0 || (count == 0 && accumulate)) return NS_OK;
   if (!grad || (count > 0 && (!ids || !dout))) return NS_EINVAL;
   const int elt = dtype == NS_BF16 ? 2 : 4, gelt = grad_dtype == NS_BF16 ? 2 : 4;
@@ -448,35 +585,38 @@ extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids,
   p.scale = scale;
   p.accumulate = accumulate;
   p.status = call.status;
-  const size_t list = (static_cast<size_t>(n) * 4 + 255) / 256 * 256;
-  uint8_t *ws = nullptr;
-  int rc = call.workspace(kSlotEmbed, 4 * list + static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, &ws);
-  if (rc) return rc;
-  SortParams sp{};
-  sp.ids = Ids{ids, id_type == NS_I64, p.vocab};
-  sp.n = n;
-  for (int k = 0; k < 2; ++k) {
-    sp.keys[k] = reinterpret_cast<int *>(ws + 2 * k * list);
-    sp.pos[k] = reinterpret_cast<int *>(ws + (2 * k + 1) * list);
+  const Ids list_ids{ids, id_type == NS_I64, p.vocab};
+  const ZeroParams zero{list_ids, n, static_cast<uint8_t *>(grad), ld_grad * gelt, static_cast<int>(dim * gelt),
+                        static_cast<size_t>((vocab - 1) * ld_grad + dim) * gelt, call.status};
+  if (n > kDirect) {
+    const size_t list = (static_cast<size_t>(n) * 4 + 255) / 256 * 256;
+    uint8_t *ws = nullptr;
+    int rc = call.workspace(kSlotEmbed, 4 * list + static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, &ws);
+    if (rc) return rc;
+    SortParams sp{};
+    sp.ids = list_ids;
+    sp.n = n;
+    for (int k = 0; k < 2; ++k) {
+      sp.keys[k] = reinterpret_cast<int *>(ws + 2 * k * list);
+      sp.pos[k] = reinterpret_cast<int *>(ws + (2 * k + 1) * list);
+    }
+    int bits = 1;
+    while (bits < 31 && (vocab >> bits)) ++bits;  // keys are 0 .. vocab
+    sp.passes = (bits + 8) / 9;
+    sp.bits = (bits + sp.passes - 1) / sp.passes;
+    sp.status = call.status;
+    p.keys = sp.keys[0];
+    p.pos = sp.pos[0];
+    p.parts = reinterpret_cast<float *>(ws + 4 * list);
+    if ((rc = call.launch(kOpSort, [&] { return run_sort(sp, zero, !accumulate, call.dev, call.sms, call.s); }))) return rc;
   }
-  int bits = 1;
-  while (bits < 31 && (vocab >> bits)) ++bits;  // keys are 0 .. vocab
-  sp.passes = (bits + 8) / 9;
-  sp.bits = (bits + sp.passes - 1) / sp.passes;
-  sp.status = call.status;
-  p.keys = sp.keys[0];
-  p.pos = sp.pos[0];
-  p.parts = reinterpret_cast<float *>(ws + 4 * list);
-  if (n > 0 && (rc = call.launch(kOpSort, [&] { return run_sort(sp, call.s); }))) return rc;
   const int vec = 16 / elt;
   const bool wide = dim % vec == 0 && rows_aligned(dout, ld_dout, elt, vec) && rows_aligned(grad, ld_grad, gelt, vec);
   return call.launch(kOpEmbedGrad, [&] {
-    if (dtype == NS_BF16) {
-      if (grad_dtype == NS_BF16)
-        return wide ? run_grad<kBF16, kBF16, 8>(p, call.s) : run_grad<kBF16, kBF16, 1>(p, call.s);
-      return wide ? run_grad<kBF16, kF32, 8>(p, call.s) : run_grad<kBF16, kF32, 1>(p, call.s);
-    }
-    if (grad_dtype == NS_BF16) return wide ? run_grad<kF32, kBF16, 4>(p, call.s) : run_grad<kF32, kBF16, 1>(p, call.s);
-    return wide ? run_grad<kF32, kF32, 4>(p, call.s) : run_grad<kF32, kF32, 1>(p, call.s);
+    if (dtype == NS_BF16)
+      return grad_dtype == NS_BF16 ? run_grad<kBF16, kBF16>(p, zero, wide, call.sms, call.s)
+                                   : run_grad<kBF16, kF32>(p, zero, wide, call.sms, call.s);
+    return grad_dtype == NS_BF16 ? run_grad<kF32, kBF16>(p, zero, wide, call.sms, call.s)
+                                 : run_grad<kF32, kF32>(p, zero, wide, call.sms, call.s);
   });
 }
