@@ -899,8 +899,9 @@ OpCall::~OpCall() {
   if (ranged) nvtxRangePop();
 }
 
-int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr) {
+int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr, bool *fresh) {
   CachedWs &c = g_ws[WsKey{dev, s, slot}];
+  if (fresh) *fresh = !(c.ptr && c.bytes >= std::max<size_t>(bytes, 256));
   const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s);
   *ptr = c.ptr;
   return e;

@@ -2,8 +2,8 @@
 // loss with a KL term, with the gradient of the logits (include/ns.h).
 //
 // Per row, with m the largest logit, k = inv_temperature * log2(e) and s = sum
-// of 2^(v k - m k) over the row's logits v: logp = (v[y] k - m k - log2 s) /
-// log2(e). A row's gradient depends on nothing but the row, so it follows at
+// of 2^(v k - m k) over the row's logits v: logp = (v[y] - m) inv_temperature -
+// log s, corrected by what rounding m k left out. A row's gradient depends on nothing but the row, so it follows at
 // once: softmax times the row's coefficient.
 //
 // One CTA per row (a cluster of up to 8 where few rows leave SMs idle), in two
@@ -22,8 +22,9 @@
 // is; the ragged ends go element by element, and so does a gradient whose
 // rows lie differently on those boundaries than the logits'. All sums run in
 // a fixed order that depends on the logits' shape and alignment alone, so log
-// probabilities are the same bits with and without a gradient; the loss is
-// summed over the rows by one CTA.
+// probabilities are the same bits with and without a gradient. The loss is
+// summed over the rows, in a fixed order, by the CTA that finishes last, or by
+// a launch of its own where that CTA would be long at it.
 #include <algorithm>
 #include <cmath>
 
@@ -45,6 +46,7 @@ struct PolicyParams {
   float inv_temp, clip_low, clip_high, kl_coef;
   int cluster;  // CTAs per row
   int kept;     // packs per thread that stay in shared memory between the passes
+  int *done;    // rows finished, 0 between calls; nullptr: the loss is summed by ns_policy_sum_kernel
   int packed;   // the gradient's rows take the packs that the logits' rows are read in
   int *status;
 };
@@ -91,7 +93,7 @@ struct MaxSum {
 __device__ __forceinline__ float rebase(float from, float m, float k) {
   if (from == m) return 1.f;
   const float mk = __fmul_rn(m, k);
-  return fabsf(mk) <= kLargest ? exp2_fast(fmaf(from, k, -mk)) : 0.f;
+  return fabsf(mk) <= kLargest ? exp2_fast(__fmul_rn(from, k) - mk) : 0.f;  // both offsets as rounded
 }
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m);
@@ -139,6 +141,20 @@ __device__ __forceinline__ void write_result(const PolicyParams &p, int64_t t, c
     if (in_bounds(p.kl + t, 4, p.kl, p.rows * 4, p.status)) p.kl[t] = r.kl;
     p.row_loss[t] = r.loss;
   }
+}
+
+// Sum of the rows' losses by the calling CTA, in thread 0: each thread a
+// fixed stride, then a fixed tree. part: a float per warp.
+__device__ __forceinline__ float sum_losses(const PolicyParams &p, float *part) {
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < p.rows; t += blockDim.x) s += __ldcg(p.row_loss + t);
+  s = warp_sum(s);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = threadIdx.x < blockDim.x >> 5 ? part[threadIdx.x] : 0.f;
+  return threadIdx.x < 32 ? warp_sum(s) : 0.f;
 }
 
 // 16 bytes of a row.
@@ -295,8 +311,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
       RowResult r{0.f, 0.f, 0.f, 0.f};
       if (a.s != 0.f) {  // else every logit is -inf: no distribution
         const Scale f(a.m, k);
-        const float z = f.plain ? fmaf(target, k, -f.mk) : (target - a.m) * k;
-        r = policy_row(p, in, (z - log2f(a.s)) * kLn2);
+        // the powers are relative to m k as rounded
+        const float left_out = f.plain ? fmaf(a.m, k, -f.mk) : 0.f;
+        r = policy_row(p, in, fmaf(left_out, kLn2, (target - a.m) * p.inv_temp - logf(a.s)));
       }
       res = r;
       if (rank == 0) write_result(p, t, r);
@@ -372,25 +389,32 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
     }
   }
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while another may read its share
-}
-
-// loss = sum of the rows' losses: one CTA, each thread a fixed stride, then a
-// fixed tree.
-__global__ void __launch_bounds__(1024) ns_policy_sum_kernel(const __grid_constant__ PolicyParams p) {
-  __shared__ float part[32];
-  float s = 0.f;
-  for (int64_t t = threadIdx.x; t < p.rows; t += 1024) s += p.row_loss[t];
-  s = warp_sum(s);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    s = warp_sum(part[threadIdx.x]);
-    if (threadIdx.x == 0 && in_bounds(p.loss, 4, p.loss, 4, p.status)) *p.loss = s;
+  if (p.weight && p.done && rank == 0) {
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+      __threadfence();  // the row's loss before its count
+      last = atomicAdd(p.done, 1) == static_cast<int>(p.rows) - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (last) {
+      const float s = sum_losses(p, reinterpret_cast<float *>(part));
+      if (threadIdx.x == 0) {
+        if (in_bounds(p.loss, 4, p.loss, 4, p.status)) *p.loss = s;
+        *p.done = 0;
+      }
+    }
   }
 }
 
+__global__ void __launch_bounds__(1024) ns_policy_sum_kernel(const __grid_constant__ PolicyParams p) {
+  __shared__ float part[32];
+  const float s = sum_losses(p, part);
+  if (threadIdx.x == 0 && in_bounds(p.loss, 4, p.loss, 4, p.status)) *p.loss = s;
+}
+
 template <int DT, bool GRAD>
-int run_rows(PolicyParams p, int sms, cudaStream_t s) {
+int run_rows(PolicyParams p, int sms, cudaStream_t s, bool *summed) {
   constexpr int elt = DT == kBF16 ? 2 : 4, VEC = 16 / elt;
   p.packed = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) % 16 == 0) &&
              (p.ld_d - p.ld) * elt % 16 == 0;
@@ -399,6 +423,9 @@ int run_rows(PolicyParams p, int sms, cudaStream_t s) {
   // bf16: 205 us, 225 with 8 packs each, 260 with 4).
   int threads = kMaxThreads;
   while (threads > 32 && static_cast<int64_t>(threads) * 4 * kAhead * VEC > p.vocab) threads /= 2;
+  // the last CTA sums the loss if that is at most 32 rows a thread
+  if (p.rows > static_cast<int64_t>(threads) * 32) p.done = nullptr;
+  *summed = p.done != nullptr;
   // few rows: a cluster of CTAs per row while SMs are idle and threads keep kAhead packs
   p.cluster = 1;
   while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= sms &&
@@ -438,8 +465,9 @@ int run_rows(PolicyParams p, int sms, cudaStream_t s) {
 template <int DT>
 int run_policy(const PolicyParams &p, int sms, cudaStream_t s) {
   int rc = 0;
-  if (p.rows > 0) rc = p.dlogits ? run_rows<DT, true>(p, sms, s) : run_rows<DT, false>(p, sms, s);
-  if (rc == 0 && p.weight) {
+  bool summed = false;
+  if (p.rows > 0) rc = p.dlogits ? run_rows<DT, true>(p, sms, s, &summed) : run_rows<DT, false>(p, sms, s, &summed);
+  if (rc == 0 && p.weight && !summed) {
     ns_policy_sum_kernel<<<1, 1024, 0, s>>>(p);
     count_launch();
     rc = cudaGetLastError() == cudaSuccess ? 0 : -1;
@@ -453,8 +481,12 @@ int policy_call(PolicyParams &p, int dtype, void *stream) {
   p.status = call.status;
   if (p.weight) {
     uint8_t *ws = nullptr;
-    if (const int rc = call.workspace(kSlotPolicy, static_cast<size_t>(p.rows) * 4, &ws)) return rc;
-    p.row_loss = reinterpret_cast<float *>(ws);
+    // a counter that every call leaves at 0, then the rows' losses
+    bool fresh = false;
+    if (const int rc = call.workspace(kSlotPolicy, 256 + static_cast<size_t>(p.rows) * 4, &ws, &fresh)) return rc;
+    if (fresh && cudaMemsetAsync(ws, 0, 256, call.s) != cudaSuccess) return NS_ECUDA;
+    p.done = reinterpret_cast<int *>(ws);
+    p.row_loss = reinterpret_cast<float *>(ws + 256);
   }
   return call.launch(kOpPolicy, [&] {
     return dtype == NS_BF16 ? run_policy<kBF16>(p, call.sms, call.s) : run_policy<kF32>(p, call.sms, call.s);

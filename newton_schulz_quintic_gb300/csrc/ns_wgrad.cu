@@ -277,13 +277,16 @@ __device__ __forceinline__ void store_tma(const WgradParams &p, int z, int row0,
 
 // The same element by element (rows that TMA cannot address, bf16 sums that
 // are added to what is there): a store instruction covers one row's 32
-// consecutive columns.
+// consecutive columns; what is added to is read kRowsAhead rows at a time.
+template <int GT, bool ADD>
 __device__ __forceinline__ void store_plain(const WgradParams &p, int e, int row0, int col0, const float (&acc)[128],
                                             float *patch) {
+  using G = typename Elem<GT>::T;
+  constexpr int kRowsAhead = 8;
   const int lane = threadIdx.x & 31;
-  const int64_t base = static_cast<int64_t>(e) * p.n_out * p.n_in;
-  const size_t count = static_cast<size_t>(p.groups) * p.n_out * p.n_in;
+  const size_t size = static_cast<size_t>(p.groups) * p.n_out * p.n_in * sizeof(G);
   const int rows = min(32, p.n_out - row0);
+  G *to = static_cast<G *>(p.grad) + (static_cast<int64_t>(e) * p.n_out + row0) * p.n_in + col0 + lane;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     __syncwarp();
@@ -291,20 +294,23 @@ __device__ __forceinline__ void store_plain(const WgradParams &p, int e, int row
 #pragma unroll
     for (int c = 0; c < 32; ++c) patch[lane * 32 + (c ^ lane)] = acc[32 * k + c];
     __syncwarp();
-    const int col = col0 + 32 * k + lane;
-    if (col >= p.n_in) continue;
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      const float v = patch[r * 32 + (lane ^ r)];
-      const int64_t at = base + static_cast<int64_t>(row0 + r) * p.n_in + col;
-      if (p.gdtype == kF32) {
-        float *g = static_cast<float *>(p.grad) + at;
-        if (in_bounds(g, 4, p.grad, count * 4, p.status)) *g = p.accumulate ? *g + v : v;
-      } else {
-        __nv_bfloat16 *g = static_cast<__nv_bfloat16 *>(p.grad) + at;
-        if (in_bounds(g, 2, p.grad, count * 2, p.status))
-          *g = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*g) + v : v);
+    if (col0 + 32 * k + lane >= p.n_in) continue;
+    G *g = to + 32 * k;
+    for (int r0 = 0; r0 < rows; r0 += kRowsAhead) {
+      G old[kRowsAhead];
+      if (ADD) {
+#pragma unroll
+        for (int r = 0; r < kRowsAhead; ++r)
+          if (r0 + r < rows) old[r] = g[static_cast<int64_t>(r) * p.n_in];
       }
+#pragma unroll
+      for (int r = 0; r < kRowsAhead; ++r) {
+        if (r0 + r >= rows) break;
+        const float v = patch[(r0 + r) * 32 + (lane ^ (r0 + r))];
+        G *at = g + static_cast<int64_t>(r) * p.n_in;
+        if (in_bounds(at, sizeof(G), p.grad, size, p.status)) *at = Elem<GT>::from_f(ADD ? Elem<GT>::to_f(old[r]) + v : v);
+      }
+      g += static_cast<int64_t>(kRowsAhead) * p.n_in;
     }
   }
 }
@@ -523,9 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
       if (!ok) break;
       const int row0 = t.n0 + static_cast<int>(rank) * 128 + quarter * 32, col0 = t.k0 + half * 128;
       if (row0 >= p.n_out) continue;
-      if (p.store == kStorePlain)
-        store_plain(p, t.e, row0, col0, sum, reinterpret_cast<float *>(patch));
-      else if (p.splits > 1 || (p.gdtype == kF32 && p.store == kStoreTma))
+      if (p.store == kStorePlain) {
+        float *words = reinterpret_cast<float *>(patch);
+        if (p.gdtype == kF32) {
+          if (p.accumulate)
+            store_plain<kF32, true>(p, t.e, row0, col0, sum, words);
+          else
+            store_plain<kF32, false>(p, t.e, row0, col0, sum, words);
+        } else if (p.accumulate) {
+          store_plain<kBF16, true>(p, t.e, row0, col0, sum, words);
+        } else {
+          store_plain<kBF16, false>(p, t.e, row0, col0, sum, words);
+        }
+      } else if (p.splits > 1 || (p.gdtype == kF32 && p.store == kStoreTma))
         store_tma<false, false>(p, t.z, row0, col0, sum, patch);
       else if (p.store == kStoreTmaAdd)
         store_tma<true, false>(p, t.z, row0, col0, sum, patch);
