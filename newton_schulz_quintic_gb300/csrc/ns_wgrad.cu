@@ -353,6 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  // the launch before this one prepares the operands; what is above ran beside it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool tmem_ok = ld_shared_cluster_u32(mapa_shared(smem_u32(&bar->tmem_base), rank ^ 1u)) == tmem;
   if (!tmem_ok && threadIdx.x == 0) set_status(p.status, kStatusTmemMismatch);
   volatile int *abort = &bar->abort;
@@ -570,14 +572,28 @@ struct PrepareParams {
   int *status;
 };
 
+// fp32 (or bf16 that TMA cannot address) as bf16 slices: the first is the
+// value rounded, each further one what the ones before leave out.
+__device__ __forceinline__ float next_slice(float &left) {
+  __nv_bfloat16 b = __float2bfloat16_rn(left);
+  if (__hisinf(b) && !isinf(left))  // beyond bf16's largest value: that one, the rest in the next slice
+    b = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(left) >> 16));
+  const float f = __bfloat162float(b);
+  left = isinf(f) || isnan(f) ? 0.f : left - f;  // an infinity or NaN stays in the first slice alone
+  return f;
+}
+
 // X widened to bf16 (16 values per thread: its pitch is a multiple of 16),
 // and dY as TMA can address it: bf16 rows of out_pitch elements (a multiple of
-// 8, 8 per thread), one slice, or three whose sum is the fp32 value to 2^-24 of it.
-template <int DT>
+// 8), one slice, or three whose sum is the fp32 value to 2^-24 of it. A thread
+// takes 8 values of dY: consecutive ones where its rows allow 16-byte
+// accesses, else four pairs 64 apart, so that a warp's accesses stay coalesced.
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256) ns_wgrad_prepare_kernel(const __grid_constant__ PrepareParams p) {
   using E = typename Elem<DT>::T;
+  asm volatile("griddepcontrol.launch_dependents;");  // the product may set itself up meanwhile
   const int64_t per_row = p.pitch / 16, nx = p.rows * per_row;
-  const int64_t dy_row = p.out_pitch / 8, ny = p.dy ? p.rows * dy_row : 0;
+  const int64_t dy_row = WIDE ? p.out_pitch / 8 : (p.out_pitch + 255) / 256 * 32, ny = p.dy ? p.rows * dy_row : 0;
   const int64_t slice = static_cast<int64_t>(p.rows) * p.out_pitch;
   const size_t xsize = static_cast<size_t>(p.rows) * p.pitch * 2, ysize = static_cast<size_t>(slice) * p.slices * 2;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < nx + ny; i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -592,24 +608,40 @@ __global__ void __launch_bounds__(256) ns_wgrad_prepare_kernel(const __grid_cons
 #pragma unroll
       for (int u = 0; u < 16; ++u) v.set(u, static_cast<float>(q[u]) * unit);
       v.store(p.x + r * p.pitch + c, p.x, xsize, p.status);
-    } else {
-      const int64_t k = i - nx, r = k / dy_row;
-      const int c = static_cast<int>(k - r * dy_row) * 8;
-      float v[8];
+      continue;
+    }
+    const int64_t k = i - nx, r = k / dy_row;
+    const int j = static_cast<int>(k - r * dy_row);
+    const E *row = static_cast<const E *>(p.dy) + r * p.ld;
+    __nv_bfloat16 *out = p.out + r * p.out_pitch;
+    float v[8];
+    if constexpr (WIDE) {
+      Pack<DT, 8> x;
+      x.load_stream(row + j * 8);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = c + u < p.n_out ? Elem<DT>::to_f(static_cast<const E *>(p.dy)[r * p.ld + c + u]) : 0.f;
+      for (int u = 0; u < 8; ++u) v[u] = x.get(u);
       for (int z = 0; z < p.slices; ++z) {
         Pack<kBF16, 8> h;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          __nv_bfloat16 b = __float2bfloat16_rn(v[u]);
-          if (__hisinf(b) && !isinf(v[u]))  // beyond bf16's largest value: that one, the rest in the next slice
-            b = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(v[u]) >> 16));
-          const float f = __bfloat162float(b);
-          h.set(u, f);
-          v[u] = isinf(f) || isnan(f) ? 0.f : v[u] - f;  // an infinity or NaN stays in the first slice alone
+        for (int u = 0; u < 8; ++u) h.set(u, next_slice(v[u]));
+        h.store(out + z * slice + j * 8, p.out, ysize, p.status);
+      }
+    } else {
+      const int c0 = (j / 32) * 256 + (j % 32) * 2;  // pairs at c0, c0 + 64, ...
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = c0 + (u / 2) * 64 + u % 2;
+        v[u] = c < p.n_out ? Elem<DT>::to_f(row[c]) : 0.f;
+      }
+      for (int z = 0; z < p.slices; ++z) {
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+          const int c = c0 + u * 32;
+          Pack<kBF16, 2> h;
+          h.set(0, next_slice(v[u]));
+          h.set(1, next_slice(v[u + 1]));
+          if (c < p.out_pitch) h.store(out + z * slice + c, p.out, ysize, p.status);
         }
-        h.store(p.out + z * slice + r * p.out_pitch + c, p.out, ysize, p.status);
       }
     }
   }
@@ -631,12 +663,16 @@ __global__ void __launch_bounds__(256) ns_wgrad_join_kernel(const __grid_constan
 }
 
 int run_prepare(const PrepareParams &p, int dtype, int sms, cudaStream_t s) {
-  const int64_t n = static_cast<int64_t>(p.rows) * (p.pitch / 16 + (p.dy ? p.out_pitch / 8 : 0));
+  const bool wide = p.dy && p.n_out % 8 == 0 && rows_aligned(p.dy, p.ld, dtype == NS_BF16 ? 2 : 4, 8);
+  const int64_t dy_row = wide ? p.out_pitch / 8 : (p.out_pitch + 255) / 256 * 32;
+  const int64_t n = static_cast<int64_t>(p.rows) * (p.pitch / 16 + (p.dy ? dy_row : 0));
   const int grid = static_cast<int>(std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(sms) * 16));
-  if (dtype == NS_BF16)
-    ns_wgrad_prepare_kernel<kBF16><<<grid, 256, 0, s>>>(p);
+  if (dtype == NS_BF16)  // a bf16 dY with aligned rows is read as it is
+    ns_wgrad_prepare_kernel<kBF16, false><<<grid, 256, 0, s>>>(p);
+  else if (wide)
+    ns_wgrad_prepare_kernel<kF32, true><<<grid, 256, 0, s>>>(p);
   else
-    ns_wgrad_prepare_kernel<kF32><<<grid, 256, 0, s>>>(p);
+    ns_wgrad_prepare_kernel<kF32, false><<<grid, 256, 0, s>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -716,11 +752,14 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
   k.wait_limit_ns = kWaitLimitNs;
 
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // it starts while the preparation still runs and waits for it (griddepcontrol)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = call.s;
@@ -781,6 +820,7 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
       return rc;
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(pairs, k.items)), 1, 1);
+  cfg.numAttrs = rows > 0 ? 2 : 1;
   rc = call.launch(kOpWgrad, [&] {
     if (cudaLaunchKernelEx(&cfg, ns_wgrad_kernel, k) != cudaSuccess) {
       cudaGetLastError();
