@@ -8,9 +8,11 @@
 // largest magnitude by shuffles. The scale is a power of two, so quantising
 // is one fused multiply-add: x * 2^k + 1.5 * 2^23 rounds the exact product
 // half to even and leaves q in the sum's low byte. Rows whose pitch or base
-// does not allow 16-byte accesses take the narrow form: a warp's access is one
-// block, a lane holds one value of each of four blocks, which stays coalesced
-// for any pitch and alignment.
+// does not allow 16-byte accesses go through a warp's piece of shared memory:
+// element by element and coalesced on the memory's side, 8 values a lane on
+// the other (a block per warp access and a value per lane instead costs 33
+// instructions per 32 values: 57 against 45 us for fp32 4093 x 6143 stored and
+// loaded).
 #include <algorithm>
 
 #include "../../include/ns.h"
@@ -21,8 +23,7 @@ namespace ns {
 namespace {
 
 constexpr int kBlock = 32;  // values per scale
-constexpr int kWide = 8;    // consecutive values per lane where rows are aligned
-constexpr int kNarrow = 4;  // else: values per lane, one of each of as many blocks
+constexpr int kN = 8;       // consecutive values per lane
 constexpr int kThreads = 256;
 
 struct Held {  // a checkpoint
@@ -55,43 +56,51 @@ __device__ __forceinline__ void put(T *at, T v, const void *base, size_t size, i
   if (in_bounds(at, sizeof(T), base, size, status)) *at = v;
 }
 
-// A lane's values of a row as they were read: wide, kWide from column c on;
-// narrow, columns c, c + 32, ...; zeros beyond the row.
-template <int DT, bool WIDE>
+// A lane's kN values of a row, columns c..., as they were read; zeros beyond the row.
+template <int DT>
 struct Values {
-  static constexpr int kN = WIDE ? kWide : kNarrow;
   using E = typename Elem<DT>::T;
   Pack<DT, kN> v;
-  __device__ __forceinline__ void load(const E *row, int c, int cols, bool here) {
-    if constexpr (WIDE) {
-      if (here) {
-        v.load_stream(row + c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) v.set(e, 0.f);
-      }
+  // rows that allow 16-byte accesses
+  __device__ __forceinline__ void load(const E *row, int c, bool here) {
+    if (here) {
+      v.load_stream(row + c);
     } else {
 #pragma unroll
-      for (int e = 0; e < kN; ++e)
-        reinterpret_cast<E *>(v.w)[e] = here && c + e * kBlock < cols ? __ldcs(row + c + e * kBlock) : Elem<DT>::from_f(0.f);
+      for (int e = 0; e < kN; ++e) v.set(e, 0.f);
     }
+  }
+  // other rows: the warp's 32 * kN columns from c0 on, lane by lane, to be exchanged afterwards
+  __device__ __forceinline__ void load_spread(const E *row, int c0, int cols, bool row_here) {
+    const int left = row_here ? cols - c0 - static_cast<int>(threadIdx.x & 31) : 0;
+    const E *at = row + c0 + (threadIdx.x & 31);
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      reinterpret_cast<E *>(v.w)[e] = e * 32 < left ? __ldcs(at + e * 32) : Elem<DT>::from_f(0.f);
+  }
+  __device__ __forceinline__ void exchange(uint4 *stage) {
+    const int lane = threadIdx.x & 31;
+    E *s = reinterpret_cast<E *>(stage);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < kN; ++e) s[e * 32 + lane] = reinterpret_cast<const E *>(v.w)[e];
+    __syncwarp();
+    constexpr int kW = sizeof(v.w) / 16;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) reinterpret_cast<uint4 *>(v.w)[i] = stage[lane * kW + i];
   }
   // largest magnitude as float bits; NaN is the largest of all
   __device__ __forceinline__ uint32_t top() const {
     uint32_t m = 0;
     if constexpr (DT == kBF16) {
 #pragma unroll
-      for (int i = 0; i < kN / 2; ++i) m = __vmaxu2(m, word(i) & 0x7fff7fffu);  // two at a time
+      for (int i = 0; i < kN / 2; ++i) m = __vmaxu2(m, reinterpret_cast<const uint32_t *>(v.w)[i] & 0x7fff7fffu);  // two at a time
       return max(m & 0xffff0000u, m << 16);
     } else {
 #pragma unroll
       for (int i = 0; i < kN; ++i) m = max(m, __float_as_uint(v.get(i)) & 0x7fffffffu);
       return m;
     }
-  }
-  __device__ __forceinline__ uint32_t word(int i) const {
-    constexpr int kPer = sizeof(v.w[0]) / 4;
-    return reinterpret_cast<const uint32_t *>(&v.w[i / kPer])[i % kPer];
   }
 };
 
@@ -106,93 +115,75 @@ __device__ __forceinline__ uint32_t quantise_rare(float x, float up, int ex) {
 
 // Quantises a lane's values and writes them (with the padding behind the row)
 // where `row`. All lanes of the warp call it.
-template <int DT, bool WIDE>
-__device__ __forceinline__ void hold(const CkptParams &p, const Held &h, int64_t t, int c, bool row, const Values<DT, WIDE> &x) {
-  constexpr int N = Values<DT, WIDE>::kN;
+template <int DT>
+__device__ __forceinline__ void hold(const CkptParams &p, const Held &h, int64_t t, int c, bool row, const Values<DT> &x) {
   const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
-  int8_t *q = h.q + t * p.pitch + c;
-  uint8_t *s = h.s + t * p.scale_pitch + c / kBlock;
-  if constexpr (WIDE) {
-    uint32_t top = x.top();
+  uint32_t top = x.top();
 #pragma unroll
-    for (int o = 1; o < kBlock / N; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int ex = block_exponent(top);
-    const float up = up_factor(ex);
-    uint32_t b[N];
-    if (plain_block(top)) {
+  for (int o = 1; o < kBlock / kN; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int ex = block_exponent(top);
+  const float up = up_factor(ex);
+  uint32_t b[kN];
+  if (plain_block(top)) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) b[e] = quantise(x.v.get(e), up);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) b[e] = quantise_rare(x.v.get(e), up, ex);
-    }
-    if (!row) return;
-    if (c < p.pitch) {
-      auto four = [&](int i) {
-        return __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410);
-      };
-      put(reinterpret_cast<uint2 *>(q), make_uint2(four(0), four(4)), h.q, qsize, p.status);
-    }
-    if (c % kBlock == 0 && c / kBlock < p.scale_pitch) put(s, static_cast<uint8_t>(c < p.cols ? ex : 0), h.s, ssize, p.status);
+    for (int e = 0; e < kN; ++e) b[e] = quantise(x.v.get(e), up);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float v = x.v.get(e);
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
-      const int ex = block_exponent(top), col = c + e * kBlock;
-      const float up = up_factor(ex);
-      const uint32_t b = plain_block(top) ? quantise(v, up) : quantise_rare(v, up, ex);
-      if (row && col < p.pitch) put(q + e * kBlock, static_cast<int8_t>(b), h.q, qsize, p.status);
-      if (row && c % kBlock == e && col / kBlock < p.scale_pitch)  // lane e writes block e's scale
-        put(s + e, static_cast<uint8_t>(col - e < p.cols ? ex : 0), h.s, ssize, p.status);
-    }
+    for (int e = 0; e < kN; ++e) b[e] = quantise_rare(x.v.get(e), up, ex);
   }
+  if (!row) return;
+  if (c < p.pitch) {
+    auto four = [&](int i) {
+      return __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410);
+    };
+    put(reinterpret_cast<uint2 *>(h.q + t * p.pitch + c), make_uint2(four(0), four(4)), h.q, qsize, p.status);
+  }
+  if (c % kBlock == 0 && c / kBlock < p.scale_pitch)
+    put(h.s + t * p.scale_pitch + c / kBlock, static_cast<uint8_t>(c < p.cols ? ex : 0), h.s, ssize, p.status);
 }
 
-// What a checkpoint holds in a lane's columns of row t: the bytes and the scales.
-template <bool WIDE>
+// What a checkpoint holds in a lane's columns of row t: the bytes and the scale.
 struct HeldValues {
-  uint32_t w[WIDE ? 2 : 4];
-  int e[WIDE ? 1 : 4];
+  uint2 w;
+  int e;
   __device__ __forceinline__ void load(const CkptParams &p, const Held &h, int64_t t, int c) {
-    const uint8_t *s = h.s + t * p.scale_pitch + c / kBlock;
-    const int8_t *q = h.q + t * p.pitch + c;
-    if constexpr (WIDE) {
-      e[0] = __ldcs(s);
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(q));
-      w[0] = v.x;
-      w[1] = v.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kNarrow; ++i)
-        if (c + i * kBlock < p.cols) {
-          e[i] = __ldcs(s + i);
-          w[i] = static_cast<uint8_t>(__ldcs(q + i * kBlock));
-        }
-    }
+    e = __ldcs(h.s + t * p.scale_pitch + c / kBlock);
+    w = __ldcs(reinterpret_cast<const uint2 *>(h.q + t * p.pitch + c));
   }
   // the i-th value: (byte + 128) + 2^23 as a float, minus both, in units; exact
   __device__ __forceinline__ float get(int i) const {
-    const uint32_t u = WIDE ? __byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540 + i % 4) : (w[i] ^ 0x80u) | 0x4B000000u;
-    return (__uint_as_float(u) - 8388736.f) * unit_of(e[WIDE ? 0 : i]);
+    const uint32_t u = __byte_perm((i < 4 ? w.x : w.y) ^ 0x80808080u, 0x4B000000u, 0x7540 + i % 4);
+    return (__uint_as_float(u) - 8388736.f) * unit_of(e);
   }
 };
 
-template <int DT, bool WIDE, int N>
-__device__ __forceinline__ void write_row(const CkptParams &p, int which, int64_t t, int c, const float (&x)[N]) {
+// Writes a lane's values at row t, columns c..., where `here`; through `stage`
+// by the whole warp (c0: its first column) for rows without 16-byte accesses.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void write_row(const CkptParams &p, int which, int64_t t, int c, int c0, bool row, bool here,
+                                          const float (&x)[kN], uint4 *stage) {
   using E = typename Elem<DT>::T;
   E *base = static_cast<E *>(p.out[which]);
-  E *to = base + t * p.ld_out[which] + c;
+  E *to = base + t * p.ld_out[which];
   const size_t size = static_cast<size_t>((p.rows - 1) * p.ld_out[which] + p.cols) * sizeof(E);
+  Pack<DT, kN> v;
+#pragma unroll
+  for (int e = 0; e < kN; ++e) v.set(e, x[e]);
   if constexpr (WIDE) {
-    Pack<DT, N> v;
-#pragma unroll
-    for (int e = 0; e < N; ++e) v.set(e, x[e]);
-    v.store(to, base, size, p.status);
+    if (here) v.store(to + c, base, size, p.status);
   } else {
+    const int lane = threadIdx.x & 31;
+    constexpr int kW = sizeof(v.w) / 16;
+    __syncwarp();
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (c + e * kBlock < p.cols) put(to + e * kBlock, Elem<DT>::from_f(x[e]), base, size, p.status);
+    for (int i = 0; i < kW; ++i) stage[lane * kW + i] = reinterpret_cast<const uint4 *>(v.w)[i];
+    __syncwarp();
+    const E *s = reinterpret_cast<const E *>(stage) + lane;
+    const int left = row ? p.cols - c0 - lane : 0;
+    E *at = to + c0 + lane;
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (e * 32 < left) put(at + e * 32, s[e * 32], base, size, p.status);
   }
 }
 
@@ -210,60 +201,68 @@ enum Op : int { kStore, kLoad, kForward, kBackward };
 template <int OP, int DT, bool WIDE>
 __global__ void __launch_bounds__(kThreads) ns_ckpt_kernel(const __grid_constant__ CkptParams p) {
   using E = typename Elem<DT>::T;
-  constexpr int N = WIDE ? kWide : kNarrow;
-  const int lane = (blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1));
-  const int c = WIDE ? lane * N : (lane / 32) * (32 * N) + lane % 32;
+  __shared__ uint4 stages[WIDE ? 1 : kThreads / 32][WIDE ? 1 : 32 * kN * sizeof(E) / 16];
+  uint4 *stage = stages[WIDE ? 0 : threadIdx.x / 32];
+  const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * kN;
+  const int c0 = c - (threadIdx.x & 31) * kN;  // the warp's first column (one row per warp where that is used)
   const int height = kThreads >> p.lanes_log2;
   const int64_t step = static_cast<int64_t>(gridDim.y) * height;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < p.rows; t0 += step) {
     const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
     const bool row = t < p.rows, here = row && c < p.cols;
-    Values<DT, WIDE> a, b;
-    HeldValues<WIDE> ga, ub;
-    if constexpr (OP != kLoad) a.load(static_cast<const E *>(p.in[0]) + t * p.ld_in, c, p.cols, here);
-    if constexpr (OP == kForward) b.load(static_cast<const E *>(p.in[1]) + t * p.ld_in, c, p.cols, here);
+    auto read = [&](int which, Values<DT> &v) {
+      const E *x = static_cast<const E *>(p.in[which]) + t * p.ld_in;
+      if constexpr (WIDE)
+        v.load(x, c, here);
+      else
+        v.load_spread(x, c0, p.cols, row);
+    };
+    auto write = [&](int which, const float (&x)[kN]) { write_row<DT, WIDE>(p, which, t, c, c0, row, here, x, stage); };
+    Values<DT> a, b;
+    HeldValues ga, ub;
+    if constexpr (OP != kLoad) read(0, a);
+    if constexpr (OP == kForward) read(1, b);
     if constexpr (OP == kLoad || OP == kBackward)
       if (here) ga.load(p, p.held[0], t, c);
     if constexpr (OP == kBackward)
       if (here) ub.load(p, p.held[1], t, c);
+    if constexpr (!WIDE && OP != kLoad) a.exchange(stage);
+    if constexpr (!WIDE && OP == kForward) b.exchange(stage);
 
-    if constexpr (OP == kStore) hold<DT, WIDE>(p, p.held[0], t, c, row, a);
-    if constexpr (OP == kLoad) {
-      if (here) {
-        float v[N];
+    if constexpr (OP == kStore) hold<DT>(p, p.held[0], t, c, row, a);
+    const bool compute = WIDE ? here : true;  // where lanes exchange values, all of them
+    if (OP == kLoad && compute) {
+      float v[kN];
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = ga.get(e);
-        write_row<DT, WIDE>(p, 0, t, c, v);
-      }
+      for (int e = 0; e < kN; ++e) v[e] = ga.get(e);
+      write(0, v);
     }
     if constexpr (OP == kForward) {
-      if (here) {
-        float h[N];
+      if (compute) {
+        float h[kN];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
+        for (int e = 0; e < kN; ++e) {
           const float g = a.v.get(e);
           h[e] = g * sigmoid<DT>(g) * b.v.get(e);
         }
-        write_row<DT, WIDE>(p, 0, t, c, h);
+        write(0, h);
       }
-      hold<DT, WIDE>(p, p.held[0], t, c, row, a);
-      hold<DT, WIDE>(p, p.held[1], t, c, row, b);
+      hold<DT>(p, p.held[0], t, c, row, a);
+      hold<DT>(p, p.held[1], t, c, row, b);
     }
-    if constexpr (OP == kBackward) {
-      if (here) {
-        float dg[N], du[N], h[N];
+    if (OP == kBackward && compute) {
+      float dg[kN], du[kN], h[kN];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float g = ga.get(e), u = ub.get(e), d = a.v.get(e);
-          const float s = sigmoid<DT>(g), act = g * s;
-          h[e] = act * u;
-          du[e] = d * act;
-          dg[e] = d * u * (s * fmaf(g, 1.f - s, 1.f));
-        }
-        write_row<DT, WIDE>(p, 0, t, c, dg);
-        write_row<DT, WIDE>(p, 1, t, c, du);
-        if (p.out[2]) write_row<DT, WIDE>(p, 2, t, c, h);
+      for (int e = 0; e < kN; ++e) {
+        const float g = ga.get(e), u = ub.get(e), d = a.v.get(e);
+        const float s = sigmoid<DT>(g), act = g * s;
+        h[e] = act * u;
+        du[e] = d * act;
+        dg[e] = d * u * (s * fmaf(g, 1.f - s, 1.f));
       }
+      write(0, dg);
+      write(1, du);
+      if (p.out[2]) write(2, h);
     }
   }
 }
@@ -273,15 +272,15 @@ int run_one(CkptParams p, int sms, cudaStream_t s) {
   // store and forward also write the padding behind the last column
   const int64_t extent =
       OP == kStore || OP == kForward ? std::max<int64_t>(p.pitch, static_cast<int64_t>(p.scale_pitch) * kBlock) : p.cols;
-  // lanes that cover a row; whole warps in the narrow form, whole blocks (4 lanes) in the wide one
-  const int64_t lanes = WIDE ? (extent + kWide - 1) / kWide : (extent + 32 * kNarrow - 1) / (32 * kNarrow) * 32;
+  // lanes that cover a row: whole blocks of 32 values (4 lanes), whole warps where they exchange values
+  const int64_t lanes = (extent + kN - 1) / kN;
   p.lanes_log2 = WIDE ? 2 : 5;
   while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < lanes) ++p.lanes_log2;
   const int64_t gx = (lanes + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
   const int height = kThreads >> p.lanes_log2;
   // Blocks beyond the resident ones even out the end; too many repeat the setup: 16384 x 14336 gated, both ways,
-  // 675 us at 32 a SM, 660 at 128, 722 without a limit; 4093 x 6143 narrow store and load 61, 73 and 79. (Two row
-  // steps in flight per thread cost registers: 10 % slower.)
+  // 675 us at 32 a SM, 660 at 128, 722 without a limit. (Two row steps in flight per thread cost registers: 10 %
+  // slower.)
   const int64_t want = (p.rows + height - 1) / height;
   const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(sms) * (WIDE ? 128 : 32) / gx);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>({want, most, 65535})), 1);
@@ -339,7 +338,7 @@ extern "C" int ns_ckpt_store(const void *x, int64_t ld_x, int64_t rows, int64_t 
   p.rows = rows;
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(q), static_cast<uint8_t *>(scales)};
-  return ckpt_call<kStore>(p, dtype, cols % kWide == 0 && rows_aligned(x, ld_x, elt, kWide), stream);
+  return ckpt_call<kStore>(p, dtype, cols % kN == 0 && rows_aligned(x, ld_x, elt, kN), stream);
 }
 
 extern "C" int ns_ckpt_load(const void *q, const void *scales, int64_t rows, int64_t cols, void *out, int64_t ld_out,
@@ -360,7 +359,7 @@ extern "C" int ns_ckpt_load(const void *q, const void *scales, int64_t rows, int
   p.rows = rows;
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(const_cast<void *>(q)), static_cast<uint8_t *>(const_cast<void *>(scales))};
-  return ckpt_call<kLoad>(p, dtype, cols % kWide == 0 && rows_aligned(out, ld_out, elt, kWide), stream);
+  return ckpt_call<kLoad>(p, dtype, cols % kN == 0 && rows_aligned(out, ld_out, elt, kN), stream);
 }
 
 extern "C" int ns_gated_forward(const void *gate, const void *up, int64_t ld_in, int64_t rows, int64_t cols, void *h,
@@ -394,8 +393,8 @@ extern "C" int ns_gated_forward(const void *gate, const void *up, int64_t ld_in,
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(q_gate), static_cast<uint8_t *>(s_gate)};
   p.held[1] = Held{static_cast<int8_t *>(q_up), static_cast<uint8_t *>(s_up)};
-  const bool wide = cols % kWide == 0 && rows_aligned(gate, ld_in, elt, kWide) && rows_aligned(up, ld_in, elt, kWide) &&
-                    rows_aligned(h, ld_h, elt, kWide);
+  const bool wide = cols % kN == 0 && rows_aligned(gate, ld_in, elt, kN) && rows_aligned(up, ld_in, elt, kN) &&
+                    rows_aligned(h, ld_h, elt, kN);
   return ckpt_call<kForward>(p, dtype, wide, stream);
 }
 
@@ -433,7 +432,7 @@ extern "C" int ns_gated_backward(const void *dh, int64_t ld_dh, const void *q_ga
   p.cols = static_cast<int>(cols);
   p.held[0] = Held{static_cast<int8_t *>(const_cast<void *>(q_gate)), static_cast<uint8_t *>(const_cast<void *>(s_gate))};
   p.held[1] = Held{static_cast<int8_t *>(const_cast<void *>(q_up)), static_cast<uint8_t *>(const_cast<void *>(s_up))};
-  const bool wide = cols % kWide == 0 && rows_aligned(dh, ld_dh, elt, kWide) && rows_aligned(dgate, ld_d, elt, kWide) &&
-                    rows_aligned(dup, ld_d, elt, kWide) && (!h || rows_aligned(h, ld_h, elt, kWide));
+  const bool wide = cols % kN == 0 && rows_aligned(dh, ld_dh, elt, kN) && rows_aligned(dgate, ld_d, elt, kN) &&
+                    rows_aligned(dup, ld_d, elt, kN) && (!h || rows_aligned(h, ld_h, elt, kN));
   return ckpt_call<kBackward>(p, dtype, wide, stream);
 }
