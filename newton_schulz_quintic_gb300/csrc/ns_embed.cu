@@ -10,7 +10,7 @@
 //     them adds them all.
 //   else: sort      one cluster of 8 CTAs, a stable radix sort of (id,
 //                   position); padding ids sort to the end;
-//         segments  the sorted list in fixed pieces of kSeg positions, one
+//         segments  the sorted list in equal pieces of positions, one
 //                   piece and column range per CTA, whatever the ids are: a
 //                   run of equal ids inside a piece is written to the table,
 //                   the parts of a run that crosses piece borders go to
@@ -43,35 +43,34 @@ struct LookupParams {
 constexpr int kLookupPacks = 4;  // packs a lane has in flight
 
 // One warp per (row, stretch of 32 * kLookupPacks packs).
-template <int DT, int VEC>
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256) ns_embed_lookup_kernel(const __grid_constant__ LookupParams p) {
-  using P = Pack<DT, VEC>;
-  using E = typename P::E;
-  constexpr int kSpan = 32 * kLookupPacks * VEC;
-  const int lane = threadIdx.x & 31;
+  using R = RowPart<DT, WIDE>;
+  using E = typename R::E;
+  constexpr int kSpan = 32 * kLookupPacks * R::kN;
   const int per_row = (p.dim + kSpan - 1) / kSpan;
   const int64_t items = p.count * per_row;
   const size_t size = static_cast<size_t>((p.count - 1) * p.ld_out + p.dim) * sizeof(E);
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
        it += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t t = it / per_row;
-    const int c0 = static_cast<int>(it - t * per_row) * kSpan + lane * VEC;
+    const int c0 = static_cast<int>(it - t * per_row) * kSpan + R::first(threadIdx.x & 31);
     const int id = p.ids.get(t);
     const E *src = static_cast<const E *>(p.table) + static_cast<int64_t>(id < 0 ? 0 : id) * p.ld_table;
     E *dst = static_cast<E *>(p.out) + t * p.ld_out;
-    P v[kLookupPacks];
+    R v[kLookupPacks];
 #pragma unroll
     for (int k = 0; k < kLookupPacks; ++k) {
-      const int c = c0 + k * 32 * VEC;
-      if (id >= 0 && c < p.dim) v[k].load(src + c);
+      const int c = c0 + k * 32 * R::kN;
+      if (id >= 0 && c < p.dim) v[k].template load<false>(src, c, p.dim);
     }
 #pragma unroll
     for (int k = 0; k < kLookupPacks; ++k) {
-      const int c = c0 + k * 32 * VEC;
+      const int c = c0 + k * 32 * R::kN;
       if (c >= p.dim) continue;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k].set(e, id >= 0 ? v[k].get(e) * p.scale : 0.f);
-      v[k].store_stream(dst + c, p.out, size, p.status);
+      for (int e = 0; e < R::kN; ++e) v[k].set(e, id >= 0 ? v[k].get(e) * p.scale : 0.f);
+      v[k].store(dst, c, p.dim, p.out, size, p.status);
     }
   }
 }
@@ -95,7 +94,10 @@ struct Bitmap {
 // The calling CTA, `part` of `parts`, clears those rows of its share of the
 // table that no id points to.
 __device__ __forceinline__ void zero_absent(const ZeroParams &p, Bitmap &seen, int part, int parts) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // lanes per row: a 16-byte word each as far as a row goes, 4 to 32
+  int lanes = 4;
+  while (lanes < 32 && lanes * 16 < p.row_bytes) lanes *= 2;
+  const int lane = threadIdx.x & (lanes - 1);
   const int64_t vocab = p.ids.vocab;
   const int64_t r0 = vocab * part / parts, r1 = vocab * (part + 1) / parts;
   for (int64_t a = r0; a < r1; a += kZeroRows) {
@@ -108,18 +110,18 @@ __device__ __forceinline__ void zero_absent(const ZeroParams &p, Bitmap &seen, i
       if (d >= 0 && d < rows) atomicOr(&seen.w[d >> 5], 1u << (d & 31));
     }
     __syncthreads();
-    for (int r = warp; r < rows; r += warps) {
+    for (int r = threadIdx.x / lanes; r < rows; r += blockDim.x / lanes) {
       if ((seen.w[r >> 5] >> (r & 31)) & 1u) continue;
       // 2- or 4-byte elements up to a 16-byte boundary, whole 16-byte words, the rest
       uint8_t *row = p.grad + (a + r) * p.ld_bytes, *end = row + p.row_bytes;
       uint8_t *lo = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(row) + 15) & ~uintptr_t(15));
       uint8_t *hi = reinterpret_cast<uint8_t *>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
       if (lo > hi) lo = hi = end;
-      for (uint8_t *at = lo + lane * 16; at < hi; at += 512)
+      for (uint8_t *at = lo + lane * 16; at < hi; at += lanes * 16)
         if (in_bounds(at, 16, p.grad, p.size, p.status)) __stcs(reinterpret_cast<uint4 *>(at), make_uint4(0, 0, 0, 0));
-      for (uint8_t *at = row + lane * 2; at < lo; at += 64)
+      for (uint8_t *at = row + lane * 2; at < lo; at += lanes * 2)
         if (in_bounds(at, 2, p.grad, p.size, p.status)) *reinterpret_cast<uint16_t *>(at) = 0;
-      for (uint8_t *at = hi + lane * 2; at < end; at += 64)
+      for (uint8_t *at = hi + lane * 2; at < end; at += lanes * 2)
         if (in_bounds(at, 2, p.grad, p.size, p.status)) *reinterpret_cast<uint16_t *>(at) = 0;
     }
     __syncthreads();
@@ -257,10 +259,14 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // ------------------------------------------------------------------ segment sums
-constexpr int kSeg = 64;         // sorted positions per piece (32: joins of a frequent id take 6 us more at 32768 ids)
+constexpr int kSegMost = 64;     // sorted positions per piece at most, and
+constexpr int kSegLeast = 16;    // at least (see run_segments)
 constexpr int kSegThreads = 128;
 constexpr int kSegAhead = 8;     // rows in flight per thread
 constexpr int kJoinAhead = 16;   // parts in flight per thread
+
+// CTAs that cover a row, with packs of vec elements per thread.
+inline int chunks_of(int dim, int vec) { return (dim + kSegThreads * vec - 1) / (kSegThreads * vec); }
 
 struct GradParams {
   const void *dout;
@@ -269,51 +275,67 @@ struct GradParams {
   float *parts;           // [piece][2][dim_pad]: the piece's share of the run that enters it / leaves it
   int64_t ld_dout, ld_grad;
   int n, vocab, dim, dim_pad, pieces;
+  int seg;                // sorted positions per piece
   int chunks;             // column ranges per piece (one CTA each)
   float scale;
   int accumulate;
   int *status;
 };
 
-template <int GT, int VEC>
-__device__ __forceinline__ void write_row(const GradParams &p, int id, int c, const float (&sum)[VEC]) {
-  using P = Pack<GT, VEC>;
-  typename P::E *g = static_cast<typename P::E *>(p.grad) + static_cast<int64_t>(id) * p.ld_grad + c;
-  P v;
-  if (p.accumulate) v.load(g);
+// The sums of a thread's columns into row id of the table; the columns are
+// those of RowPart<DT, WIDE>, of kN sums, whatever the table's type is.
+template <int GT, bool WIDE, int N>
+__device__ __forceinline__ void write_row(const GradParams &p, int id, int c, const float (&sum)[N]) {
+  using G = typename Elem<GT>::T;
+  G *row = static_cast<G *>(p.grad) + static_cast<int64_t>(id) * p.ld_grad;
+  const size_t size = static_cast<size_t>((p.vocab - 1) * p.ld_grad + p.dim) * sizeof(G);
+  if constexpr (WIDE) {
+    Pack<GT, N> v;
+    if (p.accumulate) v.load(row + c);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) v.set(e, p.accumulate ? fmaf(p.scale, sum[e], v.get(e)) : p.scale * sum[e]);
-  v.store(g, p.grad, static_cast<size_t>((p.vocab - 1) * p.ld_grad + p.dim) * sizeof(typename P::E), p.status);
+    for (int e = 0; e < N; ++e) v.set(e, p.accumulate ? fmaf(p.scale, sum[e], v.get(e)) : p.scale * sum[e]);
+    v.store(row + c, p.grad, size, p.status);
+  } else {
+    G old[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (p.accumulate && c + 32 * e < p.dim) old[e] = row[c + 32 * e];
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + 32 * e < p.dim && in_bounds(row + c + 32 * e, sizeof(G), p.grad, size, p.status))
+        row[c + 32 * e] = Elem<GT>::from_f(p.accumulate ? fmaf(p.scale, sum[e], Elem<GT>::to_f(old[e])) : p.scale * sum[e]);
+  }
 }
 
-template <int DT, int GT, int VEC>
+template <int DT, int GT, bool WIDE>
 __global__ void __launch_bounds__(kSegThreads) ns_embed_segments_kernel(const __grid_constant__ GradParams p) {
-  using P = Pack<DT, VEC>;
-  using E = typename P::E;
-  __shared__ int key[kSeg + 2];  // with the neighbours on either side
-  __shared__ int at[kSeg];
+  using R = RowPart<DT, WIDE>;
+  using E = typename R::E;
+  constexpr int kN = R::kN;
+  __shared__ int key[kSegMost + 2];  // with the neighbours on either side
+  __shared__ int at[kSegMost];
   const int piece = blockIdx.x / p.chunks, chunk = blockIdx.x - piece * p.chunks;
-  const int i0 = piece * kSeg;
-  const int len = min(kSeg, p.n - i0);
-  if (threadIdx.x < kSeg + 2) {
+  const int i0 = piece * p.seg;
+  const int len = min(p.seg, p.n - i0);
+  if (threadIdx.x < p.seg + 2) {
     const int i = i0 - 1 + static_cast<int>(threadIdx.x);
     key[threadIdx.x] = i >= 0 && i < p.n ? p.keys[i] : -1;
     if (threadIdx.x < len) at[threadIdx.x] = p.pos[i0 + threadIdx.x];
   }
   __syncthreads();
-  const int c = (chunk * kSegThreads + threadIdx.x) * VEC;
+  const int c = R::first(chunk * kSegThreads + threadIdx.x);
   if (c >= p.dim) return;
-  float sum[VEC];
+  float sum[kN];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
-  const E *src = static_cast<const E *>(p.dout) + c;
-  float *parts = p.parts + static_cast<int64_t>(piece) * 2 * p.dim_pad + c;
+  for (int e = 0; e < kN; ++e) sum[e] = 0.f;
+  const E *src = static_cast<const E *>(p.dout);
+  float *parts = p.parts + static_cast<int64_t>(piece) * 2 * p.dim_pad;
   bool entered = key[0] == key[1];  // the current run began in an earlier piece
   for (int k0 = 0; k0 < len; k0 += kSegAhead) {
-    P v[kSegAhead];
+    R v[kSegAhead];
 #pragma unroll
     for (int k = 0; k < kSegAhead; ++k)
-      if (k0 + k < len && key[k0 + k + 1] < p.vocab) v[k].load_stream(src + static_cast<int64_t>(at[k0 + k]) * p.ld_dout);
+      if (k0 + k < len && key[k0 + k + 1] < p.vocab) v[k].template load<true>(src + static_cast<int64_t>(at[k0 + k]) * p.ld_dout, c, p.dim);
 #pragma unroll
     for (int k = 0; k < kSegAhead; ++k) {
       const int i = k0 + k;
@@ -321,19 +343,22 @@ __global__ void __launch_bounds__(kSegThreads) ns_embed_segments_kernel(const __
       const int id = key[i + 1];
       if (id >= p.vocab) break;  // padding: the rest of the list
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sum[e] += v[k].get(e);
+      for (int e = 0; e < kN; ++e) sum[e] += v[k].get(e);
       const bool ends = key[i + 2] != id;
       if (ends || i == len - 1) {
         if (ends && !entered) {
-          write_row<GT, VEC>(p, id, c, sum);
+          write_row<GT, WIDE>(p, id, c, sum);
         } else {
           float *to = parts + (entered ? 0 : p.dim_pad);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (in_bounds(to + e, 4, p.parts, static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, p.status)) to[e] = sum[e];
+          for (int e = 0; e < kN; ++e) {
+            float *at_e = to + R::at(c, e);
+            if (R::at(c, e) < p.dim && in_bounds(at_e, 4, p.parts, static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, p.status))
+              *at_e = sum[e];
+          }
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
+        for (int e = 0; e < kN; ++e) sum[e] = 0.f;
         entered = false;
       }
     }
@@ -345,15 +370,15 @@ __global__ void __launch_bounds__(kSegThreads) ns_embed_segments_kernel(const __
 template <int GT, int VEC>
 __global__ void __launch_bounds__(kSegThreads) ns_embed_joins_kernel(const __grid_constant__ GradParams p) {
   const int b = blockIdx.x / p.chunks;
-  const int last = (b + 1) * kSeg - 1;
+  const int last = (b + 1) * p.seg - 1;
   if (last + 1 >= p.n) return;
   const int id = p.keys[last];
   if (id >= p.vocab || p.keys[last + 1] != id) return;              // nothing leaves
-  if (b > 0 && p.keys[b * kSeg] == id && p.keys[b * kSeg - 1] == id) return;  // began earlier
+  if (b > 0 && p.keys[b * p.seg] == id && p.keys[b * p.seg - 1] == id) return;  // began earlier
   // pieces b + 1 .. q begin with it: the CTA looks at kSegThreads of them at a time
   int q = b;
   for (int more = kSegThreads; more == kSegThreads;) {
-    const int64_t i = static_cast<int64_t>(q + 1 + static_cast<int>(threadIdx.x)) * kSeg;
+    const int64_t i = static_cast<int64_t>(q + 1 + static_cast<int>(threadIdx.x)) * p.seg;
     more = __syncthreads_count(i < p.n && p.keys[i] == id);
     q += more;
   }
@@ -378,7 +403,7 @@ __global__ void __launch_bounds__(kSegThreads) ns_embed_joins_kernel(const __gri
         for (int e = 0; e < VEC; ++e) sum[e] += v[k][e];
       }
   }
-  write_row<GT, VEC>(p, id, c, sum);
+  write_row<GT, (VEC > 1)>(p, id, c, sum);
 }
 
 // ------------------------------------------------------------------ few positions
@@ -387,11 +412,12 @@ constexpr int kDirect = 1024;  // positions at most (the words of a list of matc
 // CTAs [0, n * chunks): position t and a column range. The first position of
 // an id adds the rows of all its positions; the list of them is a bitmap, so
 // they come in order. The CTAs behind clear the absent rows.
-template <int DT, int GT, int VEC>
+template <int DT, int GT, bool WIDE>
 __global__ void __launch_bounds__(kSegThreads)
     ns_embed_direct_kernel(const __grid_constant__ GradParams p, const __grid_constant__ ZeroParams zero) {
-  using P = Pack<DT, VEC>;
-  using E = typename P::E;
+  using R = RowPart<DT, WIDE>;
+  using E = typename R::E;
+  constexpr int kN = R::kN;
   const int work = p.n * p.chunks;
   if (blockIdx.x >= work) {
     __shared__ Bitmap seen;
@@ -410,12 +436,12 @@ __global__ void __launch_bounds__(kSegThreads)
     earlier |= same && i < t;
   }
   if (__syncthreads_or(earlier)) return;
-  const int c = (chunk * kSegThreads + threadIdx.x) * VEC;
+  const int c = R::first(chunk * kSegThreads + threadIdx.x);
   if (c >= p.dim) return;
-  float sum[VEC];
+  float sum[kN];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
-  const E *src = static_cast<const E *>(p.dout) + c;
+  for (int e = 0; e < kN; ++e) sum[e] = 0.f;
+  const E *src = static_cast<const E *>(p.dout);
   int word = t >> 5;
   uint32_t left = match[word];
   const int words = (p.n + 31) >> 5;
@@ -429,12 +455,12 @@ __global__ void __launch_bounds__(kSegThreads)
     return i;
   };
   for (int i = next(); i >= 0;) {
-    P v[kSegAhead];
+    R v[kSegAhead];
     int count = 0;
 #pragma unroll
     for (int k = 0; k < kSegAhead; ++k)
       if (i >= 0) {
-        v[k].load_stream(src + static_cast<int64_t>(i) * p.ld_dout);
+        v[k].template load<true>(src + static_cast<int64_t>(i) * p.ld_dout, c, p.dim);
         ++count;
         i = next();
       }
@@ -442,19 +468,19 @@ __global__ void __launch_bounds__(kSegThreads)
     for (int k = 0; k < kSegAhead; ++k)
       if (k < count) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e] += v[k].get(e);
+        for (int e = 0; e < kN; ++e) sum[e] += v[k].get(e);
       }
   }
-  write_row<GT, VEC>(p, id, c, sum);
+  write_row<GT, WIDE>(p, id, c, sum);
 }
 
-template <int DT, int VEC>
+template <int DT, bool WIDE>
 int run_lookup(const LookupParams &p, cudaStream_t s) {
-  const int span = 32 * kLookupPacks * VEC;
+  const int span = 32 * kLookupPacks * RowPart<DT, WIDE>::kN;
   const int64_t items = p.count * ((p.dim + span - 1) / span);
   // an item per warp: 62 us at 32768 rows of 8 KB, 69 with as many warps as are resident walking over them
   const int grid = static_cast<int>(std::min<int64_t>((items + 7) / 8, INT32_MAX));
-  ns_embed_lookup_kernel<DT, VEC><<<grid, 256, 0, s>>>(p);
+  ns_embed_lookup_kernel<DT, WIDE><<<grid, 256, 0, s>>>(p);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -492,21 +518,21 @@ int run_sort(const SortParams &p, const ZeroParams &zero, bool clear, int dev, i
   return 0;
 }
 
-template <int DT, int GT, int VEC>
+template <int DT, int GT, bool WIDE>
 int run_direct(const GradParams &p, const ZeroParams &zero, int sms, cudaStream_t s) {
-  // the rows to clear: one CTA each for 64 KB, four per SM at most
-  const int64_t clear = p.accumulate ? 0 : (static_cast<int64_t>(p.vocab) * zero.row_bytes + 65535) / 65536;
-  const int64_t grid = static_cast<int64_t>(p.n) * p.chunks + std::min<int64_t>(clear, sms * 4);
-  ns_embed_direct_kernel<DT, GT, VEC><<<static_cast<int>(grid), kSegThreads, 0, s>>>(p, zero);
+  // the rows to clear: a CTA for 16 KB, as many as are resident at most
+  const int64_t clear = p.accumulate ? 0 : (static_cast<int64_t>(p.vocab) * zero.row_bytes + 16383) / 16384;
+  const int64_t grid = static_cast<int64_t>(p.n) * p.chunks + std::min<int64_t>(clear, sms * 8);
+  ns_embed_direct_kernel<DT, GT, WIDE><<<static_cast<int>(grid), kSegThreads, 0, s>>>(p, zero);
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-template <int DT, int GT, int VEC>
+template <int DT, int GT, bool WIDE>
 int run_segments(const GradParams &p, cudaStream_t s) {
-  ns_embed_segments_kernel<DT, GT, VEC><<<p.pieces * p.chunks, kSegThreads, 0, s>>>(p);
+  ns_embed_segments_kernel<DT, GT, WIDE><<<p.pieces * p.chunks, kSegThreads, 0, s>>>(p);
   count_launch();
-  constexpr int kJoin = VEC == 1 ? 1 : 4;  // a 16-byte word of the fp32 parts
+  constexpr int kJoin = WIDE ? 4 : 1;  // a 16-byte word of the fp32 parts
   GradParams j = p;
   j.chunks = (p.dim + kSegThreads * kJoin - 1) / (kSegThreads * kJoin);
   ns_embed_joins_kernel<GT, kJoin><<<p.pieces * j.chunks, kSegThreads, 0, s>>>(j);
@@ -516,11 +542,9 @@ int run_segments(const GradParams &p, cudaStream_t s) {
 
 template <int DT, int GT>
 int run_grad(GradParams p, const ZeroParams &zero, bool wide, int sms, cudaStream_t s) {
-  constexpr int VEC = DT == kBF16 ? 8 : 4;
-  const int per = kSegThreads * (wide ? VEC : 1);
-  p.chunks = (p.dim + per - 1) / per;
-  if (p.n <= kDirect) return wide ? run_direct<DT, GT, VEC>(p, zero, sms, s) : run_direct<DT, GT, 1>(p, zero, sms, s);
-  return wide ? run_segments<DT, GT, VEC>(p, s) : run_segments<DT, GT, 1>(p, s);
+  p.chunks = chunks_of(p.dim, DT == kBF16 ? 8 : 4);
+  if (p.n <= kDirect) return wide ? run_direct<DT, GT, true>(p, zero, sms, s) : run_direct<DT, GT, false>(p, zero, sms, s);
+  return wide ? run_segments<DT, GT, true>(p, s) : run_segments<DT, GT, false>(p, s);
 }
 
 }  // namespace
@@ -549,8 +573,8 @@ extern "C" int ns_embed_lookup(const void *table, int64_t ld_table, int64_t voca
   const int vec = 16 / elt;
   const bool wide = dim % vec == 0 && rows_aligned(table, ld_table, elt, vec) && rows_aligned(out, ld_out, elt, vec);
   return call.launch(kOpLookup, [&] {
-    if (dtype == NS_BF16) return wide ? run_lookup<kBF16, 8>(p, call.s) : run_lookup<kBF16, 1>(p, call.s);
-    return wide ? run_lookup<kF32, 4>(p, call.s) : run_lookup<kF32, 1>(p, call.s);
+    if (dtype == NS_BF16) return wide ? run_lookup<kBF16, true>(p, call.s) : run_lookup<kBF16, false>(p, call.s);
+    return wide ? run_lookup<kF32, true>(p, call.s) : run_lookup<kF32, false>(p, call.s);
   });
 }
 
@@ -561,7 +585,7 @@ extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids,
       (id_type != NS_I32 && id_type != NS_I64) || (accumulate != 0 && accumulate != 1))
     return NS_EINVAL;
   if (bad_shape(vocab, dim, ld_grad) || bad_shape(count, dim, ld_dout) || vocab >= INT32_MAX) return NS_EINVAL;
-  if (count > (1 << 30) || dim > (1 << 24) || (count / kSeg + 1) * (dim / kSegThreads + 1) > INT32_MAX) return NS_EINVAL;
+  if (count > (1 << 30) || dim > (1 << 24) || (count / kSegLeast + 1) * (dim / kSegThreads + 1) > INT32_MAX) return NS_EINVAL;
   if (vocab == 0 || dim == 0 || (count == 0 && accumulate)) return NS_OK;
   if (!grad || (count > 0 && (!ids || !dout))) return NS_EINVAL;
   const int elt = dtype == NS_BF16 ? 2 : 4, gelt = grad_dtype == NS_BF16 ? 2 : 4;
@@ -582,14 +606,20 @@ extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids,
   p.vocab = static_cast<int>(vocab);
   p.dim = static_cast<int>(dim);
   p.dim_pad = static_cast<int>((dim + 7) / 8 * 8);
-  p.pieces = (n + kSeg - 1) / kSeg;
   p.scale = scale;
   p.accumulate = accumulate;
   p.status = call.status;
   const Ids list_ids{ids, id_type == NS_I64, p.vocab};
   const ZeroParams zero{list_ids, n, static_cast<uint8_t *>(grad), ld_grad * gelt, static_cast<int>(dim * gelt),
                         static_cast<size_t>((vocab - 1) * ld_grad + dim) * gelt, call.status};
+  const int vec = 16 / elt;
+  const bool wide = dim % vec == 0 && rows_aligned(dout, ld_dout, elt, vec) && rows_aligned(grad, ld_grad, gelt, vec);
   if (n > kDirect) {
+    // long pieces leave fewer parts to join (32768 ids of 8 KB rows: 6 us less with 64 than with 32), short ones give
+    // few positions more CTAs: the longest that give an SM 12 CTAs
+    p.seg = kSegMost;
+    while (p.seg > kSegLeast && static_cast<int64_t>(n / p.seg) * chunks_of(p.dim, vec) < 12ll * call.sms) p.seg /= 2;
+    p.pieces = (n + p.seg - 1) / p.seg;
     const size_t list = (static_cast<size_t>(n) * 4 + 255) / 256 * 256;
     uint8_t *ws = nullptr;
     int rc = call.workspace(kSlotEmbed, 4 * list + static_cast<size_t>(p.pieces) * 2 * p.dim_pad * 4, &ws);
@@ -611,8 +641,6 @@ extern "C" int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids,
     p.parts = reinterpret_cast<float *>(ws + 4 * list);
     if ((rc = call.launch(kOpSort, [&] { return run_sort(sp, zero, !accumulate, call.dev, call.sms, call.s); }))) return rc;
   }
-  const int vec = 16 / elt;
-  const bool wide = dim % vec == 0 && rows_aligned(dout, ld_dout, elt, vec) && rows_aligned(grad, ld_grad, gelt, vec);
   return call.launch(kOpEmbedGrad, [&] {
     if (dtype == NS_BF16)
       return grad_dtype == NS_BF16 ? run_grad<kBF16, kBF16>(p, zero, wide, call.sms, call.s)

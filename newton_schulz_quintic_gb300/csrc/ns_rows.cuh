@@ -52,6 +52,46 @@ struct Pack {
   }
 };
 
+// The columns of a row that a thread holds, kN of them from its column c on:
+// consecutive ones where rows allow packed accesses (WIDE), else every 32nd,
+// so that a warp's accesses stay coalesced; beyond the row nothing is read or
+// written. first() is c of a thread, for threads numbered along the row.
+template <int DT, bool WIDE>
+struct RowPart {
+  static constexpr int kN = DT == kBF16 ? 8 : 4;
+  using E = typename Elem<DT>::T;
+  Pack<DT, kN> v;
+  static __device__ __forceinline__ int first(int thread) { return WIDE ? thread * kN : (thread / 32) * (32 * kN) + thread % 32; }
+  static __device__ __forceinline__ int at(int c, int e) { return WIDE ? c + e : c + 32 * e; }
+  // ONCE: not read again, first to leave the caches
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const E *row, int c, int cols) {
+    if constexpr (WIDE) {
+      if (ONCE)
+        v.load_stream(row + c);
+      else
+        v.load(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        reinterpret_cast<E *>(v.w)[e] =
+            c + 32 * e < cols ? (ONCE ? __ldcs(row + c + 32 * e) : row[c + 32 * e]) : Elem<DT>::from_f(0.f);
+    }
+  }
+  __device__ __forceinline__ float get(int e) const { return v.get(e); }
+  __device__ __forceinline__ void set(int e, float x) { v.set(e, x); }
+  __device__ __forceinline__ void store(E *row, int c, int cols, const void *base, size_t size, int *status) const {
+    if constexpr (WIDE) {
+      v.store_stream(row + c, base, size, status);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (c + 32 * e < cols && in_bounds(row + c + 32 * e, sizeof(E), base, size, status))
+          __stcs(row + c + 32 * e, reinterpret_cast<const E *>(v.w)[e]);
+    }
+  }
+};
+
 // Token ids: int32 or int64; anything outside [0, vocab) becomes -1.
 struct Ids {
   const void *p;
