@@ -3,7 +3,9 @@
 //
 // Per row, with m the largest logit, k = inv_temperature * log2(e) and s = sum
 // of 2^(v k - m k) over the row's logits v: logp = (v[y] - m) inv_temperature -
-// log s, corrected by what rounding m k left out. A row's gradient depends on nothing but the row, so it follows at
+// log s, corrected by what rounding m k left out (the few operations of that
+// line in fp64: its terms are about 10 where the KL term wants its differences
+// from old and reference to 1e-7). A row's gradient depends on nothing but the row, so it follows at
 // once: softmax times the row's coefficient.
 //
 // One CTA per row (a cluster of up to 8 where few rows leave SMs idle), in two
@@ -54,7 +56,8 @@ struct PolicyParams {
 constexpr int kMaxThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int64_t kKeepBytes = 216 * 1024;  // shared memory of an SM for rows kept between the passes
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLn2 = 0.69314718055994530942;
 constexpr float kLargest = 3.402823466e38f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -100,6 +103,14 @@ __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k) {
   return MaxSum{m, fmaf(a.s, rebase(a.m, m, k), __fmul_rn(b.s, rebase(b.m, m, k)))};
 }
 
+// log s, with the exponent's part in fp64 (s is 1 or more as a rule; infinities and NaN pass through).
+__device__ __forceinline__ double log_of(float s) {
+  if (!(s >= 1.f && s <= kLargest)) return logf(s);
+  const int e = (__float_as_int(s) >> 23) - 127;
+  const float f = __int_as_float((__float_as_int(s) & 0x7fffff) | 0x3f800000);  // 1 .. 2
+  return e * kLn2 + logf(f);
+}
+
 struct RowInputs {
   float old_logp, ref_logp, advantage, weight;
 };
@@ -118,14 +129,14 @@ __device__ __forceinline__ RowInputs row_inputs(const PolicyParams &p, int64_t t
 }
 
 // The row's outputs from its target's log probability.
-__device__ __forceinline__ RowResult policy_row(const PolicyParams &p, const RowInputs &in, float logp) {
-  RowResult r{logp, 0.f, 0.f, 0.f};
+__device__ __forceinline__ RowResult policy_row(const PolicyParams &p, const RowInputs &in, double logp) {
+  RowResult r{static_cast<float>(logp), 0.f, 0.f, 0.f};
   if (!p.weight) return r;
-  const float ratio = p.old_logp ? expf(logp - in.old_logp) : 1.f;
+  const float ratio = p.old_logp ? expf(static_cast<float>(logp - in.old_logp)) : 1.f;
   const float a = ratio * in.advantage, b = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * in.advantage;
   float slope = a <= b ? -a : 0.f;
   if (p.ref_logp) {
-    const float d = in.ref_logp - logp, e = expm1f(d);
+    const float d = static_cast<float>(in.ref_logp - logp), e = expm1f(d);
     r.kl = e - d;
     slope -= p.kl_coef * e;
   }
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
         const Scale f(a.m, k);
         // the powers are relative to m k as rounded
         const float left_out = f.plain ? fmaf(a.m, k, -f.mk) : 0.f;
-        r = policy_row(p, in, fmaf(left_out, kLn2, (target - a.m) * p.inv_temp - logf(a.s)));
+        r = policy_row(p, in, (static_cast<double>(target) - a.m) * p.inv_temp + left_out * kLn2 - log_of(a.s));
       }
       res = r;
       if (rank == 0) write_result(p, t, r);
