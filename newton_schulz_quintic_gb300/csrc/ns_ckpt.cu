@@ -13,6 +13,10 @@
 // the other (a block per warp access and a value per lane instead costs 33
 // instructions per 32 values: 57 against 45 us for fp32 4093 x 6143 stored and
 // loaded).
+//
+// 16384 x 14336 bf16: gated forward 301 us, 6.4 TB/s; backward 359 us, 6.6 TB/s
+// (96 and 99 % of the copy rate). fp32 4093 x 6143, unaligned, stored and loaded:
+// 45 us, 5.6 TB/s.
 #include <algorithm>
 
 #include "../../include/ns.h"
