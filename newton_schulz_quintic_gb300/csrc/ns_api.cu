@@ -887,12 +887,17 @@ OpCall::OpCall(void *stream) : s(static_cast<cudaStream_t>(stream)), lock(g_mu) 
     nvtxRangePushA("ns call");
     ranged = true;
   }
-  DevInfo *di = nullptr;
-  rc = device_info(&di);
-  if (rc) return;
-  sms = di->sms;
-  status = di->status;
-  cudaGetDevice(&dev);
+  // the maps behind these allocate; an exception must not reach the C boundary
+  try {
+    DevInfo *di = nullptr;
+    rc = device_info(&di);
+    if (rc) return;
+    sms = di->sms;
+    status = di->status;
+    cudaGetDevice(&dev);
+  } catch (...) {
+    rc = NS_ENOMEM;
+  }
 }
 
 OpCall::~OpCall() {
@@ -900,11 +905,15 @@ OpCall::~OpCall() {
 }
 
 int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr, bool *fresh) {
-  CachedWs &c = g_ws[WsKey{dev, s, slot}];
-  if (fresh) *fresh = !(c.ptr && c.bytes >= std::max<size_t>(bytes, 256));
-  const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s);
-  *ptr = c.ptr;
-  return e;
+  try {
+    CachedWs &c = g_ws[WsKey{dev, s, slot}];
+    if (fresh) *fresh = !(c.ptr && c.bytes >= std::max<size_t>(bytes, 256));
+    const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s);
+    *ptr = c.ptr;
+    return e;
+  } catch (...) {
+    return NS_ENOMEM;
+  }
 }
 
 int OpCall::tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
@@ -925,7 +934,11 @@ int OpCall::tensor_map(CUtensorMap *map, int elt, const void *base, int rank, co
 }
 
 int OpCall::timed_launch(int kind, int (*fn)(void *), void *arg) {
-  return timed(kind, s, [&] { return fn(arg); }) ? NS_ECUDA : NS_OK;
+  try {
+    return timed(kind, s, [&] { return fn(arg); }) ? NS_ECUDA : NS_OK;
+  } catch (...) {
+    return NS_ENOMEM;
+  }
 }
 
 }  // namespace ns

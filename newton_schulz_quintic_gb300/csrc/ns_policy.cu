@@ -29,6 +29,7 @@
 // a launch of its own where that CTA would be long at it.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/ns.h"
 #include "ns_rows.cuh"
@@ -66,37 +67,42 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Factor and offset with which a logit v becomes the exponent v k - m k. Where
-// m k overflows, distinct logits of that size differ by more than 2^100 in the
-// exponent, and by more than 2^35 with k's power of two times 2^-64, which does
-// not overflow and whose products are exact: the powers are 0 or 1 either way.
-// m = -inf: nothing but -inf so far, whose powers are 0.
+// How a logit v becomes the power 2^((v - m) k). As long as |m k| is below
+// kPlain, by one fused multiply-add: v k - mk, with mk = m k rounded, is off by
+// that rounding (2^-5 at most), the same for every v. Logits beyond (the
+// type's largest and lowest values, or tiny temperatures) take the difference
+// first. m = -inf: nothing but -inf so far, whose powers are 0.
+// (Here and below, products and sums that a compiler may contract one way in one
+// instance of the kernel and another way in the next are written out, so that
+// all of them round alike.)
+constexpr float kPlain = 1048576.f;
 struct Scale {
-  float k, mk;
+  float k, m, mk;
   bool plain;
-  __device__ __forceinline__ Scale(float m, float factor) {
-    mk = __fmul_rn(m, factor);
-    plain = fabsf(mk) <= kLargest;
+  __device__ __forceinline__ Scale(float top, float factor) {
     k = factor;
-    if (!plain) {
-      k = __uint_as_float(__float_as_uint(factor) & 0x7f800000u) * 5.421010862427522e-20f;
-      mk = m == -INFINITY ? 0.f : __fmul_rn(m, k);
-    }
+    m = top == -INFINITY ? 0.f : top;
+    mk = __fmul_rn(m, k);
+    plain = fabsf(mk) <= kPlain;
   }
-  __device__ __forceinline__ float power(float v) const { return exp2_fast(fmaf(v, k, -mk)); }
+  // what the powers are relative to, over 2^(m k), as an exponent
+  __device__ __forceinline__ float left_out() const { return plain ? fmaf(m, k, -mk) : 0.f; }
+  __device__ __forceinline__ float power(float v) const {
+    return exp2_fast(plain ? fmaf(v, k, -mk) : __fmul_rn(__fadd_rn(v, -m), k));
+  }
 };
 
 // The largest logit m so far and s = sum of the powers relative to it; m = -inf, s = 0 is nothing.
 struct MaxSum {
   float m, s;
 };
-// (Products and sums that a compiler may contract one way here and another
-// way there are written out, so that every instance of the kernel rounds alike.)
 // What a sum relative to `from` is multiplied by to be relative to m >= from.
 __device__ __forceinline__ float rebase(float from, float m, float k) {
   if (from == m) return 1.f;
-  const float mk = __fmul_rn(m, k);
-  return fabsf(mk) <= kLargest ? exp2_fast(__fmul_rn(from, k) - mk) : 0.f;  // both offsets as rounded
+  if (from == -INFINITY) return 0.f;
+  const Scale a(from, k), b(m, k);
+  if (a.plain && b.plain) return exp2_fast(a.mk - b.mk);  // both as rounded
+  return exp2_fast(fmaf(from - m, k, b.left_out() - a.left_out()));
 }
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m);
@@ -202,9 +208,24 @@ struct RowPack {
       return fmaxf(fmaxf(v.get(0), v.get(1)), fmaxf(v.get(2), v.get(3)));
     }
   }
+  template <bool PLAIN>
   __device__ __forceinline__ float2 powers(int i, const Scale &f) const {
-    const float2 x = __ffma2_rn(pair(i), make_float2(f.k, f.k), make_float2(-f.mk, -f.mk));
+    const float2 v = pair(i), k = make_float2(f.k, f.k);
+    const float2 x = PLAIN ? __ffma2_rn(v, k, make_float2(-f.mk, -f.mk))
+                           : __fmul2_rn(__fadd2_rn(v, make_float2(-f.m, -f.m)), k);
     return make_float2(exp2_fast(x.x), exp2_fast(x.y));
+  }
+  template <bool PLAIN>
+  __device__ __forceinline__ float sum(const Scale &f) const {
+    float2 s = powers<PLAIN>(0, f);
+#pragma unroll
+    for (int i = 1; i < VEC / 2; ++i) s = __fadd2_rn(s, powers<PLAIN>(i, f));
+    return __fadd_rn(s.x, s.y);
+  }
+  template <bool PLAIN>
+  __device__ __forceinline__ void to_gradient(float scale, const Scale &f) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) set_pair(i, __fmul2_rn(make_float2(scale, scale), powers<PLAIN>(i, f)));
   }
 };
 
@@ -271,20 +292,27 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
     };
     for (int n = 0, j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride, n += kAhead) {
       RP v[kAhead];
+      const int left = packs.full1 - j0;  // pack u of these is there if u * stride < left
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (j0 + u * stride < packs.full1) v[u].v.load(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+        if (u * stride < left) v[u].v.load(base + static_cast<int64_t>(j0 + u * stride) * VEC);
+      float top = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (j0 + u * stride >= packs.full1) break;
-        if (GRAD && n < p.kept) keep[(n + u) * blockDim.x + threadIdx.x] = v[u].v.w[0];
-        const float top = v[u].top();
-        if (top > a.m) raise(top);
-        float2 s = v[u].powers(0, f);
+      for (int u = 0; u < kAhead; ++u)
+        if (u * stride < left) {
+          if (GRAD && n < p.kept) keep[(n + u) * blockDim.x + threadIdx.x] = v[u].v.w[0];
+          top = fmaxf(top, v[u].top());
+        }
+      if (top > a.m) raise(top);
+      auto add = [&](auto plain) {
 #pragma unroll
-        for (int i = 1; i < VEC / 2; ++i) s = __fadd2_rn(s, v[u].powers(i, f));
-        a.s = __fadd_rn(a.s, __fadd_rn(s.x, s.y));
-      }
+        for (int u = 0; u < kAhead; ++u)
+          if (u * stride < left) a.s = __fadd_rn(a.s, v[u].template sum<decltype(plain)::value>(f));
+      };
+      if (f.plain)
+        add(std::true_type());
+      else
+        add(std::false_type());
     }
     for (int c = edge0; c < edge1; ++c) {
       const float v = Elem<DT>::to_f(x[c]);
@@ -323,8 +351,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
       if (a.s != 0.f) {  // else every logit is -inf: no distribution
         const Scale f(a.m, k);
         // the powers are relative to m k as rounded
-        const float left_out = f.plain ? fmaf(a.m, k, -f.mk) : 0.f;
-        r = policy_row(p, in, (static_cast<double>(target) - a.m) * p.inv_temp + left_out * kLn2 - log_of(a.s));
+        r = policy_row(p, in, (static_cast<double>(target) - a.m) * p.inv_temp + f.left_out() * kLn2 - log_of(a.s));
       }
       res = r;
       if (rank == 0) write_result(p, t, r);
@@ -356,37 +383,42 @@ __global__ void __launch_bounds__(kMaxThreads, 2) ns_policy_kernel(const __grid_
       if (in_bounds(g + c, sizeof(E), p.dlogits, dsize, p.status)) g[c] = Elem<DT>::from_f(v);
     };
     if (live) {
-      const float2 scale2 = make_float2(scale, scale);
       const int target_pack = (y + packs.phase) / VEC;
-      for (int n = 0, j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride, n += kAhead) {
-        RP v[kAhead];
-        if (n < p.kept) {
+      auto second_pass = [&](auto plain) {
+        for (int n = 0, j0 = packs.full0 + first; j0 < packs.full1; j0 += kAhead * stride, n += kAhead) {
+          RP v[kAhead];
+          const int left = packs.full1 - j0;  // pack u of these is there if u * stride < left
+          if (n < p.kept) {
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-            if (j0 + u * stride < packs.full1) v[u].v.w[0] = keep[(n + u) * blockDim.x + threadIdx.x];
-        } else {
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-            if (j0 + u * stride < packs.full1) v[u].v.load_stream(base + static_cast<int64_t>(j0 + u * stride) * VEC);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int j = j0 + u * stride;
-          if (j >= packs.full1) break;
-          if (j != target_pack) {
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) v[u].set_pair(i, __fmul2_rn(scale2, v[u].powers(i, f)));
+            for (int u = 0; u < kAhead; ++u)
+              if (u * stride < left) v[u].v.w[0] = keep[(n + u) * blockDim.x + threadIdx.x];
           } else {
-            const int at = y + packs.phase - j * VEC;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float d = scale * f.power(v[u].v.get(e));
-              v[u].v.set(e, e == at ? d + slope : d);
-            }
+            for (int u = 0; u < kAhead; ++u)
+              if (u * stride < left) v[u].v.load_stream(base + static_cast<int64_t>(j0 + u * stride) * VEC);
           }
-          put(j, v[u]);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (u * stride >= left) break;
+            const int j = j0 + u * stride;
+            if (j != target_pack) {
+              v[u].template to_gradient<decltype(plain)::value>(scale, f);
+            } else {
+              const int at = y + packs.phase - j * VEC;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float d = scale * f.power(v[u].v.get(e));
+                v[u].v.set(e, e == at ? d + slope : d);
+              }
+            }
+            put(j, v[u]);
+          }
         }
-      }
+      };
+      if (f.plain)
+        second_pass(std::true_type());
+      else
+        second_pass(std::false_type());
       for (int c = edge0; c < edge1; ++c) {
         const float d = scale * f.power(Elem<DT>::to_f(x[c]));
         put_one(c, c == y ? d + slope : d);

@@ -306,6 +306,31 @@ def test_policy_masks_infinities_and_nan(dtype, vocab):
     assert torch.equal(bad.dlogits[keep], got.dlogits[keep]) and torch.equal(bad.logp[keep], got.logp[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [65, 40000])
+@pytest.mark.parametrize("temp", [1.0, 0.05, 40.0])
+def test_policy_rows_of_the_types_extreme_values(dtype, vocab, temp):
+    # rows of one value are uniform whatever it is: logp = -log(vocab); next to -inf or smaller values those have none
+    top, low = torch.finfo(dtype).max, torch.finfo(dtype).min
+    x = torch.empty((6, vocab), dtype=dtype, device="cuda")
+    x[0], x[1], x[2] = low, top, low
+    x[2, ::2] = -INF
+    x[3], x[4], x[5] = low, -INF, top
+    x[3, :3] = 0
+    x[4, 1] = low
+    x[5, 1::2] = 0
+    y = torch.tensor([5, 5, 5, 1, 1, 6], device="cuda")
+    live = torch.tensor([vocab, vocab, vocab // 2, 3, 1, (vocab + 1) // 2], device="cuda").double()
+    got = api.policy_loss(x, y, torch.ones(6, device="cuda"), torch.ones(6, device="cuda"), temperature=temp)
+    within(got.logp, -live.log(), policy_bounds(torch.zeros_like(x), torch.zeros_like(x).double(), 1.0))
+    # on-policy with A = 1: the gradient is softmax - onehot over the temperature
+    p = torch.zeros((6, vocab), dtype=F64, device="cuda")
+    p[0], p[1], p[2, 1::2], p[3, :3], p[4, 1], p[5, ::2] = (float(1 / n) for n in live)
+    p[torch.arange(6, device="cuda"), y] -= 1
+    # the softmax carries the sum's error (policy_bounds') and one of its own, the type one rounding
+    within(got.dlogits, p / temp, (p.abs() + (p < 0)) / temp * ((vocab / 128 + 200) * E + 2.0 ** -18 + U[dtype]))
+
+
 def test_policy_in_place_and_no_rows():
     x, y, adv, w, old, ref = make_policy(37, 30001, BF16, 5)
     a = api.policy_loss(x, y, adv, w, old_logp=old)
@@ -556,6 +581,20 @@ def test_wgrad_nan_reaches_its_columns_only():
     g = api.checkpoint_wgrad(dy, api.checkpoint_store(x), dtype=F32)[0]
     rest = torch.arange(64, device="cuda") != 5
     assert torch.isfinite(g[rest]).all() and not torch.isfinite(g[5]).any()
+
+
+def test_wgrad_fp32_beyond_bf16s_largest_value():
+    # FLT_MAX rounds to infinity in bf16: its first slice has to stop below, the rest follows in the next ones
+    r = gen(16)
+    dy, x = normal((64, 40), r), normal((64, 64), r)
+    big = torch.finfo(F32).max
+    dy[7], x[7] = big, 0.25
+    dy[8], x[8] = -big, 0.125
+    ck = api.checkpoint_store(x)
+    ref, mag = wgrad_reference(dy, ck, [0, 64])
+    got = api.checkpoint_wgrad(dy, ck)
+    assert torch.isfinite(got).all()
+    within(got, ref, wgrad_bound(mag, ref, F32, 64, F32))
 
 
 def test_wgrad_offsets_are_clamped():
