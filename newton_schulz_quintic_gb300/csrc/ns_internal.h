@@ -246,7 +246,7 @@ enum OpKind : int {
 };
 // Workspace cache slots of the operators (one scratch per operator and
 // stream, so one operator's growth never moves another's scratch).
-enum OpSlot : int { kSlotEmbed = 1000, kSlotPolicy, kSlotWgrad };
+enum OpSlot : int { kSlotEmbed = 1000, kSlotPolicy, kSlotWgrad, kSlotWgradSync };
 
 // One operator call, once its arguments are validated: holds the library's
 // lock, knows the current device (rc != NS_OK: unusable), and reaches the

@@ -6,12 +6,24 @@
 // of X is q * 2^(E - 133) with |q| <= 127, exact in bf16, so the product runs
 // at the bf16 rate with no rounding of X.
 //
-// X is widened to bf16 in scratch first, one pass over it (with fp32 dY, dY's
-// slices in the same launch). Widening inside the product, on the way to
-// shared memory, was built and measured: every tile of X is then widened
-// again for each tile row of G (32 times at 8192 x 6144), which took 2400 warp
-// instructions and 570 cycles of shared-memory traffic per 64 rows next to the
-// 512 cycles of MMA, 767 us at 8192 x 8192 x 6144.
+// X is widened to bf16 in scratch, once. Widening on the way to shared memory
+// was built and measured: every tile of X is then widened again for each tile
+// row of G (32 times at 8192 x 6144), which took 2400 warp instructions and
+// 570 cycles of shared-memory traffic per 64 rows next to the 512 cycles of
+// MMA, 767 us at 8192 x 8192 x 6144. There are two forms, to the same bits:
+//   in the product's launch (ns_wgrad_kernel<true>, when TMA reads dY as it
+//     lies): four more warps per CTA widen pieces of 64 x 256 in the order in
+//     which the tiles need them and count them; a tile is handed out once its
+//     part of X is counted. The launch is cooperative, since CTAs wait for one
+//     another's pieces.
+//   in a launch of its own before (ns_wgrad_prepare_kernel; the product sets
+//     itself up meanwhile), which also makes dY's slices.
+// The first form hides the widening behind the product, but the pieces that
+// the first tiles wait for come at half the rate: 38912 rows in 76 groups,
+// 2048 x 6144: 880 us against 900; 16384 in 8, 2048 x 2048: 120 against 128; 64 x 64
+// x 64: 13.4 against 16; but 8192 rows, 8192 x 6144: 545 against 528, and 16384, 512 x
+// 512: 42 against 38. So it is taken when what the first tiles need, counted three
+// times, is no more than all pieces and four per CTA (the second launch).
 //
 // The product is one persistent kernel of CTA pairs (clusters of 2), one 256 x
 // 256 tile of one group's G at a time (tcgen05.mma.cta_group::2, M = 256, N =
@@ -25,7 +37,8 @@
 //           nothing of the next group (infinities, NaN) takes part.
 //   3       looks the pair's tiles up (place, group, rows) a few ahead and
 //           hands them to the other warps through a small queue
-//   4..11   sums: every kChunk k-blocks the accumulator is added to fp32
+//   4..7    (first form) X to bf16
+//   last 8  sums: every kChunk k-blocks the accumulator is added to fp32
 //           registers (128 columns x 1 row per thread) while the MMAs go on in
 //           the other one; the tile is written at its end. The tensor cores'
 //           own accumulation loses up to a unit in the last place per
@@ -45,8 +58,8 @@
 // Bound by the tensor pipe: 8192 rows, 8192 x 6144 bf16 in 500 to 550 us, 1.5 to
 // 1.65 PFLOP/s (the copy to bf16 25 of them; 620 cycles a k-block, whose MMAs
 // take 512; clocks at the power cap). 76 experts of 512 rows on average, 2048 x
-// 6144: 880 to 900 us, of which the copy to bf16 takes 115 (HBM) and G's stores
-// 150 (their staging shares the shared memory that the operands already fill).
+// 6144: 875 to 885 us, of which G's stores take 150 (their staging shares the
+// shared memory that the operands already fill).
 // Every wait is bounded (mbar_wait): on a timeout the status word is set, the
 // CTA waits for its own copies and MMAs, frees TMEM and exits.
 #include <algorithm>
@@ -63,8 +76,14 @@ constexpr int kStages = 6;
 constexpr int kShare = 128 * kBK * 2;            // one operand's share of a stage: 16 KB
 constexpr int kBoxBytes = 64 * kBK * 2;          // one TMA box
 constexpr int kChunk = 8;                        // k-blocks between two drains of an accumulator
-constexpr int kThreads = 384;
-constexpr int kSum0 = 4, kSumWarps = 8;
+constexpr int kIssueWarps = 4, kWidenWarps = 4, kSumWarps = 8;
+constexpr int threads_of(bool widen) { return 32 * (kIssueWarps + (widen ? kWidenWarps : 0) + kSumWarps); }
+// Registers a thread with the widening warps: the block is launched with 128
+// each, 65536 in all, and its four warpgroups divide no more than that.
+constexpr int kRegsIssue = 56, kRegsWiden = 80, kRegsSum = 176;
+static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSum <= 4 * 128, "registers of the weight-gradient kernel");
+constexpr int kUnitRows = 64, kUnitCols = 256;   // piece of X that four warps widen at a time
+constexpr int kBlockRows = 512;                  // rows of X that one counter stands for
 constexpr int kTmemCols = 512;
 constexpr int kPatch = 32 * 32 * 4;              // staging of a block of 32 rows x 128 bytes per sum warp
 
@@ -85,6 +104,15 @@ struct WgradParams {
   int accumulate, gdtype, store;
   int *status;
   uint64_t wait_limit_ns;
+  // X as the caller holds it, when the kernel widens it itself (units > 0)
+  const int8_t *q;
+  const uint8_t *s;
+  __nv_bfloat16 *x;        // rows x pitch
+  int pitch, scale_pitch;
+  int units;               // pieces of X, the last bands' empty ones counted
+  int band_units;          // pieces of kUnitRows rows in a band of rows
+  int *widened;            // per kBlockRows rows and kUnitCols columns: pieces in place
+  int *left;               // CTAs that have ended
 };
 
 // One tile of the pair's list as warp 3 hands it out.
@@ -171,6 +199,62 @@ struct TileReader {
     return t.lo >= 0;
   }
 };
+
+// 16 values of X in bf16, exactly. e: their block's exponent.
+__device__ __forceinline__ Pack<kBF16, 16> widen16(const uint4 &w, int e) {
+  const float unit = e == 255 ? __int_as_float(0x7fc00000) : __int_as_float((max(e, 7) - 6) << 23);
+  const int8_t *q = reinterpret_cast<const int8_t *>(&w);
+  Pack<kBF16, 16> v;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) v.set(u, static_cast<float>(q[u]) * unit);
+  return v;
+}
+
+// This CTA's pieces of X, in the order in which the tiles need them: bands of
+// rows (all of them for one group, else about a group's), in a band column by
+// column. thread: 0..127.
+__device__ __forceinline__ void widen(const WgradParams &p, int thread) {
+  constexpr int kAcross = kUnitCols / 16, kStep = kWidenWarps * 32 / kAcross, kLoads = kUnitRows / kStep;
+  const size_t size = static_cast<size_t>(p.rows) * p.pitch * 2;
+  const int per_band = p.band_units * p.tk;
+  for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const int band = u / per_band, in = u - band * per_band;
+    const int col = in / p.band_units, piece = band * p.band_units + in - col * p.band_units;
+    const int row0 = piece * kUnitRows, c = col * kUnitCols + thread % kAcross * 16, r0 = row0 + thread / kAcross;
+    if (row0 >= p.rows) continue;
+    if (c < p.pitch) {
+      uint4 w[kLoads];
+      int e[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kStep;
+        if (r < p.rows) {
+          w[i] = __ldcs(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(r) * p.pitch + c));
+          e[i] = p.s[static_cast<int64_t>(r) * p.scale_pitch + c / 32];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kStep;
+        if (r < p.rows) widen16(w[i], e[i]).store(p.x + static_cast<int64_t>(r) * p.pitch + c, p.x, size, p.status);
+      }
+    }
+    fence_proxy_async_global();  // TMA reads it
+    asm volatile("bar.sync 1, %0;" ::"n"(kWidenWarps * 32) : "memory");
+    if (thread == 0) red_release_gpu_add(p.widened + row0 / kBlockRows * p.tk + col, 1);
+  }
+}
+
+// Whether tile t's part of X is in place; the whole warp waits for it.
+__device__ __forceinline__ bool wait_widened(const WgradParams &p, const WTile &t, const Waiter &w) {
+  int ok = 1;
+  if (t.lo < t.hi)
+    for (int b = t.lo / kBlockRows + (threadIdx.x & 31); b <= (t.hi - 1) / kBlockRows; b += 32) {
+      const int pieces = min(kBlockRows / kUnitRows, (p.rows - b * kBlockRows + kUnitRows - 1) / kUnitRows);
+      ok = ok && wait_count(p.widened + b * p.tk + t.k0 / kUnitCols, pieces, w);
+    }
+  return __all_sync(0xffffffffu, ok);
+}
 
 // The k-blocks of a tile in order: chunks of kChunk blocks, in each the
 // slices of dY from smallest to largest, in each slice the chunk's blocks.
@@ -321,7 +405,9 @@ __device__ __forceinline__ void store_plain(const WgradParams &p, int e, int row
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_constant__ WgradParams p) {
+template <bool kWiden>
+__global__ void __launch_bounds__(threads_of(kWiden), 1) ns_wgrad_kernel(const __grid_constant__ WgradParams p) {
+  constexpr int kSum0 = kIssueWarps + (kWiden ? kWidenWarps : 0);
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned, by an offset so that accesses stay in the shared window
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -366,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   volatile int *abort = &bar->abort;
   const Waiter w{abort, p.status, p.wait_limit_ns};
 
+  if (kWiden && warp < kIssueWarps)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
   if (tmem_ok && warp == 0) {
     // ---------------------------------------------------- operands by TMA, issued by one lane
     if (lane == 0) {
@@ -379,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
         const bool ok = for_blocks(t, p.slices, [&](int block, int z) {
           if (!mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w)) return false;
           mbar_arrive_expect_tx(&bar->full[stage], 2 * kShare);
+          if (kWiden && block == 0) fence_proxy_async_global();  // X was written by this launch's threads
           const int y = t.lo + block * kBK;
           uint8_t *a = sA + stage * kShare, *b = sB + stage * kShare;
           tma_load_3d(a, &p.tm_dy, t.n0 + x, y, z, &bar->full[stage]);
@@ -476,28 +565,35 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
     }
   } else if (tmem_ok && warp == 3) {
     // ---------------------------------------------------- the pair's tiles, looked up ahead
-    if (lane == 0) {
-      int slot = 0;
-      uint32_t parity = 0;
-      bool more = true;
-      for (int item = pair; more; item += npairs) {
-        WTile t;
-        more = item < p.items;
-        if (more)
-          t = look_up(p, item);
-        else
-          t.lo = -1;
-        if (!mbar_wait(&bar->qempty[slot], parity ^ 1u, w)) break;
+    int slot = 0;
+    uint32_t parity = 0;
+    bool more = true;
+    for (int item = pair; more; item += npairs) {
+      WTile t;
+      more = item < p.items;
+      if (more)
+        t = look_up(p, item);
+      else
+        t.lo = -1;
+      if (kWiden && more && !wait_widened(p, t, w)) break;
+      __syncwarp();  // orders the other lanes' looks at the counters before lane 0's arrival
+      if (!warp_mbar_wait<false>(&bar->qempty[slot], parity ^ 1u, w)) break;
+      if (lane == 0) {
         bar->queue[slot] = t;
         mbar_arrive(&bar->qfull[slot]);
-        if (++slot == kQueue) {
-          slot = 0;
-          parity ^= 1u;
-        }
+      }
+      if (++slot == kQueue) {
+        slot = 0;
+        parity ^= 1u;
       }
     }
+  } else if (kWiden && warp >= kIssueWarps && warp < kSum0) {
+    // ---------------------------------------------------- X to bf16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    widen(p, threadIdx.x - kIssueWarps * 32);
   } else if (tmem_ok && warp >= kSum0) {
     // ---------------------------------------------------- sums and the tile's store
+    if (kWiden) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
     const int e = warp - kSum0, quarter = warp & 3, half = e >> 2;
     uint8_t *patch = patches + e * kPatch;
     int acc = 0;
@@ -564,6 +660,19 @@ __global__ void __launch_bounds__(kThreads, 1) ns_wgrad_kernel(const __grid_cons
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+  if (kWiden && warp == 2) {  // the last CTA leaves the counters at 0 for the next call
+    int n = 0;
+    if (lane == 0) {
+      __threadfence();  // this CTA's counting is done before it counts itself
+      n = atomicAdd(p.left, 1);
+      __threadfence();
+    }
+    if (__shfl_sync(0xffffffffu, n, 0) == static_cast<int>(gridDim.x) - 1) {
+      const int counters = (p.rows + kBlockRows - 1) / kBlockRows * p.tk;
+      for (int i = lane; i < counters; i += 32) p.widened[i] = 0;
+      if (lane == 0) *p.left = 0;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ around the product
@@ -607,13 +716,7 @@ __global__ void __launch_bounds__(256) ns_wgrad_prepare_kernel(const __grid_cons
       const int64_t r = i / per_row;
       const int c = static_cast<int>(i - r * per_row) * 16;
       const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.q + r * p.pitch + c));
-      const int e = p.s[r * p.scale_pitch + c / 32];
-      const float unit = e == 255 ? __int_as_float(0x7fc00000) : __int_as_float((max(e, 7) - 6) << 23);
-      const int8_t *q = reinterpret_cast<const int8_t *>(&w);
-      Pack<kBF16, 16> v;
-#pragma unroll
-      for (int u = 0; u < 16; ++u) v.set(u, static_cast<float>(q[u]) * unit);
-      v.store(p.x + r * p.pitch + c, p.x, xsize, p.status);
+      widen16(w, p.s[r * p.scale_pitch + c / 32]).store(p.x + r * p.pitch + c, p.x, xsize, p.status);
       continue;
     }
     const int64_t k = i - nx, r = k / dy_row;
@@ -684,19 +787,29 @@ int run_prepare(const PrepareParams &p, int dtype, int sms, cudaStream_t s) {
 }
 
 // CTA pairs that can be resident at once on this device (one CTA per SM).
+template <bool kWiden>
 int resident_pairs(int dev, int sms, cudaLaunchConfig_t &cfg) {
   static int cached[64] = {};
   int &n = cached[dev & 63];
   if (n == 0) {
     static SmemOptIn opt_in;
-    if (opt_in.ensure(reinterpret_cast<const void *>(ns_wgrad_kernel), kSmem)) return 0;
+    if (opt_in.ensure(reinterpret_cast<const void *>(ns_wgrad_kernel<kWiden>), kSmem)) return 0;
     cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&n, ns_wgrad_kernel, &cfg) != cudaSuccess || n <= 0) {
+    cfg.blockDim = dim3(threads_of(kWiden), 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&n, ns_wgrad_kernel<kWiden>, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       n = 0;
     }
   }
   return n;
+}
+
+// Pieces of X that the first `pairs` tiles of the list need.
+int64_t first_wave_pieces(const WgradParams &p, int pairs) {
+  const int64_t wave = std::min(pairs, p.items), per_group = static_cast<int64_t>(p.tn) * p.tk * p.splits;
+  if (wave > per_group) return (wave + per_group - 1) / per_group * p.band_units * p.tk;
+  const int64_t column = static_cast<int64_t>(std::min(p.tn, 8)) * p.splits;  // tiles of one column of a band
+  return std::min<int64_t>(p.tk, (wave + column - 1) / column) * p.band_units;
 }
 
 int run_join(const WgradParams &p, int sms, cudaStream_t s) {
@@ -766,12 +879,11 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
   // it starts while the preparation still runs and waits for it (griddepcontrol)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = call.s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int pairs = resident_pairs(call.dev, call.sms, cfg);
+  const int pairs = std::min(resident_pairs<false>(call.dev, call.sms, cfg), resident_pairs<true>(call.dev, call.sms, cfg));
   if (pairs <= 0) return NS_ECUDA;
   const int64_t tiles = static_cast<int64_t>(groups) * k.tn * k.tk;
   // Fewer tiles than half the pairs: parts of the rows, of one drain interval
@@ -811,11 +923,29 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
     if ((rc = call.tensor_map(&k.tm_dy, 2, direct ? dy : ws + x_bytes, 3, dims, strides, box))) return rc;
     const int64_t xdims[2] = {n_in, rows}, xstride[1] = {q_pitch * 2};
     if ((rc = call.tensor_map(&k.tm_x, 2, ws, 2, xdims, xstride, box))) return rc;
+    k.q = static_cast<const int8_t *>(q);
+    k.s = static_cast<const uint8_t *>(scales);
+    k.x = reinterpret_cast<__nv_bfloat16 *>(ws);
+    k.pitch = static_cast<int>(q_pitch);
+    k.scale_pitch = static_cast<int>(scale_pitch);
+    const int64_t pieces = (rows + kUnitRows - 1) / kUnitRows;
+    k.band_units = static_cast<int>(std::max<int64_t>(1, pieces / groups));
+    const int64_t units = (pieces + k.band_units - 1) / k.band_units * k.band_units * k.tk;
+    if (direct && units <= INT32_MAX / 2 && 3 * first_wave_pieces(k, pairs) <= units + 4ll * 2 * pairs) {
+      k.units = static_cast<int>(units);
+      uint8_t *sync = nullptr;
+      bool fresh = false;  // counters that every call leaves at 0
+      const size_t bytes = 256 + static_cast<size_t>((rows + kBlockRows - 1) / kBlockRows) * k.tk * 4;
+      if ((rc = call.workspace(kSlotWgradSync, bytes, &sync, &fresh))) return rc;
+      if (fresh && cudaMemsetAsync(sync, 0, bytes, call.s) != cudaSuccess) return NS_ECUDA;
+      k.left = reinterpret_cast<int *>(sync);
+      k.widened = reinterpret_cast<int *>(sync + 256);
+    }
     PrepareParams pp{static_cast<const int8_t *>(q), static_cast<const uint8_t *>(scales),
                      reinterpret_cast<__nv_bfloat16 *>(ws), direct ? nullptr : dy,
                      reinterpret_cast<__nv_bfloat16 *>(ws + x_bytes), ld_dy, k.rows, k.n_in, static_cast<int>(q_pitch),
                      static_cast<int>(scale_pitch), k.n_out, static_cast<int>(pitch), k.slices, k.status};
-    if ((rc = call.launch(kOpWgrad, [&] { return run_prepare(pp, dtype, call.sms, call.s); }))) return rc;
+    if (k.units == 0 && (rc = call.launch(kOpWgrad, [&] { return run_prepare(pp, dtype, call.sms, call.s); }))) return rc;
   }
   if (k.store != kStorePlain) {
     const bool f32 = k.splits > 1 || grad_dtype == NS_F32;
@@ -825,10 +955,15 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
     if ((rc = call.tensor_map(&k.tm_out, f32 ? 4 : 2, k.splits > 1 ? static_cast<void *>(k.parts) : grad, 3, dims, strides, box)))
       return rc;
   }
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(pairs, k.items)), 1, 1);
+  if (k.units > 0) {  // CTAs that wait for one another's pieces of X: all resident at once
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(pairs, std::max(k.items, (k.units + 1) / 2))), 1, 1);
   cfg.numAttrs = rows > 0 ? 2 : 1;
+  cfg.blockDim = dim3(threads_of(k.units > 0), 1, 1);
   rc = call.launch(kOpWgrad, [&] {
-    if (cudaLaunchKernelEx(&cfg, ns_wgrad_kernel, k) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, k.units > 0 ? ns_wgrad_kernel<true> : ns_wgrad_kernel<false>, k) != cudaSuccess) {
       cudaGetLastError();
       return -1;
     }

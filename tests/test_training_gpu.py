@@ -597,6 +597,35 @@ def test_wgrad_fp32_beyond_bf16s_largest_value():
     within(got, ref, wgrad_bound(mag, ref, F32, 64, F32))
 
 
+def test_wgrad_widens_x_the_same_way_in_one_launch_and_before():
+    # a bf16 dY whose rows TMA reads has X widened within the product's launch, one off 16 bytes before it; the
+    # sizes follow one another on a stream, larger and smaller, so each call has to leave its counters as it found them
+    for t, n, k, groups in [(70, 40, 64, 1), (3000, 600, 1000, 5), (1, 8, 32, 1), (2100, 264, 520, 3), (3000, 600, 1000, 5),
+                            (513, 1032, 2304, 1), (70, 40, 64, 1)]:
+        r = gen(t + n + k)
+        dy, ck = normal((t, n), r, BF16), api.checkpoint_store(normal((t, k), r))
+        cuts = [0] + sorted(torch.randint(0, t + 1, (groups - 1,), generator=torch.Generator().manual_seed(t)).tolist()) + [t]
+        offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda") if groups > 1 else None
+        got = api.checkpoint_wgrad(dy, ck, offsets=offsets, dtype=F32)
+        ref, mag = wgrad_reference(dy, ck, cuts)
+        within(got, ref, wgrad_bound(mag, ref, F32, t, BF16))
+        view, _ = padded(dy, 3, 1)
+        assert torch.equal(got, api.checkpoint_wgrad(view, ck, offsets=offsets, dtype=F32))
+    graph, out = torch.cuda.CUDAGraph(), torch.zeros_like(got)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        api.checkpoint_wgrad(dy, ck, grad=out, stream=side)
+    side.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        api.checkpoint_wgrad(dy, ck, grad=out, stream=side)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+
+
 def test_wgrad_offsets_are_clamped():
     r = gen(13)
     dy, ck = normal((50, 32), r, BF16), api.checkpoint_store(normal((50, 64), r))
