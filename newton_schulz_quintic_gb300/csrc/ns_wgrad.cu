@@ -19,11 +19,12 @@
 //   in a launch of its own before (ns_wgrad_prepare_kernel; the product sets
 //     itself up meanwhile), which also makes dY's slices.
 // The first form hides the widening behind the product, but the pieces that
-// the first tiles wait for come at half the rate: 38912 rows in 76 groups,
-// 2048 x 6144: 880 us against 900; 16384 in 8, 2048 x 2048: 120 against 128; 64 x 64
-// x 64: 13.4 against 16; but 8192 rows, 8192 x 6144: 545 against 528, and 16384, 512 x
-// 512: 42 against 38. So it is taken when what the first tiles need, counted three
-// times, is no more than all pieces and four per CTA (the second launch).
+// the first tiles wait for come at a lower rate than with all threads: 8192 rows,
+// 8192 x 6144: 513 us against 522; 38912 rows in 76 groups, 2048 x 6144: 848 against
+// 880; 4096 rows, 4096 x 4096: 96 against 104; 64 rows, 64 x 64: 12.8 against 16; but
+// 16384 rows, 512 x 512, where the first tiles need all: 40 against 38. So it is
+// taken when what the first tiles need, counted one and a half times, is no more
+// than all pieces and one per CTA (the second launch).
 //
 // The product is one persistent kernel of CTA pairs (clusters of 2), one 256 x
 // 256 tile of one group's G at a time (tcgen05.mma.cta_group::2, M = 256, N =
@@ -55,11 +56,14 @@
 // rows are split and the parts, fp32 in scratch, are added in order by a
 // second kernel.
 //
-// Bound by the tensor pipe: 8192 rows, 8192 x 6144 bf16 in 500 to 550 us, 1.5 to
-// 1.65 PFLOP/s (the copy to bf16 25 of them; 620 cycles a k-block, whose MMAs
-// take 512; clocks at the power cap). 76 experts of 512 rows on average, 2048 x
-// 6144: 875 to 885 us, of which G's stores take 150 (their staging shares the
-// shared memory that the operands already fill).
+// One elected lane issues the copies and the MMAs (elect.sync, which tells the
+// compiler that one lane runs there: with a test for lane 0 the MMAs of the same
+// loop were issued 4 % slower at 8192 rows, 8192 x 6144, 7 % with the registers divided).
+//
+// Bound by the tensor pipe: 8192 rows, 8192 x 6144 bf16 in 500 to 525 us, 1.57 to
+// 1.65 PFLOP/s at power-capped clocks; 4096 x 4096 x 4096 in 96 us. 76 experts of 512
+// rows on average, 2048 x 6144: 848 us, of which G's stores take 150 (their
+// staging shares the shared memory that the operands already fill).
 // Every wait is bounded (mbar_wait): on a timeout the status word is set, the
 // CTA waits for its own copies and MMAs, frees TMEM and exits.
 #include <algorithm>
@@ -78,10 +82,16 @@ constexpr int kBoxBytes = 64 * kBK * 2;          // one TMA box
 constexpr int kChunk = 8;                        // k-blocks between two drains of an accumulator
 constexpr int kIssueWarps = 4, kWidenWarps = 4, kSumWarps = 8;
 constexpr int threads_of(bool widen) { return 32 * (kIssueWarps + (widen ? kWidenWarps : 0) + kSumWarps); }
-// Registers a thread with the widening warps: the block is launched with 128
-// each, 65536 in all, and its four warpgroups divide no more than that.
-constexpr int kRegsIssue = 56, kRegsWiden = 80, kRegsSum = 176;
-static_assert(kRegsIssue + kRegsWiden + 2 * kRegsSum <= 4 * 128, "registers of the weight-gradient kernel");
+// Registers a thread: the block is launched with one number for all (168 or
+// 128), which its warpgroups then divide again. The built kernel is checked for
+// it before its first launch: a share beyond what the launch holds would never
+// be granted. Without the division the sums spill: bf16 sums added to 4096 x 4096 in
+// 143 us against 148.
+template <bool kWiden>
+struct Regs {
+  static constexpr int kIssue = 56, kWidening = 80, kSum = 176;
+  static constexpr int kTotal = 128 * (kIssue + (kWiden ? kWidening : 0) + 2 * kSum);
+};
 constexpr int kUnitRows = 64, kUnitCols = 256;   // piece of X that four warps widen at a time
 constexpr int kBlockRows = 512;                  // rows of X that one counter stands for
 constexpr int kTmemCols = 512;
@@ -452,11 +462,11 @@ __global__ void __launch_bounds__(threads_of(kWiden), 1) ns_wgrad_kernel(const _
   volatile int *abort = &bar->abort;
   const Waiter w{abort, p.status, p.wait_limit_ns};
 
-  if (kWiden && warp < kIssueWarps)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+  if (warp < kIssueWarps)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kWiden>::kIssue));
   if (tmem_ok && warp == 0) {
     // ---------------------------------------------------- operands by TMA, issued by one lane
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t parity = 0;
       uint32_t issued = 0, last = 0;  // per stage: whether copies were issued, the parity of the last
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(threads_of(kWiden), 1) ns_wgrad_kernel(const _
     }
   } else if (tmem_ok && warp == 1 && leader) {
     // ---------------------------------------------------- MMAs, issued by one lane
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = umma_idesc_bf16(256, 256, 1, 1);
       const uint64_t desc_a = sw128_mnmajor_desc(smem_u32(sA)), desc_b = sw128_mnmajor_desc(smem_u32(sB));
       int stage = 0, acc = 0;
@@ -589,11 +599,11 @@ __global__ void __launch_bounds__(threads_of(kWiden), 1) ns_wgrad_kernel(const _
     }
   } else if (kWiden && warp >= kIssueWarps && warp < kSum0) {
     // ---------------------------------------------------- X to bf16
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kWiden>::kWidening));
     widen(p, threadIdx.x - kIssueWarps * 32);
   } else if (tmem_ok && warp >= kSum0) {
     // ---------------------------------------------------- sums and the tile's store
-    if (kWiden) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kWiden>::kSum));
     const int e = warp - kSum0, quarter = warp & 3, half = e >> 2;
     uint8_t *patch = patches + e * kPatch;
     int acc = 0;
@@ -794,6 +804,12 @@ int resident_pairs(int dev, int sms, cudaLaunchConfig_t &cfg) {
   if (n == 0) {
     static SmemOptIn opt_in;
     if (opt_in.ensure(reinterpret_cast<const void *>(ns_wgrad_kernel<kWiden>), kSmem)) return 0;
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, ns_wgrad_kernel<kWiden>) != cudaSuccess ||
+        attr.numRegs * threads_of(kWiden) < Regs<kWiden>::kTotal) {
+      cudaGetLastError();
+      return 0;
+    }
     cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
     cfg.blockDim = dim3(threads_of(kWiden), 1, 1);
     if (cudaOccupancyMaxActiveClusters(&n, ns_wgrad_kernel<kWiden>, &cfg) != cudaSuccess || n <= 0) {
@@ -931,7 +947,7 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
     const int64_t pieces = (rows + kUnitRows - 1) / kUnitRows;
     k.band_units = static_cast<int>(std::max<int64_t>(1, pieces / groups));
     const int64_t units = (pieces + k.band_units - 1) / k.band_units * k.band_units * k.tk;
-    if (direct && units <= INT32_MAX / 2 && 3 * first_wave_pieces(k, pairs) <= units + 4ll * 2 * pairs) {
+    if (direct && units <= INT32_MAX / 2 && 3 * first_wave_pieces(k, pairs) <= 2 * (units + 2ll * pairs)) {
       k.units = static_cast<int>(units);
       uint8_t *sync = nullptr;
       bool fresh = false;  // counters that every call leaves at 0
