@@ -120,6 +120,13 @@ def _same_device(device, *tensors):
 
 
 # ------------------------------------------------------------------ embedding
+def _flat(ids):
+    """``ids`` in one dimension. For a view that is not contiguous this is a copy
+    by a kernel of its own: made inside _on's block, it runs on the call's
+    stream before the call's kernels, and its memory belongs to that stream."""
+    return ids if ids.dim() == 1 else ids.reshape(-1)
+
+
 def embed_lookup(table, ids, scale: float = 1.0, out=None, stream=None):
     """``out[t] = scale * table[ids[t]]`` (ns_embed_lookup). ``table`` is vocab x
     dim; ``ids`` an int32 or int64 tensor of any shape. Ids outside the
@@ -128,10 +135,10 @@ def embed_lookup(table, ids, scale: float = 1.0, out=None, stream=None):
     ld = _matrix(table, "table")
     vocab, dim = table.shape
     dev, dt = table.device, table.dtype
-    flat = ids if ids.dim() == 1 else ids.reshape(-1)
-    n = flat.shape[0]
-    p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
+    n = ids.numel()
     with _on(dev, stream):
+        flat = _flat(ids)
+        p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
         if out is None:
             out, ld_out = _empty((*ids.shape, dim), dtype=dt, device=dev), dim
         else:
@@ -152,8 +159,6 @@ def embed_grad(dout, ids, vocab: int | None = None, scale: float = 1.0, grad=Non
     ld = _matrix(dout, "dout")
     n, dim = dout.shape
     dev = dout.device
-    flat = ids if ids.dim() == 1 else ids.reshape(-1)
-    p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
     if grad is None:
         if accumulate or vocab is None:
             raise ValueError("without grad, give vocab and do not accumulate")
@@ -163,6 +168,8 @@ def embed_grad(dout, ids, vocab: int | None = None, scale: float = 1.0, grad=Non
         _same_device(dev, grad)
         ld_grad = _matrix(grad, "grad", None, dim, dtype)
     with _on(dev, stream):
+        flat = _flat(ids)
+        p_ids = _vector(flat, "ids", n, _IDTYPE, dev)
         if grad is None:
             grad = _empty((int(vocab), dim), dtype=dtype or dout.dtype, device=dev)
             ld_grad = _matrix(grad, "grad")
