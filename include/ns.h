@@ -36,7 +36,13 @@
  *    graph on that stream and replayed. The library keeps the descriptor
  *    tables of the last 8 distinct batches per stream on the device, so a
  *    caller alternating between a few batches (e.g. remainder batches) also
- *    uploads nothing after the first call of each.
+ *    uploads nothing after the first call of each. What a captured call uses
+ *    of the workspace cache stays allocated for its graph until
+ *    ns_release_workspace, whatever later calls on that stream need. All
+ *    calls on one stream share that scratch, the captured ones among them:
+ *    replays of graphs captured on a stream must not run at the same time as
+ *    one another or as later calls on that stream (replay them on it, or order
+ *    them otherwise).
  */
 #ifndef NS_H_
 #define NS_H_
@@ -195,8 +201,14 @@ int ns_muon_update_batched(void *const *G, void *const *Mom, void *const *Out, c
  * rounded once. Results are the same bits from call to call: no sum's order
  * depends on the schedule. Outputs must not overlap inputs or each other
  * unless stated (NS_EINVAL). Scratch comes from the internal per-(device,
- * stream) workspace cache; once a call of the same sizes has run on a stream,
- * a repeat allocates nothing and may be captured into a CUDA graph.
+ * stream) workspace cache, one block per operator that grows to the largest
+ * call: ns_embed_grad of more than 1024 ids 16 bytes an id and 8 bytes a column
+ * for every 16 to 64 ids, ns_policy_loss 4 bytes a row, ns_ckpt_wgrad 2 bytes
+ * per value of X, 2 (bf16 that TMA cannot address) or 6 (fp32) per value of
+ * dY, and 4 per value of G and part when the rows are split between CTAs; the
+ * others none. Once a call of the same sizes has run on a stream, a repeat
+ * allocates nothing and may be captured into a CUDA graph, on the terms at the
+ * top of this file.
  */
 
 /* types of token ids and targets */
@@ -395,7 +407,8 @@ const char *ns_strerror(int code);
 
 /*
  * ns_release_workspace -- synchronise the device and free the internal
- * workspace cache of the current device. Returns NS_OK or NS_ECUDA.
+ * workspace cache of the current device, which ends the use of every graph
+ * that holds captured calls. Returns NS_OK or NS_ECUDA.
  */
 int ns_release_workspace(void);
 

@@ -520,11 +520,75 @@ struct CachedWs {
   size_t bytes = 0;
   std::vector<DevBlob> blobs;  // tables whose pointers refer to this scratch
   uint64_t uses = 0;
+  // A captured call's graph keeps the addresses of the scratch and of the
+  // tables. Once a capture has used this scratch, it and the tables are kept
+  // when they are replaced, not freed, until ns_release_workspace.
+  bool captured = false;
+  std::vector<uint8_t *> kept;
 };
 
+bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &st) == cudaSuccess) return st != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  return false;
+}
+
+// A block of the cache that no later call uses.
+int drop_block(CachedWs &c, uint8_t *p, cudaStream_t s) {
+  if (c.captured) {
+    c.kept.push_back(p);
+    return NS_OK;
+  }
+  return cudaFreeAsync(p, s) == cudaSuccess ? NS_OK : NS_ECUDA;
+}
+
 void drop_blobs(CachedWs &c, cudaStream_t s) {
-  for (DevBlob &b : c.blobs) cudaFreeAsync(b.ptr, s);
+  for (DevBlob &b : c.blobs) drop_block(c, b.ptr, s);
   c.blobs.clear();
+}
+
+// A device block for calls on stream s, its first `fill` bytes copied from
+// `from`, or zero where that is nullptr; ordered on s. While s is being
+// captured the block is made and filled outside the capture, at once: inside,
+// it would be memory that exists only while the graph runs, filled only by it,
+// and calls outside the graph use it too.
+int new_block(uint8_t **out, size_t bytes, const void *from, size_t fill, cudaStream_t s) {
+  g_allocations.fetch_add(1, std::memory_order_relaxed);
+  void *p = nullptr;
+  auto fill_on = [&](cudaStream_t on) {
+    if (fill == 0) return cudaSuccess;
+    return from ? cudaMemcpyAsync(p, from, fill, cudaMemcpyHostToDevice, on) : cudaMemsetAsync(p, 0, fill, on);
+  };
+  int rc = NS_OK;
+  if (!capturing(s)) {
+    if (cudaMallocAsync(&p, bytes, s) != cudaSuccess) {
+      cudaGetLastError();
+      return NS_ENOMEM;
+    }
+    if (fill_on(s) != cudaSuccess) {
+      cudaFreeAsync(p, s);
+      rc = NS_ECUDA;
+    }
+  } else {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return NS_ECUDA;
+    cudaStream_t own = nullptr;
+    if (cudaMalloc(&p, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      rc = NS_ENOMEM;
+    } else if (fill > 0) {
+      if (cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) != cudaSuccess || fill_on(own) != cudaSuccess ||
+          cudaStreamSynchronize(own) != cudaSuccess) {
+        cudaFree(p);
+        rc = NS_ECUDA;
+      }
+      if (own) cudaStreamDestroy(own);
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+  }
+  if (rc == NS_OK) *out = static_cast<uint8_t *>(p);
+  return rc;
 }
 // keyed by (device, stream, slot): slot 0 serves the device entry points,
 // slot 1 holds the host entry point's device copies, slot 2 + g the workspace
@@ -541,23 +605,22 @@ struct WsKey {
 };
 std::map<WsKey, CachedWs> g_ws;
 
-int ensure_ws(CachedWs &c, size_t bytes, cudaStream_t s) {
+// The cached scratch grown to `bytes`; its first `zero` bytes are zero when it
+// is made.
+int ensure_ws(CachedWs &c, size_t bytes, cudaStream_t s, size_t zero = 0) {
+  const bool now = capturing(s);
+  c.captured = c.captured || now;
   if (c.ptr && c.bytes >= bytes) return NS_OK;
   const size_t limit = g_ws_limit.load();
   if (limit && bytes > limit) return NS_ENOMEM;  // refused before any allocation
   drop_blobs(c, s);  // their descriptors point into the old scratch
   if (c.ptr) {
-    if (cudaFreeAsync(c.ptr, s) != cudaSuccess) return NS_ECUDA;
+    if (const int rc = drop_block(c, c.ptr, s)) return rc;
     c.ptr = nullptr;
     c.bytes = 0;
   }
-  void *p = nullptr;
-  g_allocations.fetch_add(1, std::memory_order_relaxed);
-  if (cudaMallocAsync(&p, bytes, s) != cudaSuccess) {
-    cudaGetLastError();
-    return NS_ENOMEM;
-  }
-  c.ptr = static_cast<uint8_t *>(p);
+  c.captured = now;
+  if (const int rc = new_block(&c.ptr, bytes, nullptr, zero, s)) return rc;
   c.bytes = bytes;
   return NS_OK;
 }
@@ -783,6 +846,7 @@ int run(void *const *X, const int64_t *shapes, int count, int steps, const float
     key = call_key(X, shapes, count, steps, dtype);
     for (DevBlob &b : c.blobs)
       if (b.layout && b.key == key) {
+        c.captured = c.captured || capturing(s);
         b.last_use = ++c.uses;
         return execute(*b.layout, c.ptr, b.ptr, steps, co, table, eps, di, s, opt);
       }
@@ -819,21 +883,11 @@ int run(void *const *X, const int64_t *shapes, int count, int steps, const float
       if (cache->blobs.size() >= kBlobsPerWs) {  // evict the least recently used table (stream-ordered free)
         auto lru = std::min_element(cache->blobs.begin(), cache->blobs.end(),
                                     [](const DevBlob &a, const DevBlob &b) { return a.last_use < b.last_use; });
-        cudaFreeAsync(lru->ptr, s);
+        drop_block(*cache, lru->ptr, s);
         cache->blobs.erase(lru);
       }
-      void *p = nullptr;
-      g_allocations.fetch_add(1, std::memory_order_relaxed);
-      if (cudaMallocAsync(&p, std::max<size_t>(blob.size(), 256), s) != cudaSuccess) {
-        cudaGetLastError();
-        return NS_ENOMEM;
-      }
-      if (cudaMemcpyAsync(p, blob.data(), blob.size(), cudaMemcpyHostToDevice, s) != cudaSuccess) {
-        cudaFreeAsync(p, s);
-        return NS_ECUDA;
-      }
       DevBlob nb;
-      nb.ptr = static_cast<uint8_t *>(p);
+      if ((rc = new_block(&nb.ptr, std::max<size_t>(blob.size(), 256), blob.data(), blob.size(), s))) return rc;
       nb.bytes = std::move(blob);
       cache->blobs.push_back(std::move(nb));
       hit = &cache->blobs.back();
@@ -904,11 +958,10 @@ OpCall::~OpCall() {
   if (ranged) nvtxRangePop();
 }
 
-int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr, bool *fresh) {
+int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr, size_t zero) {
   try {
     CachedWs &c = g_ws[WsKey{dev, s, slot}];
-    if (fresh) *fresh = !(c.ptr && c.bytes >= std::max<size_t>(bytes, 256));
-    const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s);
+    const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s, zero);
     *ptr = c.ptr;
     return e;
   } catch (...) {
@@ -1206,6 +1259,7 @@ int ns_release_workspace(void) {
   for (auto it = g_ws.begin(); it != g_ws.end();) {
     if (it->first.dev == dev) {
       for (DevBlob &b : it->second.blobs) cudaFree(b.ptr);
+      for (uint8_t *p : it->second.kept) cudaFree(p);
       if (it->second.ptr) cudaFree(it->second.ptr);
       it = g_ws.erase(it);
     } else {

@@ -261,8 +261,8 @@ struct OpCall {
   bool ranged = false;
   explicit OpCall(void *stream);
   ~OpCall();
-  // fresh: whether this call allocated it (its contents are then undefined)
-  int workspace(int slot, size_t bytes, uint8_t **ptr, bool *fresh = nullptr);
+  // at least `bytes`; when this call allocates it, its first `zero` bytes are zero
+  int workspace(int slot, size_t bytes, uint8_t **ptr, size_t zero = 0);
   // elt 2: bf16, elt 4: fp32; 128-byte swizzle; reads outside give 0, writes outside are dropped
   int tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
                  const int64_t *pitch_bytes, const int *box);

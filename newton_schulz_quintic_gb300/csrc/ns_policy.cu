@@ -525,9 +525,7 @@ int policy_call(PolicyParams &p, int dtype, void *stream) {
   if (p.weight) {
     uint8_t *ws = nullptr;
     // a counter that every call leaves at 0, then the rows' losses
-    bool fresh = false;
-    if (const int rc = call.workspace(kSlotPolicy, 256 + static_cast<size_t>(p.rows) * 4, &ws, &fresh)) return rc;
-    if (fresh && cudaMemsetAsync(ws, 0, 256, call.s) != cudaSuccess) return NS_ECUDA;
+    if (const int rc = call.workspace(kSlotPolicy, 256 + static_cast<size_t>(p.rows) * 4, &ws, 256)) return rc;
     p.done = reinterpret_cast<int *>(ws);
     p.row_loss = reinterpret_cast<float *>(ws + 256);
   }

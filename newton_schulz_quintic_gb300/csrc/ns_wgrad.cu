@@ -967,11 +967,9 @@ extern "C" int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_
     const int64_t units = (pieces + k.band_units - 1) / k.band_units * k.band_units * k.tk;
     if (direct && units <= INT32_MAX / 2 && 3 * first_wave_pieces(k, pairs) <= 2 * (units + 2ll * pairs)) {
       k.units = static_cast<int>(units);
-      uint8_t *sync = nullptr;
-      bool fresh = false;  // counters that every call leaves at 0
+      uint8_t *sync = nullptr;  // counters that every call leaves at 0
       const size_t bytes = 256 + static_cast<size_t>((rows + kBlockRows - 1) / kBlockRows) * k.tk * 4;
-      if ((rc = call.workspace(kSlotWgradSync, bytes, &sync, &fresh))) return rc;
-      if (fresh && cudaMemsetAsync(sync, 0, bytes, call.s) != cudaSuccess) return NS_ECUDA;
+      if ((rc = call.workspace(kSlotWgradSync, bytes, &sync, bytes))) return rc;
       k.left = reinterpret_cast<int *>(sync);
       k.widened = reinterpret_cast<int *>(sync + 256);
     }

@@ -56,3 +56,64 @@ def test_sliced_ids_on_another_stream():
             s.synchronize()  # the current stream still sleeps
             assert torch.equal(a.cpu().view(-1, dim), looked_up.cpu()) and torch.equal(b.cpu(), grad.cpu())
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ graphs
+def step_inputs(seed, rows, vocab, t, n, k, ids):
+    r = gen(seed)
+    x, y = normal((rows, vocab), r, BF16), torch.randint(0, vocab, (rows,), device="cuda", generator=r)
+    dy, ck = normal((t, n), r, BF16), api.checkpoint_store(normal((t, k), r))
+    tokens, dout = torch.randint(0, 700, (ids,), device="cuda", generator=r), normal((ids, 64), r, BF16)
+    mats = [normal((n, k), r, BF16), normal((24, 200), r, BF16)]
+
+    def go():
+        p = api.policy_loss(x, y, torch.ones(rows, device="cuda"), torch.ones(rows, device="cuda"))
+        out = [m.clone() for m in mats]
+        return [p.loss, p.logp, p.dlogits, api.checkpoint_wgrad(dy, ck, dtype=F32),
+                api.embed_grad(dout, tokens, vocab=700), out], out
+    return go
+
+
+def run_step(go, mats=None):
+    got, out = go()
+    api.orthogonalize_batched(mats if mats is not None else out)
+    return got[:-1] + list(mats if mats is not None else out)
+
+
+@pytest.mark.parametrize("warm", [True, False])
+def test_a_graph_outlives_larger_calls_on_its_stream(warm):
+    # every operator with scratch of its own (and the orthogonalization) is captured small; larger calls on the same
+    # stream then replace that scratch, and the graph's addresses have to stay good: its loss is summed by counters that
+    # start at 0, its weight gradient waits for counters of its own. Without a call before the capture, the scratch
+    # made during it serves the calls behind it too.
+    small = step_inputs(5, 40, 3000, 600, 264, 520, 1500)
+    large = step_inputs(6, 900, 3000, 9000, 1032, 1544, 40000)
+    ref, ref_large = run_step(small), run_step(large)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    mats = small()[1]
+    start = [m.clone() for m in mats]
+    graph = torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        if warm:
+            run_step(small, mats)
+    s.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        out = run_step(small, mats)
+    with torch.cuda.stream(s):
+        if not warm:  # calls of the captured sizes, before the graph ever runs
+            assert all(torch.equal(a, b) for a, b in zip(ref, run_step(small)))
+        for k in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(ref_large, run_step(large)))
+            for a, b in zip(mats, start):
+                a.copy_(b)
+            for a in out[:-2]:
+                a.zero_()
+            graph.replay()
+            s.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(ref, out)), k
+            for m in range(9):  # more batches than the cache keeps tables of
+                api.orthogonalize_batched([torch.ones((64 + m, 256), device="cuda", dtype=BF16)])
+    s.synchronize()
+    assert api.get_status() == 0
