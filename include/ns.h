@@ -267,7 +267,8 @@ int ns_token_logprobs(const void *logits, int64_t ld_logits, int64_t rows, int64
  * A row is masked when its target is outside [0, vocab), its weight is 0 or its
  * logits are all -infinity: it adds nothing to the loss, its logp and kl are
  * 0, its gradient row is zero, and (but for the last case) its logits and its
- * other inputs are not looked at, whatever they hold. kl_coef, clip_low,
+ * other inputs are not looked at, whatever they hold. A NaN in any input of
+ * another row makes the loss and the row's gradient NaN. kl_coef, clip_low,
  * clip_high finite and >= 0, inv_temperature finite and > 0.
  */
 int ns_policy_loss(const void *logits, int64_t ld_logits, int64_t rows, int64_t vocab, const void *targets,

@@ -134,19 +134,35 @@ __device__ __forceinline__ RowInputs row_inputs(const PolicyParams &p, int64_t t
   return r;
 }
 
+// The smaller and the larger of two, NaN where either is (fminf and fmaxf take the other).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // The row's outputs from its target's log probability.
 __device__ __forceinline__ RowResult policy_row(const PolicyParams &p, const RowInputs &in, double logp) {
   RowResult r{static_cast<float>(logp), 0.f, 0.f, 0.f};
   if (!p.weight) return r;
-  const float ratio = p.old_logp ? expf(static_cast<float>(logp - in.old_logp)) : 1.f;
-  const float a = ratio * in.advantage, b = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * in.advantage;
-  float slope = a <= b ? -a : 0.f;
+  const float apart = p.old_logp ? static_cast<float>(logp - in.old_logp) : 0.f;
+  const float ratio = p.old_logp ? expf(apart) : 1.f;
+  // a ratio beyond fp32's largest value is finite all the same, and 0 times no advantage
+  const float a = in.advantage == 0.f && fabsf(apart) <= kLargest ? 0.f : ratio * in.advantage;
+  const float b = min_nan(max_nan(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * in.advantage;
+  const float gain = min_nan(a, b);
+  float slope = a <= b ? -a : a > b ? 0.f : gain;  // neither: NaN
   if (p.ref_logp) {
     const float d = static_cast<float>(in.ref_logp - logp), e = expm1f(d);
     r.kl = e - d;
     slope -= p.kl_coef * e;
   }
-  r.loss = in.weight * (p.kl_coef * r.kl - fminf(a, b));
+  r.loss = in.weight * (p.kl_coef * r.kl - gain);
   r.slope = in.weight * slope * p.inv_temp;
   return r;
 }

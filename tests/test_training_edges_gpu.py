@@ -117,3 +117,47 @@ def test_a_graph_outlives_larger_calls_on_its_stream(warm):
                 api.orthogonalize_batched([torch.ones((64 + m, 256), device="cuda", dtype=BF16)])
     s.synchronize()
     assert api.get_status() == 0
+
+
+# ------------------------------------------------------------------ policy loss
+def policy_rows(vocab, dtype, seed=7, n=8):
+    g = gen(seed)
+    x, y = normal((n, vocab), g, dtype, 2.0), torch.randint(0, vocab, (n,), device="cuda", generator=g)
+    one = torch.ones(n, device="cuda")
+    return x, y, one, api.token_logprobs(x, y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [65, 40001])
+@pytest.mark.parametrize("where,ref", [(w, r) for w in ("logits", "old", "advantage", "weight") for r in (True, False)]
+                         + [("ref", True)])
+@pytest.mark.parametrize("advantage", [1.0, -1.0, 0.0])
+def test_policy_nan_of_a_live_row_reaches_the_loss(dtype, vocab, where, ref, advantage):
+    # min(r A, clip(r) A) and clip(r) are NaN where r or A is; what is NaN must not read as a clipped ratio
+    x, y, one, lp = policy_rows(vocab, dtype)
+    given = dict(old=lp + 0.1, ref=lp - 0.1, advantage=one * advantage, weight=one.clone())
+    call = lambda **kw: api.policy_loss(x, y, given["advantage"], given["weight"], old_logp=given["old"],  # noqa: E731
+                                        ref_logp=given["ref"] if ref else None, kl_coef=0.1 if ref else 0.0, **kw)
+    clean = call()
+    assert torch.isfinite(clean.loss) and torch.isfinite(clean.dlogits).all()
+    if where == "logits":
+        x[3, (int(y[3]) + 7) % vocab] = NAN
+    else:
+        given[where][3] = NAN
+    got, alone = call(), call(grad=False)
+    assert torch.isnan(got.loss) and torch.isnan(alone.loss)
+    assert torch.isnan(got.dlogits[3]).all()
+    assert bool(torch.isnan(got.logp[3])) == (where == "logits")
+    keep = torch.arange(8, device="cuda") != 3
+    for a, b in ((got.dlogits, clean.dlogits), (got.logp, clean.logp), (got.kl, clean.kl)):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_policy_overflowing_ratio_without_advantage():
+    # r = exp(logp - old) beyond fp32's largest value times A = 0 is 0; times another A it is what the clip leaves
+    x, y, one, lp = policy_rows(300, F32)
+    old = lp - 120.0
+    none = api.policy_loss(x, y, one * 0, one, old_logp=old)
+    assert float(none.loss) == 0 and torch.all(none.dlogits == 0)
+    up = api.policy_loss(x, y, one, one, old_logp=old, clip_high=0.25)
+    assert float(up.loss) == -8 * 1.25 and torch.all(up.dlogits == 0)
