@@ -268,8 +268,9 @@ int ns_token_logprobs(const void *logits, int64_t ld_logits, int64_t rows, int64
  * logits are all -infinity: it adds nothing to the loss, its logp and kl are
  * 0, its gradient row is zero, and (but for the last case) its logits and its
  * other inputs are not looked at, whatever they hold. A NaN in any input of
- * another row makes the loss and the row's gradient NaN. kl_coef, clip_low,
- * clip_high finite and >= 0, inv_temperature finite and > 0.
+ * another row makes the loss and the row's gradient NaN; but with kl_coef 0 the
+ * KL term has no part in them, whatever k is, and is only written. kl_coef,
+ * clip_low, clip_high finite and >= 0, inv_temperature finite and > 0.
  */
 int ns_policy_loss(const void *logits, int64_t ld_logits, int64_t rows, int64_t vocab, const void *targets,
                    int id_type, const float *old_logp, const float *ref_logp, const float *advantage,

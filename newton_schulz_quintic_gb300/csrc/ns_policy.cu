@@ -160,9 +160,9 @@ __device__ __forceinline__ RowResult policy_row(const PolicyParams &p, const Row
   if (p.ref_logp) {
     const float d = static_cast<float>(in.ref_logp - logp), e = expm1f(d);
     r.kl = e - d;
-    slope -= p.kl_coef * e;
+    if (p.kl_coef != 0.f) slope -= p.kl_coef * e;  // 0 times a term beyond fp32's range is NaN
   }
-  r.loss = in.weight * (p.kl_coef * r.kl - gain);
+  r.loss = in.weight * ((p.kl_coef != 0.f ? p.kl_coef * r.kl : 0.f) - gain);
   r.slope = in.weight * slope * p.inv_temp;
   return r;
 }

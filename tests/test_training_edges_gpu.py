@@ -161,3 +161,22 @@ def test_policy_overflowing_ratio_without_advantage():
     assert float(none.loss) == 0 and torch.all(none.dlogits == 0)
     up = api.policy_loss(x, y, one, one, old_logp=old, clip_high=0.25)
     assert float(up.loss) == -8 * 1.25 and torch.all(up.dlogits == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_policy_kl_far_apart_without_its_coefficient(dtype):
+    # kl_coef = 0: the term is watched, not trained on. k beyond fp32's largest value (its row's target has become
+    # impossible next to the reference) is written as infinity and leaves loss and gradient as they are without it
+    x, y, one, lp = policy_rows(500, dtype)
+    ref = lp.clone()
+    ref[1], ref[2] = lp[1] + 95, lp[2] + 1000
+    got = api.policy_loss(x, y, one, one, old_logp=lp, ref_logp=ref, kl_coef=0.0)
+    plain = api.policy_loss(x, y, one, one, old_logp=lp)
+    assert torch.equal(got.loss, plain.loss) and torch.equal(got.dlogits, plain.dlogits)
+    # logp is written rounded to fp32: d is up to 2^-21 there, k is d^2 / 2 and a rounding of d
+    assert torch.isinf(got.kl[1:3]).all() and torch.all(got.kl[3:].abs() <= 2.0 ** -40)
+    x[4, int(y[4])] = -INF  # the target's own logit
+    got = api.policy_loss(x, y, one, one, ref_logp=ref, kl_coef=0.0)
+    plain = api.policy_loss(x, y, one, one)
+    assert torch.equal(got.loss, plain.loss) and torch.equal(got.dlogits, plain.dlogits)
+    assert torch.isfinite(got.loss) and torch.isfinite(got.dlogits).all()
