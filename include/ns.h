@@ -61,7 +61,8 @@ extern "C" {
 /* status codes */
 #define NS_OK 0
 #define NS_EINVAL (-1)   /* null pointer, negative dims/count/steps, bad dtype, a side above
-                            2^30 - 1 or a matrix above 2^40 elements, overlapping matrices */
+                            2^30 - 1 or a matrix above 2^40 elements (training operators: the
+                            limits they state), overlapping matrices */
 #define NS_EALIGN (-2)   /* a pointer is not aligned to its element size (8-bit checkpoints: 16 bytes) */
 #define NS_ENOMEM (-3)   /* workspace allocation failed / caller workspace too small */
 #define NS_ECUDA (-4)    /* a CUDA runtime or driver call failed */
@@ -219,7 +220,9 @@ int ns_muon_update_batched(void *const *G, void *const *Mom, void *const *Out, c
  * ns_embed_lookup -- Out[t, :] = scale * Table[ids[t], :] for `count` ids.
  *   table  vocab x dim of dtype; ids: count integers of id_type on the device;
  *   out    count x dim of dtype.
- * An id outside [0, vocab) is padding: its row of Out is zero.
+ * An id outside [0, vocab) is padding: its row of Out is zero. dim < 2^30;
+ * here and below, other sides and pitches are at most 2^31 - 1 and 2^31 unless
+ * stated, and a matrix spans at most 2^46 elements.
  */
 int ns_embed_lookup(const void *table, int64_t ld_table, int64_t vocab, int64_t dim, const void *ids, int id_type,
                     int64_t count, float scale, void *out, int64_t ld_out, int dtype, void *stream);
@@ -233,7 +236,8 @@ int ns_embed_lookup(const void *table, int64_t ld_table, int64_t vocab, int64_t 
  *   NS_BF16, whatever dtype is).
  * Sums run in fp32 over the positions in a fixed order and are rounded once.
  * Ids outside [0, vocab) have no gradient; their rows of dOut are not read.
- * count <= 2^30, vocab < 2^31 - 1, dim <= 2^24, count * dim below 2^43.
+ * count <= 2^30, vocab < 2^31 - 1, dim <= 2^24, (count / 16 + 1) *
+ * (dim / 128 + 1) < 2^31 (count * dim up to about 2^42).
  */
 int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids, int id_type, int64_t count, float scale,
                   void *grad, int64_t ld_grad, int64_t vocab, int64_t dim, int dtype, int grad_dtype, int accumulate,
@@ -245,6 +249,7 @@ int ns_embed_grad(const void *dout, int64_t ld_dout, const void *ids, int id_typ
  * `vocab` logits. A row whose target is outside [0, vocab) is masked: its
  * logits are not read and its logp is 0. A row of logits that are all
  * -infinity holds no distribution and gives 0 as well. logp: rows floats.
+ * vocab < 2^30 (ns_policy_loss too).
  */
 int ns_token_logprobs(const void *logits, int64_t ld_logits, int64_t rows, int64_t vocab, const void *targets,
                       int id_type, float inv_temperature, float *logp, int dtype, void *stream);
@@ -336,7 +341,8 @@ int ns_gated_backward(const void *dh, int64_t ld_dh, const void *q_gate, const v
  * are exact to 2^-24). Rows of other groups never reach a group's sum,
  * whatever they hold. Sums in fp32: the tensor cores' accumulators are added
  * to fp32 registers every 512 rows (their own sum loses up to a unit in the
- * last place per instruction).
+ * last place per instruction). rows, n_out and n_in <= 2^30, groups * n_out *
+ * n_in <= 2^42.
  */
 int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_t n_out, const void *q, const void *scales,
                   int64_t n_in, const int32_t *offsets, int groups, void *grad, int dtype, int grad_dtype,

@@ -561,7 +561,7 @@ extern "C" int ns_embed_lookup(const void *table, int64_t ld_table, int64_t voca
                                int id_type, int64_t count, float scale, void *out, int64_t ld_out, int dtype,
                                void *stream) {
   if ((dtype != NS_F32 && dtype != NS_BF16) || (id_type != NS_I32 && id_type != NS_I64)) return NS_EINVAL;
-  if (bad_shape(vocab, dim, ld_table) || bad_shape(count, dim, ld_out)) return NS_EINVAL;
+  if (bad_shape(vocab, dim, ld_table) || bad_shape(count, dim, ld_out) || dim > kMaxRowCols) return NS_EINVAL;
   if (count == 0 || dim == 0) return NS_OK;
   if (!ids || !out || (!table && vocab > 0)) return NS_EINVAL;
   const int elt = dtype == NS_BF16 ? 2 : 4;

@@ -290,6 +290,8 @@ inline bool bad_shape(int64_t rows, int64_t cols, int64_t ld) {
   if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || ld < cols || ld > (int64_t(1) << 31)) return true;
   return rows > 0 && ld > 0 && rows > (int64_t(1) << 46) / ld;
 }
+// Most columns of a row where columns are counted in 32 bits, with room for rounding up.
+constexpr int64_t kMaxRowCols = (int64_t(1) << 30) - 1;
 inline bool misaligned(const void *p, int to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
 }  // namespace ns

@@ -559,7 +559,7 @@ extern "C" int ns_token_logprobs(const void *logits, int64_t ld_logits, int64_t 
                                  const void *targets, int id_type, float inv_temperature, float *logp, int dtype,
                                  void *stream) {
   if ((dtype != NS_F32 && dtype != NS_BF16) || (id_type != NS_I32 && id_type != NS_I64)) return NS_EINVAL;
-  if (bad_shape(rows, vocab, ld_logits) || !std::isfinite(inv_temperature) || inv_temperature <= 0) return NS_EINVAL;
+  if (bad_shape(rows, vocab, ld_logits) || vocab > kMaxRowCols || !std::isfinite(inv_temperature) || inv_temperature <= 0) return NS_EINVAL;
   if (rows == 0) return NS_OK;
   if (!targets || !logp || (vocab > 0 && !logits)) return NS_EINVAL;
   const int elt = dtype == NS_BF16 ? 2 : 4, ielt = id_type == NS_I64 ? 8 : 4;
@@ -584,7 +584,8 @@ extern "C" int ns_policy_loss(const void *logits, int64_t ld_logits, int64_t row
                               float clip_high, float kl_coef, float *loss, float *logp, float *kl, void *dlogits,
                               int64_t ld_dlogits, int dtype, void *stream) {
   if ((dtype != NS_F32 && dtype != NS_BF16) || (id_type != NS_I32 && id_type != NS_I64)) return NS_EINVAL;
-  if (bad_shape(rows, vocab, ld_logits) || (dlogits && bad_shape(rows, vocab, ld_dlogits))) return NS_EINVAL;
+  if (bad_shape(rows, vocab, ld_logits) || (dlogits && bad_shape(rows, vocab, ld_dlogits)) || vocab > kMaxRowCols)
+    return NS_EINVAL;
   if (!std::isfinite(inv_temperature) || inv_temperature <= 0 || !std::isfinite(clip_low) || !std::isfinite(clip_high) ||
       !std::isfinite(kl_coef) || clip_low < 0 || clip_high < 0 || kl_coef < 0)
     return NS_EINVAL;

@@ -154,3 +154,21 @@ def test_python_layer_rejects_before_the_library():
         api.Checkpoint8(torch.zeros((4, 16), dtype=torch.int8), torch.zeros((4, 4), dtype=torch.uint8), 16)  # CPU
     with pytest.raises(ValueError):
         api.token_logprobs(x, ids)
+
+
+@NO_GPU
+def test_sides_at_their_limits(call):
+    # a row's columns are counted in 32 bits with room for what rounding up adds: at most 2^30 - 1 of them
+    most, ld = (1 << 30) - 1, 1 << 30
+    far = 1 << 44  # beyond what a row of that length spans
+    lookup = lambda dim: call("ns_embed_lookup", LOOKUP, dim=dim, ld=ld, ldo=ld, vocab=2, count=2, ids=far, out=2 * far)  # noqa: E731
+    assert lookup(most) == ENODEV and lookup(most + 1) == EINVAL
+    logp = lambda v: call("ns_token_logprobs", LOGP, vocab=v, ld=ld, rows=2, y=far, logp=2 * far)  # noqa: E731
+    assert logp(most) == ENODEV and logp(most + 1) == EINVAL
+    away = {k: far + 4096 * i for i, k in enumerate(("y", "old", "ref", "adv", "w", "loss", "logp", "kl"))}
+    loss = lambda v: call("ns_policy_loss", POLICY, vocab=v, ld=ld, ldd=ld, rows=2, d=2 * far, **away)  # noqa: E731
+    assert loss(most) == ENODEV and loss(most + 1) == EINVAL
+    # the pieces of the table's gradient: (count / 16 + 1) * (dim / 128 + 1) below 2^31, 2^42 values
+    grad = lambda n, dim: call("ns_embed_grad", GRAD, count=n, dim=dim, ld=dim, ldg=dim, vocab=2, ids=far * 2, grad=far * 4)  # noqa: E731
+    assert grad(1 << 30, 3840) == ENODEV and grad(1 << 30, 3968) == EINVAL and grad((1 << 30) + 1, 64) == EINVAL
+    assert grad(1 << 20, 1 << 21) == ENODEV and grad(8, (1 << 24) + 1) == EINVAL
