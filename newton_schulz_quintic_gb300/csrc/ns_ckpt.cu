@@ -191,11 +191,25 @@ __device__ __forceinline__ void write_row(const CkptParams &p, int which, int64_
   }
 }
 
-// 1 / (1 + exp(-x)) to a few units in the last place of fp32 (fp32 data), or
-// within |x| of them (bf16 data, far below its rounding)
+// 1 / (1 + exp(-x)). The fast division holds for divisors up to 2^126 and gives
+// 0 beyond, where x is below -87.3 and the value 2^-126; so neither form divides
+// by 1 + exp(-x) itself. fp32 data: below zero t / (1 + t) with t = exp(x), to a
+// few units in the last place (of the smallest subnormal, where that is more).
+// bf16 data: both sides of the fraction times 2^-24, which the exponential's
+// argument takes in, to within 24 + |x| units of fp32, far below bf16's rounding.
+// 16384 x 14336 bf16 both ways: 654 us (681 in the form for fp32); 8192 x 14336 fp32: 244
+// us forward, 332 backward.
 template <int DT>
 __device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.f, 1.f + (DT == kF32 ? expf(-x) : __expf(-x)));
+  if constexpr (DT == kF32) {
+    const float t = expf(-fabsf(x));
+    return __fdividef(x >= 0.f ? 1.f : t, 1.f + t);
+  } else {
+    constexpr float kLog2e = 1.44269504088896340736f, kDown = 1.f / 16777216.f;
+    float t;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(x, -kLog2e, -24.f)));
+    return __fdividef(kDown, kDown + t);
+  }
 }
 
 enum Op : int { kStore, kLoad, kForward, kBackward };

@@ -180,3 +180,30 @@ def test_policy_kl_far_apart_without_its_coefficient(dtype):
     plain = api.policy_loss(x, y, one, one)
     assert torch.equal(got.loss, plain.loss) and torch.equal(got.dlogits, plain.dlogits)
     assert torch.isfinite(got.loss) and torch.isfinite(got.dlogits).all()
+
+
+# ------------------------------------------------------------------ gated activation
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gate_far_below_zero(dtype):
+    # silu(g) = g s with s = 1 / (1 + exp(-g)), about exp(g): below g = -87.3 s is a subnormal, above its smallest down
+    # to -103; large values of up carry it back into range. As test_gated, and s and g s rounded to 2^-149
+    gate = torch.linspace(-104, -80, 24 * 64, device="cuda").view(24, 64).to(dtype)
+    up = torch.full_like(gate, 1e30)
+    dh = normal((24, 64), gen(9), dtype)
+    h, a, b = api.gated_forward(gate, up)
+
+    def near(got, ref, g, far):
+        bound = ref.abs() * ((12 + 2 * g.abs()) * 2 * E + U[dtype] * (1 + 2 ** -7)) + far * (2 * g.abs() + 2) * 2.0 ** -149
+        assert torch.all((got.double() - ref).abs() <= bound)
+
+    g, u = gate.double(), up.double()
+    ref = g * torch.sigmoid(g) * u
+    assert float(ref.abs().min()) > 1e-15
+    near(h, ref, g, u)
+    dgu, again = api.gated_backward(dh, a, b)
+    g, u = api.checkpoint_load(a, dtype=F32).double(), api.checkpoint_load(b, dtype=F32).double()
+    s, d = torch.sigmoid(g), dh.double()
+    near(again, g * s * u, g, u)
+    if dtype == F32:  # du = d g s without up lies below bf16's normal range
+        near(dgu[:, 64:], d * g * s, g, d.abs() + 1)
+    near(dgu[:, :64], d * u * (s + g * s * (1 - s)), g, (d * u).abs())
