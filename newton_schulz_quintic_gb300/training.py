@@ -275,7 +275,13 @@ class Checkpoint8:
 
     @classmethod
     def empty(cls, rows: int, cols: int, device):
-        """Room for a matrix, in one allocation, uninitialised."""
+        """Room for a matrix, in one allocation, uninitialised, on a CUDA device."""
+        if not isinstance(device, torch.device):
+            device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("a checkpoint must be on a CUDA device")
+        if device.index is None:
+            device = torch.device("cuda", _current_device())
         return cls._empties(1, rows, cols, device)[0]
 
     @classmethod
@@ -321,7 +327,7 @@ def checkpoint_store(x, stream=None) -> Checkpoint8:
     rows, cols = x.shape
     dev = x.device
     with _on(dev, stream):
-        ck = Checkpoint8.empty(rows, cols, dev)
+        ck, = Checkpoint8._empties(1, rows, cols, dev)
         _call("ns_ckpt_store", x.data_ptr(), ld, rows, cols, ck._p_q, ck._p_scales, _DTYPE[x.dtype],
               _raw_stream(dev.index))
     return ck

@@ -16,7 +16,8 @@ class Stub:
     is_cuda, device = True, DEV
 
     def __init__(self, shape, dtype, log=None, contiguous=True):
-        self.shape, self.dtype, self.log, self.contiguous = tuple(shape), dtype, log, contiguous
+        self.shape = (shape,) if isinstance(shape, int) else tuple(shape)
+        self.dtype, self.log, self.contiguous = dtype, log, contiguous
 
     def dim(self):
         return len(self.shape)
@@ -68,3 +69,19 @@ def test_ids_are_copied_on_the_stream_of_the_call(log, stream):
     log.clear()
     training.embed_grad(Stub((24, 8), torch.float32), ids, vocab=50, stream=stream)
     assert log == [("enter", DEV, stream), "copy", "ns_embed_grad", "exit"]
+
+
+@pytest.mark.parametrize("device", [DEV, "cuda:0", "cuda", torch.device("cuda"), 0])
+def test_an_empty_checkpoint_knows_its_device(log, monkeypatch, device):
+    # whatever names the device, calls compare it with tensors' and take its index
+    monkeypatch.setattr(training, "_current_device", lambda: 0)
+    ck = training.Checkpoint8.empty(4, 40, device)
+    assert ck.device == DEV and ck.device.index == 0
+    training.checkpoint_load(ck)
+    training.checkpoint_wgrad(Stub((4, 8), torch.float32), ck)
+    assert [e for e in log if isinstance(e, str) and e != "exit"] == ["ns_ckpt_load", "ns_ckpt_wgrad"]
+
+
+def test_an_empty_checkpoint_is_on_a_gpu(log):
+    with pytest.raises(ValueError):
+        training.Checkpoint8.empty(4, 40, "cpu")
