@@ -201,7 +201,8 @@ int ns_muon_update_batched(void *const *G, void *const *Mom, void *const *Out, c
  * dtype NS_F32 or NS_BF16; arithmetic and every sum in fp32, each output
  * rounded once. Results are the same bits from call to call: no sum's order
  * depends on the schedule. Outputs must not overlap inputs or each other
- * unless stated (NS_EINVAL). Scratch comes from the internal per-(device,
+ * unless stated (NS_EINVAL); column ranges of one buffer, with its pitch, do
+ * not. Scratch comes from the internal per-(device,
  * stream) workspace cache, one block per operator that grows to the largest
  * call: ns_embed_grad of more than 1024 ids 16 bytes an id and 8 bytes a column
  * for every 16 to 64 ids, ns_policy_loss 4 bytes a row, ns_ckpt_wgrad 2 bytes

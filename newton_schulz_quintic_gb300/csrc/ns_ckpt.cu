@@ -322,15 +322,6 @@ int ckpt_call(CkptParams &p, int dtype, bool wide, void *stream) {
 bool bad_dtype(int dtype) { return dtype != NS_F32 && dtype != NS_BF16; }
 constexpr int64_t kMaxCols = int64_t(1) << 30;
 
-// Two rows x cols matrices with one pitch: disjoint, or the interleaved halves of wider rows.
-bool halves_overlap(const void *a, const void *b, int64_t rows, int64_t cols, int64_t ld, int elt) {
-  if (!Range(a, rows, cols, ld, elt).overlaps(Range(b, rows, cols, ld, elt))) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t d = x < y ? y - x : x - y;
-  const uintptr_t in_row = d % (static_cast<uintptr_t>(ld) * elt);  // d is less than a matrix: some row lies beside another
-  return in_row < static_cast<uintptr_t>(cols) * elt || in_row > static_cast<uintptr_t>(ld - cols) * elt;
-}
-
 }  // namespace
 }  // namespace ns
 
@@ -438,7 +429,7 @@ extern "C" int ns_gated_backward(const void *dh, int64_t ld_dh, const void *q_ga
   for (const Range &o : out)
     for (const Range &i : in)
       if (o.overlaps(i)) return NS_EINVAL;
-  if (out[2].overlaps(out[0]) || out[2].overlaps(out[1]) || halves_overlap(dgate, dup, rows, cols, ld_d, elt)) return NS_EINVAL;
+  if (out[2].overlaps(out[0]) || out[2].overlaps(out[1]) || out[0].overlaps(out[1])) return NS_EINVAL;
   p.in[0] = dh;
   p.ld_in = ld_dh;
   p.out[0] = dgate;

@@ -276,13 +276,24 @@ struct OpCall {
   int timed_launch(int kind, int (*fn)(void *), void *arg);
 };
 
-// Byte range of a rows x cols matrix with a row pitch, for overlap checks.
+// The bytes of a rows x cols matrix with a row pitch, for overlap checks.
 struct Range {
   uintptr_t begin, end;
+  uintptr_t row, pitch;
   Range(const void *p, int64_t rows, int64_t cols, int64_t ld, int elt)
       : begin(reinterpret_cast<uintptr_t>(p)),
-        end(begin + (p && rows > 0 && cols > 0 ? static_cast<uintptr_t>((rows - 1) * ld + cols) * elt : 0)) {}
-  bool overlaps(const Range &o) const { return begin < o.end && o.begin < end; }
+        end(begin + (p && rows > 0 && cols > 0 ? static_cast<uintptr_t>((rows - 1) * ld + cols) * elt : 0)),
+        row(static_cast<uintptr_t>(cols) * elt),
+        pitch(static_cast<uintptr_t>(ld) * elt) {}
+  // Whether the two share a byte. Of two with one pitch (columns of one buffer, say) the rows of the second lie at the
+  // same place between the first one's rows throughout; of other pitches the spans decide.
+  bool overlaps(const Range &o) const {
+    if (!(begin < o.end && o.begin < end)) return false;
+    if (pitch != o.pitch) return true;
+    const Range &a = begin <= o.begin ? *this : o, &b = begin <= o.begin ? o : *this;
+    const uintptr_t at = (b.begin - a.begin) % pitch;  // spans that meet have rows, and a pitch
+    return at < a.row || at + b.row > pitch;
+  }
 };
 // Shape checks shared by the operators: sides in [0, 2^31), a pitch no shorter
 // than the row, fewer than 2^46 elements spanned.

@@ -172,3 +172,23 @@ def test_sides_at_their_limits(call):
     grad = lambda n, dim: call("ns_embed_grad", GRAD, count=n, dim=dim, ld=dim, ldg=dim, vocab=2, ids=far * 2, grad=far * 4)  # noqa: E731
     assert grad(1 << 30, 3840) == ENODEV and grad(1 << 30, 3968) == EINVAL and grad((1 << 30) + 1, 64) == EINVAL
     assert grad(1 << 20, 1 << 21) == ENODEV and grad(8, (1 << 24) + 1) == EINVAL
+
+
+@NO_GPU
+def test_columns_of_one_buffer_side_by_side(call):
+    # matrices whose rows interleave in one buffer share no element: inputs and outputs may be columns of it
+    def both(name, good, inside, outside):
+        for change in inside:
+            assert call(name, good, **change) == ENODEV, change
+        for change in outside:
+            assert call(name, good, **change) == EINVAL, change
+    wide = dict(ld=256, ldo=256)  # rows of 64 bf16 values, 512 bytes apart
+    both("ns_embed_lookup", LOOKUP, [dict(wide, out=A + 128), dict(wide, out=A + 384), dict(wide, out=A - 128), dict(wide, out=A + 5 * 512 + 128)],
+         [dict(wide, out=A + 126), dict(wide, out=A + 386), dict(wide, out=A - 126), dict(wide, out=A + 5 * 512 + 126), dict(wide, out=A),
+          dict(ld=256, ldo=128, out=A + 128)])
+    wide = dict(ld=200, ldd=200)  # 100 values in 400 bytes
+    both("ns_policy_loss", POLICY, [dict(wide, d=A + 200), dict(wide, d=A - 200)], [dict(wide, d=A + 198), dict(wide, d=A + 202)])
+    wide = dict(ld=192, ldh=192)  # gate, up and h
+    both("ns_gated_forward", FORWARD, [dict(wide, h=A + 256)], [dict(wide, h=A + 254), dict(wide, h=A + 258), dict(wide, h=A + 128)])
+    wide = dict(ld=256, ldd=256, ldh=256, dh=B + 384)  # dgate, dup, h and dh
+    both("ns_gated_backward", BACKWARD, [dict(wide, h=B + 256)], [dict(wide, h=B + 254), dict(wide, h=B + 258), dict(wide, h=B + 384)])

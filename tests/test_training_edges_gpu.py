@@ -207,3 +207,31 @@ def test_gate_far_below_zero(dtype):
     if dtype == F32:  # du = d g s without up lies below bf16's normal range
         near(dgu[:, 64:], d * g * s, g, d.abs() + 1)
     near(dgu[:, :64], d * u * (s + g * s * (1 - s)), g, (d * u).abs())
+
+
+# ------------------------------------------------------------------ buffers
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("f", [64, 63])
+def test_inputs_and_outputs_in_columns_of_one_buffer(dtype, f):
+    g = gen(11)
+    n = 37
+    buf = normal((n, 4 * f), g, dtype)
+    a, b, c, d = (buf[:, k * f:(k + 1) * f] for k in range(4))
+    h, ck_a, ck_b = api.gated_forward(a, b)
+    kept = buf.clone()
+    api.gated_forward(a, b, out=c)
+    assert torch.equal(c, h) and torch.equal(buf[:, :2 * f], kept[:, :2 * f]) and torch.equal(d, kept[:, 3 * f:])
+    ref, _ = api.gated_backward(d, ck_a, ck_b)
+    api.gated_backward(d, ck_a, ck_b, dgu=buf[:, :2 * f])
+    assert torch.equal(buf[:, :2 * f], ref) and torch.equal(c, h) and torch.equal(d, kept[:, 3 * f:])
+    ids = torch.randint(-1, n, (n,), device="cuda", generator=g)
+    ref = api.embed_lookup(a, ids)
+    api.embed_lookup(a, ids, out=b)
+    assert torch.equal(b, ref) and torch.equal(c, h)
+    ref = api.embed_grad(a, ids, vocab=n)
+    api.embed_grad(a, ids, grad=c)
+    assert torch.equal(c, ref) and torch.equal(d, kept[:, 3 * f:])
+    y, one = torch.randint(0, f, (n,), device="cuda", generator=g), torch.ones(n, device="cuda")
+    ref = api.policy_loss(d, y, one, one)
+    got = api.policy_loss(d, y, one, one, dlogits=b)
+    assert torch.equal(b, ref.dlogits) and torch.equal(got.loss, ref.loss) and torch.equal(c, api.embed_grad(a, ids, vocab=n))
