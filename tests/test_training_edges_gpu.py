@@ -2,6 +2,11 @@
 values are out of the ordinary. Tolerances as in test_training_gpu.py: U is the
 unit roundoff of the output type, E = 2^-24 that of fp32 arithmetic."""
 import math
+import os
+import subprocess
+import sys
+import textwrap
+import threading
 
 import pytest
 import torch
@@ -9,6 +14,7 @@ import torch
 from newton_schulz_quintic_gb300 import api
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
 U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
@@ -235,3 +241,180 @@ def test_inputs_and_outputs_in_columns_of_one_buffer(dtype, f):
     ref = api.policy_loss(d, y, one, one)
     got = api.policy_loss(d, y, one, one, dlogits=b)
     assert torch.equal(b, ref.dlogits) and torch.equal(got.loss, ref.loss) and torch.equal(c, api.embed_grad(a, ids, vocab=n))
+
+
+# ------------------------------------------------------------------ long rows, long lists, many elements
+def padded(x, extra):
+    """x as a view with `extra` elements more between its rows, one element into its buffer."""
+    n, m = x.shape
+    v = torch.full((n * (m + extra) + 64,), 7.0, dtype=x.dtype, device=x.device)[1:1 + n * (m + extra)].view(n, m + extra)[:, :m]
+    v.copy_(x)
+    return v
+
+
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("n,vocab,dim,extra", [(3000, 700, 2304, 0), (3000, 50, 1543, 0), (1025, 3, 4096, 0), (5000, 300, 2048, 3),
+                                               (20000, 7, 1032, 0)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_of_long_lists_and_several_column_ranges(dtype, gdtype, n, vocab, dim, extra, accumulate):
+    # more than 1024 positions and rows longer than a CTA covers (1024 bf16 or 512 fp32 columns in pieces, 512 or 128 in
+    # joins); a third of the positions share one id, whose run crosses many pieces
+    g = gen(n + dim)
+    ids = torch.randint(0, vocab, (n,), device="cuda", generator=g)
+    u = torch.rand(n, device="cuda", generator=g)
+    ids[u < 0.3], ids[u > 0.95] = vocab // 2, -1
+    dout = normal((n, dim), g, dtype)
+    dout[ids < 0] = NAN
+    old = normal((vocab, dim), g, gdtype)
+    live = ids >= 0
+    ref, mag = (torch.zeros((vocab, dim), dtype=F64, device="cuda") for _ in range(2))
+    ref.index_put_((ids[live],), dout[live].double(), accumulate=True)
+    mag.index_put_((ids[live],), dout[live].double().abs(), accumulate=True)
+    most, scale = int(torch.bincount(ids[live]).max()), 0.37
+    ref, mag = ref * float(torch.tensor(scale)), mag * scale
+    grad = old.clone() if accumulate else torch.full_like(old, 3.0)
+    if extra:
+        dout, grad = padded(dout, extra), padded(grad, extra)
+    if accumulate:
+        ref, mag = ref + old.double(), mag + old.double().abs()
+    got = api.embed_grad(dout, ids, grad=grad, scale=scale, accumulate=accumulate).double()
+    # sums of `most` terms in fp32 in any order, scaled and added: (most + 2) roundings of at most mag
+    assert torch.all((got - ref).abs() <= (most + 2) * E * mag + U[gdtype] * ref.abs() * (1 + 2 ** -7))
+
+
+def test_wgrad_holds_every_slice_of_fp32():
+    # one row a group: an entry of G is one product, so dY's three bf16 slices show. Their products are exact and their
+    # two additions lose up to a unit (2 E) each: below 6 E with the slices' own remainder, where two slices alone
+    # err by up to 2^-17 (128 E)
+    r = gen(13)
+    dy, ck = normal((6, 200), r), api.checkpoint_store(normal((6, 264), r))
+    x = api.checkpoint_load(ck, dtype=F32).double()
+    off = torch.arange(7, dtype=torch.int32, device="cuda")
+    ref = dy.double()[:, :, None] * x[:, None, :]
+    for view in (dy, padded(dy, 3)):
+        got = api.checkpoint_wgrad(view, ck, offsets=off)
+        assert torch.all((got.double() - ref).abs() <= 6 * E * ref.abs())
+    high = dy.to(BF16).double()
+    two = high + (dy.double() - high).to(BF16).double()
+    assert torch.any((two[:, :, None] * x[:, None, :] - ref).abs() > 24 * E * ref.abs())
+
+
+@pytest.mark.parametrize("k", [64, 63])
+def test_wgrad_adds_to_subnormals(k):
+    # added by TMA where G's rows are 16-byte aligned, element by element where not: neither drops a subnormal of G,
+    # of the sum 1.5 * 2^-125 - 1.25 * 2^-125 = 2^-127, or of nothing added
+    x = torch.zeros((8, k), device="cuda")
+    x[0] = 2.0 ** -120
+    dy = torch.zeros((8, 40), device="cuda", dtype=BF16)
+    dy[0, :20] = -1.25 * 2.0 ** -5
+    ck = api.checkpoint_store(x)
+    grad = torch.full((1, 40, k), 1.5 * 2.0 ** -125, device="cuda")
+    grad[:, 20:] = 2.0 ** -130
+    api.checkpoint_wgrad(dy, ck, grad=grad, accumulate=True)
+    assert torch.all(grad[:, :20].double() == 2.0 ** -127) and torch.all(grad[:, 20:].double() == 2.0 ** -130)
+
+
+def test_offsets_past_32_bits():
+    # more than 2^31 elements each; what the last rows give is compared with a call of those rows alone
+    g = gen(14)
+    tail = 64
+    # the table's gradient
+    vocab, dim = (1 << 20) + 3, 2304
+    dout = normal((1500, dim), g, BF16)
+    ids = torch.full((1500,), vocab - 1, device="cuda")
+    ids[700:] = torch.arange(vocab - 801, vocab - 1, device="cuda")
+    grad = torch.empty((vocab, dim), dtype=BF16, device="cuda")
+    for part in (slice(0, 1500), slice(600, 800)):  # by sorting, and by searching the list
+        grad[-900:] = 5
+        api.embed_grad(dout[part], ids[part], grad=grad)
+        small = api.embed_grad(dout[part], torch.where(ids[part] >= vocab - 900, ids[part] - (vocab - 900), -1), vocab=900)
+        assert torch.equal(grad[-900:], small)
+    del grad, dout
+    # gated activation and its 8-bit form
+    n, f = 150001, 14336
+    gu, dh = torch.zeros((n, 2 * f), dtype=BF16, device="cuda"), torch.zeros((n, f), dtype=BF16, device="cuda")
+    gu[-tail:], dh[-tail:] = normal((tail, 2 * f), g, BF16), normal((tail, f), g, BF16)
+    h, a, b = api.gated_forward(gu[:, :f], gu[:, f:])
+    hs, sa, sb = api.gated_forward(gu[-tail:, :f], gu[-tail:, f:])
+    assert torch.equal(h[-tail:], hs) and torch.equal(a.q[-tail:], sa.q) and torch.equal(b.scales[-tail:], sb.scales)
+    dgu, again = api.gated_backward(dh, a, b)
+    ds, ags = api.gated_backward(dh[-tail:], sa, sb)
+    assert torch.equal(dgu[-tail:], ds) and torch.equal(again[-tail:], ags)
+    del h, dgu, again
+    # a weight gradient from the last rows of both operands: the rows before them are zeros
+    off = torch.tensor([0, n - tail, n], dtype=torch.int32, device="cuda")
+    big = api.checkpoint_wgrad(dh[:, :32], a, offsets=off, dtype=F32)
+    assert torch.all(big[0] == 0) and torch.equal(big[1], api.checkpoint_wgrad(dh[-tail:, :32], sa, dtype=F32)[0])
+    wide = api.checkpoint_store(normal((n, 32), g))
+    got = api.checkpoint_wgrad(dh, wide, offsets=off, dtype=F32)[1].double()
+    x = api.checkpoint_load(wide, dtype=F32)[-tail:].double()
+    d = dh[-tail:].double()
+    assert torch.all((got - d.t() @ x).abs() <= 64 * 2 * E * (d.abs().t() @ x.abs()) + 1e-37)
+    del gu, dh, a, b, wide
+    # the policy loss
+    n, vocab = 16390, 131080
+    x = torch.zeros((n, vocab), dtype=BF16, device="cuda")
+    x[-tail:] = normal((tail, vocab), g, BF16, 2.0)
+    y = torch.randint(0, vocab, (n,), device="cuda", generator=g)
+    one = torch.ones(n, device="cuda")
+    ref = api.policy_loss(x[-tail:].clone(), y[-tail:], one[-tail:], one[-tail:])
+    got = api.policy_loss(x, y, one, one, dlogits=x)
+    # one row of either is summed in another order: vocab / 128 + 64 additions, and the bf16 rounding
+    tol = (vocab / 128 + 64) * 2 * E
+    assert torch.all((got.logp[-tail:] - ref.logp).abs() <= tol * 16)
+    assert torch.all((x[-tail:].double() - ref.dlogits.double()).abs() <= ref.dlogits.double().abs() * (2.0 ** -7 + 32 * tol) + 1e-37)
+
+
+def test_operators_from_several_threads():
+    # each thread on a stream of its own, with scratch and counters of its own
+    work = [step_inputs(20 + k, 40 + 60 * k, 3000, 600 + 300 * k, 264, 520, 1500 + 700 * k) for k in range(3)]
+    ref = [run_step(w) for w in work]
+    torch.cuda.synchronize()
+    bad = []
+
+    def go(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(10):
+                    got = run_step(work[k])
+                    s.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(ref[k], got)):
+                        bad.append(k)
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=go, args=(k,)) for k in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and api.get_status() == 0
+
+
+CHILD = textwrap.dedent("""
+    import os, sys
+    import torch
+    sys.path.insert(0, %r)
+    from newton_schulz_quintic_gb300 import build, api
+    os.environ["NS_LIBRARY_PATH"] = build.build()
+    api.load_library()
+    bf16, f32 = torch.bfloat16, torch.float32
+    for dt, gd in ((bf16, bf16), (f32, f32), (bf16, f32), (f32, bf16)):
+        for n, vocab, dim in ((3000, 700, 2304), (3000, 50, 1543)):
+            ids = torch.randint(-1, vocab, (n,), device="cuda")
+            ids[torch.rand(n, device="cuda") < 0.3] = vocab // 2
+            dout = torch.randn(n, dim, device="cuda").to(dt)
+            g = api.embed_grad(dout, ids, vocab=vocab, dtype=gd)
+            api.embed_grad(dout, ids, grad=g, accumulate=True)
+    assert api.get_status() == 0, "a bounds check fired"
+    print("debug-bounds ok")
+""") % ROOT
+
+
+def test_debug_build_checks_several_column_ranges():
+    env = dict(os.environ, NS_BUILD_TAG="debugbounds", NS_EXTRA_NVCC_FLAGS="-DNS_DEBUG_BOUNDS")
+    env.pop("NS_LIBRARY_PATH", None)
+    r = subprocess.run([sys.executable, "-c", CHILD], env=env, capture_output=True, text=True, timeout=1200, cwd=ROOT)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "debug-bounds ok" in r.stdout
