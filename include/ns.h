@@ -26,7 +26,10 @@
  *    except the library's internal workspace cache (see ns_release_workspace).
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream). All device work is stream-ordered on it; calls do not
- *    synchronise unless stated.
+ *    synchronise unless stated. The workspace cache goes by the handle (for
+ *    cudaStreamPerThread, by the thread's stream): before a stream with work
+ *    of this library in flight is destroyed, wait for it, as another stream
+ *    may get the same handle.
  *  - Return value: NS_OK (0) or a negative NS_E* code. Arguments are
  *    validated before anything is launched; on a validation error nothing
  *    runs and the matrices are untouched. No C++ exception crosses the ABI.

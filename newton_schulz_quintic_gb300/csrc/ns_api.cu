@@ -596,14 +596,22 @@ int new_block(uint8_t **out, size_t bytes, const void *from, size_t fill, cudaSt
 struct WsKey {
   int dev;
   cudaStream_t stream;
+  unsigned long long id;  // cudaStreamPerThread is one handle for a stream of every thread: which of them; else 0
   int slot;
   bool operator<(const WsKey &o) const {
     if (dev != o.dev) return dev < o.dev;
     if (stream != o.stream) return stream < o.stream;
+    if (id != o.id) return id < o.id;
     return slot < o.slot;
   }
 };
 std::map<WsKey, CachedWs> g_ws;
+
+CachedWs &cached_ws(int dev, cudaStream_t s, int slot) {
+  WsKey key{dev, s, 0, slot};
+  if (s == cudaStreamPerThread && cudaStreamGetId(s, &key.id) != cudaSuccess) cudaGetLastError();
+  return g_ws[key];
+}
 
 // The cached scratch grown to `bytes`; its first `zero` bytes are zero when it
 // is made.
@@ -842,7 +850,7 @@ int run(void *const *X, const int64_t *shapes, int count, int steps, const float
     // dropped with it) runs from that plan: nothing is planned, encoded or uploaded
     int dev = 0;
     cudaGetDevice(&dev);
-    CachedWs &c = g_ws[WsKey{dev, s, slot}];
+    CachedWs &c = cached_ws(dev, s, slot);
     key = call_key(X, shapes, count, steps, dtype);
     for (DevBlob &b : c.blobs)
       if (b.layout && b.key == key) {
@@ -865,7 +873,7 @@ int run(void *const *X, const int64_t *shapes, int count, int steps, const float
   } else {
     int dev = 0;
     cudaGetDevice(&dev);
-    cache = &g_ws[WsKey{dev, s, slot}];
+    cache = &cached_ws(dev, s, slot);
     rc = ensure_ws(*cache, L.total, s);
     if (rc) return rc;
     ws = cache->ptr;
@@ -960,7 +968,7 @@ OpCall::~OpCall() {
 
 int OpCall::workspace(int slot, size_t bytes, uint8_t **ptr, size_t zero) {
   try {
-    CachedWs &c = g_ws[WsKey{dev, s, slot}];
+    CachedWs &c = cached_ws(dev, s, slot);
     const int e = ensure_ws(c, std::max<size_t>(bytes, 256), s, zero);
     *ptr = c.ptr;
     return e;
@@ -1135,7 +1143,7 @@ int ns_orthogonalize_batched_host(void *const *X_host, const int64_t *shapes, in
     if (rc) return rc;
     int dev = 0;
     cudaGetDevice(&dev);
-    CachedWs &c = g_ws[WsKey{dev, s, 1}];
+    CachedWs &c = cached_ws(dev, s, 1);
     rc = ensure_ws(c, std::max<size_t>(total, 256), s);
     if (rc) return rc;
     dbuf = c.ptr;

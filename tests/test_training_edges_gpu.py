@@ -418,3 +418,45 @@ def test_debug_build_checks_several_column_ranges():
     r = subprocess.run([sys.executable, "-c", CHILD], env=env, capture_output=True, text=True, timeout=1200, cwd=ROOT)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
     assert "debug-bounds ok" in r.stdout
+
+
+def test_threads_that_use_the_per_thread_stream():
+    # cudaStreamPerThread (handle 2) is another stream in each thread: they must not share scratch. (Every output is made
+    # beforehand: torch's allocator goes by the handle.)
+    r = gen(30)
+    work = []
+    for k in range(3):
+        t, ids = 600 + 300 * k, 1500 + 700 * k
+        dy, ck = normal((t, 264), r, BF16), api.checkpoint_store(normal((t, 520), r))
+        tokens, dout = torch.randint(0, 700, (ids,), device="cuda", generator=r), normal((ids, 64), r, BF16)
+        mats = [normal((264, 520 + 8 * k), r, BF16) for _ in range(8)]
+        ref = [api.checkpoint_wgrad(dy, ck, dtype=F32), api.embed_grad(dout, tokens, vocab=700), mats[0].clone()]
+        mats[1:] = [mats[0].clone() for _ in mats[1:]]
+        api.orthogonalize_batched([ref[2]])
+        out = [(torch.empty_like(ref[0]), torch.empty_like(ref[1]), m) for m in mats]
+        work.append((dy, ck, dout, tokens, ref, out))
+    torch.cuda.synchronize()
+    bad, start = [], threading.Barrier(3)
+
+    def go(dy, ck, dout, tokens, ref, out):
+        try:
+            s = torch.cuda.ExternalStream(2)
+            with torch.cuda.stream(s):
+                start.wait()
+                for a, b, m in out:
+                    api.checkpoint_wgrad(dy, ck, grad=a)
+                    api.embed_grad(dout, tokens, grad=b)
+                    api.orthogonalize_batched([m])
+                s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=go, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad and api.get_status() == 0
+    for *_, ref, out in work:
+        assert all(torch.equal(a, b) for got in out for a, b in zip(ref, got))
