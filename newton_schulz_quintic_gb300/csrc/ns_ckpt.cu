@@ -14,8 +14,8 @@
 // instructions per 32 values: 57 against 45 us for fp32 4093 x 6143 stored and
 // loaded).
 //
-// 16384 x 14336 bf16: gated forward 301 us, 6.4 TB/s; backward 359 us, 6.6 TB/s
-// (96 and 99 % of the copy rate). fp32 4093 x 6143, unaligned, stored and loaded:
+// 16384 x 14336 bf16: gated forward 298 us, 6.4 TB/s; backward 357 us, 6.6 TB/s
+// (95 and 99 % of the copy rate). fp32 4093 x 6143, unaligned, stored and loaded:
 // 45 us, 5.6 TB/s.
 #include <algorithm>
 
@@ -296,9 +296,9 @@ int run_one(CkptParams p, int sms, cudaStream_t s) {
   while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < lanes) ++p.lanes_log2;
   const int64_t gx = (lanes + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
   const int height = kThreads >> p.lanes_log2;
-  // Blocks beyond the resident ones even out the end; too many repeat the setup: 16384 x 14336 gated, both ways,
-  // 675 us at 32 a SM, 660 at 128, 722 without a limit. (Two row steps in flight per thread cost registers: 10 %
-  // slower.)
+  // Blocks beyond the resident ones even out the end; too many repeat the setup: 16384 x 14336 gated, both ways, with
+  // a sigmoid that has since made 660 us 654: 675 us at 32 a SM, 660 at 128, 722 without a limit. (Two row steps in
+  // flight per thread cost registers: 10 % slower.)
   const int64_t want = (p.rows + height - 1) / height;
   const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(sms) * (WIDE ? 128 : 32) / gx);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>({want, most, 65535})), 1);

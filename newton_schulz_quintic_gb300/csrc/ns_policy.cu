@@ -13,7 +13,7 @@
 // the passes a row stays in shared memory as far as that goes (110 KB a CTA,
 // two CTAs an SM) and in L2 beyond. That leaves the instructions per element:
 // packed maxima and pairs of fp32 operations. Measured at 8192 x 131072 bf16
-// with a quarter of the rows masked: 665 us, 85 % of the copy bandwidth (565
+// with a quarter of the rows masked: 660 us, 85 % of the copy bandwidth (564
 // us). On the way there: separate fp32 operations 800 us; CTAs that walk over
 // the rows in a fixed stride 754 us, because masked rows are cheap and leave
 // some CTAs with more work, where the block scheduler hands rows out as CTAs

@@ -214,7 +214,9 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
     pass (ns_policy_loss): the sum over rows of weights * (kl_coef * k - min(r A,
     clip(r, 1 - clip_low, 1 + clip_high) A)), r = exp(logp - old_logp), k =
     exp(ref_logp - logp) - (ref_logp - logp) - 1. Rows whose target is outside
-    the vocabulary or whose weight is 0 are masked. ``dlogits`` is where the
+    the vocabulary or whose weight is 0 are masked; a NaN of any other row reaches
+    the loss. With ``kl_coef`` 0 the KL term is only returned, whatever it is.
+    ``dlogits`` is where the
     gradient goes; it may be ``logits`` itself; allocated when not given;
     ``grad=False`` computes none."""
     ld = _matrix(logits, "logits")
