@@ -353,6 +353,166 @@ int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_t n_out, co
                   int accumulate, void *stream);
 
 /*
+ * Operators of an expert layer. As the operators above: the checks come before
+ * any launch, work is ordered on `stream`, nothing synchronises. Scratch, where
+ * a call needs some, is the caller's (device memory, no initial values needed),
+ * so calls captured into different graphs share none; nothing is allocated.
+ */
+
+/*
+ * ns_route -- the router: for each of `rows` rows of `experts` logits l (pitch
+ * ld_logits) the top_k experts of largest l, ties to the lower index, with the
+ * weights softmax(l) (renormalise = 1: divided by the sum of the chosen ones).
+ *   live       NULL, or rows bytes: a row with 0 is padding, it is not read
+ *   ids        rows x top_k experts, largest logit first; -1 where none is left
+ *              (logits of -infinity are never chosen) and in rows of padding; a
+ *              row of -infinity alone counts as padding
+ *   weights    rows x top_k floats, 0 where the id is -1
+ *   logz       rows floats, log sum exp l (0 for padding)
+ *   counts     experts: slots of each;  offsets: experts + 1, their running sum
+ *   order      rows x top_k: the slots (row * top_k + place) in the experts'
+ *              order, ascending within an expert, then -1
+ *   live_rows  one int: T, the rows that are not padding
+ *   loss       one float: balance_coef * experts / (top_k T^2) * sum_e counts[e] *
+ *              (sum over rows of softmax(l)[e]) + z_coef / T * sum of logz^2 (T = 0: 0)
+ * A NaN orders above every number; a NaN or +infinity in a row makes its
+ * weights, its logz and the loss NaN. offsets is what ns_blocks_matmul and
+ * ns_ckpt_wgrad take, order what ns_blocks_store_rows takes (per = top_k).
+ * experts <= 1024, top_k <= 32 and <= experts, rows * top_k <= 2^30. workspace:
+ * ns_route_workspace(rows, experts) bytes, 4-byte aligned (less: NS_ENOMEM).
+ */
+int64_t ns_route_workspace(int64_t rows, int experts); /* -1 for bad sizes */
+int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int experts, int top_k, const uint8_t *live,
+             int renormalise, float balance_coef, float z_coef, int32_t *ids, float *weights, float *logz,
+             int32_t *counts, int32_t *offsets, int32_t *order, int32_t *live_rows, float *loss, void *workspace,
+             size_t workspace_bytes, int dtype, void *stream);
+
+/*
+ * ns_route_backward -- the logits' gradient of the loss (its own gradient 1)
+ * and of the weights, dweights (rows x top_k, NULL: none; not read where the id
+ * is -1). ids, weights, logz, counts, live_rows and the coefficients as ns_route
+ * gave and got them; counts are taken as constants. With p = softmax(l) and s[e] =
+ * balance_coef * experts * counts[e] / (top_k T^2):
+ *     dl = p (s - sum p s + 2 z_coef logz / T) + the weights' part:
+ *     renormalise 1: w (dw - sum w dw) at the chosen; 0: dw joins s at the chosen
+ * Rows of padding get zeros. dlogits may be logits itself (same pitch).
+ */
+int ns_route_backward(const void *logits, int64_t ld_logits, int64_t rows, int experts, int top_k, const int32_t *ids,
+                      const float *weights, const float *dweights, const float *logz, const int32_t *counts,
+                      const int32_t *live_rows, int renormalise, float balance_coef, float z_coef, void *dlogits,
+                      int64_t ld_dlogits, int dtype, void *stream);
+
+/*
+ * Matrices held in 8-bit floating point ("blocks"): e4m3 values q with one scale
+ * byte s per block of 128 values of a row ("rows") or of 128 x 128 values
+ * ("tiles"; blocks at a matrix's ends are smaller):
+ *     value = q * 2^(s - 127)
+ *     s     = smallest >= 1 with (largest magnitude of the block) <= 448 * 2^(s - 127)
+ *     q     = x * 2^(127 - s) rounded to e4m3, half to even
+ * A block that holds an infinity or NaN has s = 255 and reads back as NaN
+ * throughout. The scale is a power of two, so x is rounded once.
+ *   q       rows x ns_blocks_pitch(cols) bytes; bytes beyond cols are 0
+ *   scales  rows x ns_blocks_scale_pitch(cols) bytes; for tiles one such row for
+ *           every 128 rows of a matrix, counted anew for each of a stack; 0 beyond
+ * Both 16-byte aligned (NS_EALIGN). cols < 2^30.
+ */
+int64_t ns_blocks_pitch(int64_t cols);       /* cols rounded up to a multiple of 16; -1 if negative */
+int64_t ns_blocks_scale_pitch(int64_t cols); /* ceil(cols / 128) rounded up to a multiple of 4 */
+
+/* ns_blocks_store_rows -- rows of X with a scale per 128 values. With index
+ * (`rows` int32 on the device) row r holds X[index[r] / per], a row of zeros where
+ * index[r] is negative or beyond x_rows; without, rows = x_rows and per = 1. */
+int ns_blocks_store_rows(const void *x, int64_t ld_x, int64_t x_rows, const int32_t *index, int per, int64_t rows,
+                         int64_t cols, void *q, void *scales, int dtype, void *stream);
+/* ns_blocks_store_tiles -- a stack of `groups` matrices of rows x cols (one
+ * behind the other, all rows ld_x apart) with a scale per 128 x 128 values. */
+int ns_blocks_store_tiles(const void *x, int64_t ld_x, int groups, int64_t rows, int64_t cols, void *q, void *scales,
+                          int dtype, void *stream);
+/* ns_blocks_load -- Out = the values held (groups * rows rows; groups = 1 unless tiles). */
+int ns_blocks_load(const void *q, const void *scales, int tiles, int groups, int64_t rows, int64_t cols, void *out,
+                   int64_t ld_out, int dtype, void *stream);
+
+/*
+ * ns_blocks_matmul -- the product of such matrices, A (rows x k, rows form) and
+ * a stack of W (tiles form):
+ *     back = 0: Out[t] = A[t] W[e]^T, W[e] n x k      (a layer, forward)
+ *     back = 1: Out[t] = A[t] W[e],   W[e] k x n      (its input's gradient)
+ * for the rows t of group e.
+ *   offsets  groups + 1 ascending int32 on the device, as for ns_ckpt_wgrad:
+ *            group e is rows [offsets[e], offsets[e+1]); rows of no group become
+ *            zeros. NULL with groups = 1 for all rows.
+ *   out      rows x n of dtype
+ * The tensor cores add the 128 products of a block in their fp32 accumulators;
+ * the blocks' sums are scaled and added in fp32 registers, and rounded once. rows, n
+ * and k <= 2^30, groups <= 2^20, groups * n * k <= 2^42.
+ */
+int ns_blocks_matmul(const void *qa, const void *sa, int64_t rows, int64_t k, const void *qw, const void *sw, int64_t n,
+                     int back, const int32_t *offsets, int groups, void *out, int64_t ld_out, int dtype, void *stream);
+
+/*
+ * ns_block_norm -- the norms after and before a block, with the block's gate
+ * and the residual scale, in one pass. Per row, with mean over cols:
+ *     u = Y * rsqrt(mean Y^2 + eps) * post   (post NULL: u = Y)
+ *     R = a X + b gate u                     (Y NULL: R = a X)
+ *     Z = R * rsqrt(mean R^2 + eps) * pre    (pre NULL: no Z), from R before it is rounded
+ *   x, r   rows x cols of dtype, the residual stream
+ *   y, z   rows x cols of block_dtype: the block's output, the next block's input;
+ *          block_dtype may be bf16 beside an fp32 dtype, not the other way round
+ *   gate   gate_dtype; gate_form NS_GATE_NONE (NULL, 1), NS_GATE_COLS (cols values),
+ *          NS_GATE_ROWS (one value a row, ld_gate apart), NS_GATE_FULL (rows x cols)
+ *   post, pre   cols values of weight_dtype
+ *   post_rstd, pre_rstd   rows floats for the backward pass (where post / pre)
+ * r may be x and z may be y (same pitch). cols <= 16384. Y or pre must be given.
+ */
+#define NS_GATE_NONE 0
+#define NS_GATE_COLS 1
+#define NS_GATE_ROWS 2
+#define NS_GATE_FULL 3
+int ns_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, const void *gate, int gate_form,
+                  int64_t ld_gate, const void *post, const void *pre, int64_t rows, int64_t cols, float a, float b,
+                  float eps, void *r, int64_t ld_r, void *z, int64_t ld_z, float *post_rstd, float *pre_rstd, int dtype,
+                  int block_dtype, int weight_dtype, int gate_dtype, void *stream);
+
+/*
+ * ns_block_norm_backward -- from dR (NULL: zero, only with pre) and dZ: dX, dY, the
+ * gate's gradient in the gate's form, and dpost, dpre (weight_dtype). X, Y, gate, post,
+ * pre, a and b as given to ns_block_norm, whose rstd's it takes; R is formed again
+ * from them. dx may be dR and dy may be dZ (same type and pitch). Sums over rows
+ * are taken in fp32 in a fixed order. workspace: ns_block_norm_workspace(rows, cols)
+ * bytes, 4-byte aligned (less: NS_ENOMEM).
+ */
+int64_t ns_block_norm_workspace(int64_t rows, int64_t cols); /* -1 for bad sizes */
+int ns_block_norm_backward(const void *dr, int64_t ld_dr, const void *dz, int64_t ld_dz, const void *x, int64_t ld_x,
+                           const void *y, int64_t ld_y, const void *gate, int gate_form, int64_t ld_gate,
+                           const void *post, const void *pre, const float *post_rstd, const float *pre_rstd,
+                           int64_t rows, int64_t cols, float a, float b, void *dx, int64_t ld_dx, void *dy,
+                           int64_t ld_dy, void *dgate, int64_t ld_dgate, void *dpost, void *dpre, void *workspace,
+                           size_t workspace_bytes, int dtype, int block_dtype, int weight_dtype, int gate_dtype,
+                           void *stream);
+
+/*
+ * ns_dropout -- Out = [residual +] X with a share `prob` of its elements dropped
+ * and the others divided by the share that stays. The mask is drawn, not
+ * stored: the same call on the gradient is the backward pass.
+ * Eight consecutive columns of a row share a counter n = offset + row *
+ * ceil(cols / 8) + column / 8 (mod 2^64). Philox4x32-10 with the key `seed` and the
+ * counter words (n mod 2^32, n / 2^32, 0, 0) gives eight 16-bit numbers h, a word's
+ * low half first; with (.., .., 1, 0) eight more, l. An element is dropped when
+ * h * 65536 + l < limit = round(prob * 2^32), the others are multiplied by 2^32 /
+ * (2^32 - limit). A call uses rows * ceil(cols / 8) counters.
+ *   state     NULL, or {seed, offset} on the device (two 64-bit numbers, 8-byte
+ *             aligned) added to the arguments: a captured call draws anew when
+ *             they change
+ *   residual  NULL, or rows x cols of out_dtype
+ *   out       rows x cols of out_dtype: dtype, or fp32 with a residual; may be x
+ *             or residual (same type and pitch)
+ * A dropped element has no part in the result, whatever it holds. prob in [0, 1].
+ */
+int ns_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t rows, int64_t cols,
+               double prob, uint64_t seed, uint64_t offset, const void *state, void *out, int64_t ld_out, int dtype,
+               int out_dtype, void *stream);
+
+/*
  * ns_cost -- Newton-Schulz cost of an M x N matrix, max(M,N) * min(M,N)^2
  * (second page, "Changes" item 1: the dominant term of the orthogonalization).
  * Returns -1 if M or N is negative.
@@ -468,8 +628,9 @@ int64_t ns_num_workspace_allocations(void);
  * (ns_muon_update_batched's element-wise step), 9 embedding lookup, 10 sort of
  * the ids, 11 embedding gradient, 12 log probabilities and policy loss, 13
  * 8-bit checkpoints and the gated activation, 14 weight gradient (with its
- * preparation), the total milliseconds into
- * ms[k] and the launch count into launches[k] for k < n (n <= 15). Returns
+ * preparation), 15 router, 16 matrices held in blocks, 17 their product, 18
+ * block norms, 19 dropout, the total milliseconds into
+ * ms[k] and the launch count into launches[k] for k < n (n <= 20). Returns
  * NS_OK or NS_EINVAL / NS_ECUDA.
  */
 int ns_set_kernel_timing(int enable);

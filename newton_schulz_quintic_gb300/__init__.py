@@ -9,13 +9,24 @@ missing: there is no CPU fallback.
 from .api import (  # noqa: F401
     NS_BF16,
     NS_F32,
+    BlockNorm,
+    BlockNormGrads,
+    Blocks8,
     Checkpoint8,
     NSError,
     PolicyLoss,
+    Routing,
+    block_norm,
+    block_norm_backward,
+    blocks_load,
+    blocks_matmul,
+    blocks_store,
     checkpoint_load,
     checkpoint_store,
     checkpoint_wgrad,
     cost,
+    dropout,
+    dropout_counters,
     embed_grad,
     embed_lookup,
     gated_backward,
@@ -26,6 +37,8 @@ from .api import (  # noqa: F401
     orthogonalize_batched,
     orthogonalize_batched_host,
     policy_loss,
+    route,
+    route_backward,
     token_logprobs,
     workspace_bytes,
 )

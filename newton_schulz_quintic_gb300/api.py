@@ -343,7 +343,8 @@ def num_kernel_launches() -> int:
 
 
 KERNEL_KINDS = ("norm_pass", "norm_finish", "gram", "square", "apply", "resident", "gemm", "prep",
-                "momentum", "embed_lookup", "embed_sort", "embed_grad", "policy", "checkpoint", "wgrad")
+                "momentum", "embed_lookup", "embed_sort", "embed_grad", "policy", "checkpoint", "wgrad", "route", "blocks",
+                "blocks_matmul", "block_norm", "dropout")
 
 
 def set_kernel_timing(enable: bool) -> None:
@@ -459,4 +460,21 @@ from .training import (  # noqa: E402,F401
     gated_forward,
     policy_loss,
     token_logprobs,
+)
+
+# the operators of an expert layer
+from .layers import (  # noqa: E402,F401
+    BlockNorm,
+    BlockNormGrads,
+    Blocks8,
+    Routing,
+    block_norm,
+    block_norm_backward,
+    blocks_load,
+    blocks_matmul,
+    blocks_store,
+    dropout,
+    dropout_counters,
+    route,
+    route_backward,
 )

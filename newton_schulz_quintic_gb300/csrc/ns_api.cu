@@ -667,7 +667,8 @@ bool nvtx_on() {
 const char *const kKindNames[] = {"ns norm pass", "ns norm finish", "ns gram", "ns square", "ns apply",
                                   "ns resident", "ns gemm (all phases)", "ns prep", "ns momentum",
                                   "ns embed lookup", "ns embed sort", "ns embed grad", "ns policy",
-                                  "ns checkpoint", "ns wgrad"};
+                                  "ns checkpoint", "ns wgrad", "ns route", "ns blocks",
+                                  "ns blocks matmul", "ns block norm", "ns dropout"};
 static_assert(sizeof(kKindNames) / sizeof(kKindNames[0]) == kKinds, "one name per kind");
 struct NvtxRange {
   bool on;
@@ -987,8 +988,10 @@ int OpCall::tensor_map(CUtensorMap *map, int elt, const void *base, int rank, co
     bx[i] = static_cast<cuuint32_t>(box[i]);
     if (i) st[i - 1] = static_cast<cuuint64_t>(pitch_bytes[i - 1]);
   }
-  const CUresult r = g_encode(map, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                              static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, bx, one,
+  const CUtensorMapDataType type = elt == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, bx, one,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? NS_OK : NS_ECUDA;

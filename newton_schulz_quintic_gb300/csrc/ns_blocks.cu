@@ -1,0 +1,371 @@
+// ns_blocks.cu -- matrices held in e4m3 with a power-of-two scale for each
+// block of 128 (include/ns.h): rows with 1 x 128 blocks, rows gathered on the
+// way, and weights with 128 x 128 blocks; and the values read back. Their
+// product is in ns_blocks_mm.cu.
+//
+// The scale is the smallest power of two that brings a block's largest
+// magnitude to 448 or less, found in the bits of that magnitude, so x * 2^-e is
+// exact and the conversion to e4m3 rounds once, half to even.
+//
+// Element-wise work bound by HBM: one read, one write. Rows: a lane holds 8
+// consecutive values and the 16 lanes of a block find its largest magnitude by
+// shuffles. Weights: a CTA holds one 128 x 128 block in registers between the
+// two steps.
+#include <algorithm>
+
+#include "../../include/ns.h"
+#include "ns_rows.cuh"
+
+namespace ns {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 128;
+
+struct BlocksParams {
+  const void *x;          // store: values; load: nothing
+  void *out;              // load: values
+  int64_t ld;             // pitch of the values
+  int64_t rows;           // rows of q (of one matrix of a stack)
+  int64_t src_rows;       // rows form: rows of x
+  const int32_t *index;   // rows form: row r holds x[index[r] / per]; nullptr: x[r]
+  uint32_t per;
+  uint8_t *q, *s;
+  int cols, pitch, scale_pitch;
+  int groups;             // matrices of a stack (tiles)
+  int tiles;              // load: 128 x 128 blocks
+  int lanes_log2;
+  int *status;
+};
+
+// The scale byte of a block whose largest magnitude has the float bits `top`, and 2^(127 - byte).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  return top >= 0x7f800000u ? 255u : static_cast<uint32_t>(max(static_cast<int>((top + 0x1fffffu) >> 23) - 8, 1));
+}
+__device__ __forceinline__ float up_of(uint32_t s) {  // NaN for a block with infinities or NaN: every value of it
+  return __uint_as_float(s == 255 ? 0x7fc00000u : (254u - s) << 23);
+}
+__device__ __forceinline__ float unit_of(uint32_t s) {  // a padding byte 0 reads as 1
+  return __uint_as_float(s == 255 ? 0x7fc00000u : max(s, 1u) << 23);
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float low, float high) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(high), "f"(low));
+  return v;
+}
+// Two e4m3 values as floats, exactly (every e4m3 value is an fp16 value).
+__device__ __forceinline__ void from_e4m3x2(uint32_t v, float &low, float &high) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(low), "=f"(high) : "r"(h));
+}
+
+template <typename T>
+__device__ __forceinline__ void put(void *at, T v, const void *base, size_t size, int *status) {
+  if (in_bounds(at, sizeof(T), base, size, status)) *static_cast<T *>(at) = v;
+}
+
+// Largest magnitude of a lane's 8 values as float bits; NaN is the largest of all.
+template <int DT, typename V>
+__device__ __forceinline__ uint32_t top_of(const V &v) {
+  uint32_t m = 0;
+  if constexpr (DT == kBF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, reinterpret_cast<const uint32_t *>(v.w)[i] & 0x7fff7fffu);
+    return max(m & 0xffff0000u, m << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v.get(i)) & 0x7fffffffu);
+    return m;
+  }
+}
+template <typename V>
+__device__ __forceinline__ uint2 eight_e4m3(const V &v, float up) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = to_e4m3x2(v.get(2 * i) * up, v.get(2 * i + 1) * up);
+  return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
+
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(kThreads) ns_blocks_store_rows_kernel(const __grid_constant__ BlocksParams p) {
+  using E = typename Elem<DT>::T;
+  using V = Eight<DT, WIDE>;
+  __shared__ uint4 stages[WIDE ? 1 : kThreads / 32][WIDE ? 1 : V::kStage];
+  uint4 *stage = stages[WIDE ? 0 : threadIdx.x / 32];
+  const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * 8;
+  const int height = kThreads >> p.lanes_log2;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * height;
+  const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < p.rows; t0 += step) {
+    const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
+    const bool row = t < p.rows;
+    int64_t from = t;
+    if (p.index) {
+      const int32_t i = row ? __ldg(p.index + t) : -1;
+      from = i < 0 ? -1 : static_cast<int64_t>(static_cast<uint32_t>(i) / p.per);
+    }
+    const bool here = row && from >= 0 && from < p.src_rows;
+    V x;
+    x.load(static_cast<const E *>(p.x) + (here ? from : 0) * p.ld, c, p.cols, here);
+    x.settle(stage);
+    uint32_t top = top_of<DT>(x.v);
+#pragma unroll
+    for (int o = 1; o < kBlock / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t sb = scale_byte(top);
+    const uint2 w = eight_e4m3(x, up_of(sb));
+    if (!row) continue;
+    // columns past the row were read as zeros, and so is what lies behind it (a NaN block's too)
+    if (c < p.pitch) {
+      uint2 v = w;
+      if (sb == 255 && c + 8 > p.cols) {
+        uint8_t *b = reinterpret_cast<uint8_t *>(&v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e >= p.cols) b[e] = 0;
+      }
+      put(p.q + t * p.pitch + c, v, p.q, qsize, p.status);
+    }
+    if (c % kBlock == 0 && c / kBlock < p.scale_pitch)
+      put(p.s + t * p.scale_pitch + c / kBlock, static_cast<uint8_t>(c < p.cols ? sb : 0), p.s, ssize, p.status);
+  }
+}
+
+// One CTA per 128 x 128 block: thread i holds columns (i % 16) * 8.. of rows i / 16 + 16 k.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(kThreads) ns_blocks_store_tiles_kernel(const __grid_constant__ BlocksParams p) {
+  using E = typename Elem<DT>::T;
+  __shared__ uint32_t tops[kThreads / 32];
+  const int tiles_x = (p.cols + kBlock - 1) / kBlock;
+  const int64_t tiles_y = (p.rows + kBlock - 1) / kBlock;
+  const int64_t per = tiles_x * tiles_y, total = per * p.groups;
+  const size_t qsize = static_cast<size_t>(p.groups) * p.rows * p.pitch;
+  const size_t ssize = static_cast<size_t>(p.groups) * tiles_y * p.scale_pitch;
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const int64_t g = i / per, in = i - g * per, ty = in / tiles_x;
+    const int tx = static_cast<int>(in - ty * tiles_x);
+    const int c = tx * kBlock + static_cast<int>(threadIdx.x % 16) * 8;
+    const int64_t r0 = ty * kBlock + threadIdx.x / 16;
+    const E *x = static_cast<const E *>(p.x) + (g * p.rows) * p.ld;
+    Pack<DT, 8> v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t r = r0 + 16 * k;
+      if (WIDE && r < p.rows && c < p.cols) {
+        v[k].load_stream(x + r * p.ld + c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<E *>(v[k].w)[e] = !WIDE && r < p.rows && c + e < p.cols ? __ldcs(x + r * p.ld + c + e) : Elem<DT>::from_f(0.f);
+      }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, top_of<DT>(v[k]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();  // the last block's have been read
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) top = max(top, tops[k]);
+    const uint32_t sb = scale_byte(top);
+    const float up = up_of(sb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t r = r0 + 16 * k;
+      if (r >= p.rows || c >= p.pitch) continue;
+      uint2 w = eight_e4m3(v[k], up);
+      if (sb == 255 && c + 8 > p.cols) {
+        uint8_t *b = reinterpret_cast<uint8_t *>(&w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e >= p.cols) b[e] = 0;
+      }
+      put(p.q + (g * p.rows + r) * p.pitch + c, w, p.q, qsize, p.status);
+    }
+    // the row of scales up to its pitch: the last block of a row also writes the zeros behind it
+    const int last = tx + 1 == tiles_x ? p.scale_pitch : tx + 1;
+    if (tx + static_cast<int>(threadIdx.x) < last)
+      put(p.s + (g * tiles_y + ty) * p.scale_pitch + tx + threadIdx.x, static_cast<uint8_t>(threadIdx.x == 0 ? sb : 0), p.s,
+          ssize, p.status);
+  }
+}
+
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(kThreads) ns_blocks_load_kernel(const __grid_constant__ BlocksParams p) {
+  using E = typename Elem<DT>::T;
+  using V = Eight<DT, WIDE>;
+  __shared__ uint4 stages[WIDE ? 1 : kThreads / 32][WIDE ? 1 : V::kStage];
+  uint4 *stage = stages[WIDE ? 0 : threadIdx.x / 32];
+  const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * 8;
+  const int height = kThreads >> p.lanes_log2;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * height, all = p.rows * p.groups;
+  const int64_t bands = (p.rows + kBlock - 1) / kBlock;
+  const size_t size = static_cast<size_t>((all - 1) * p.ld + p.cols) * sizeof(E);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < all; t0 += step) {
+    const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
+    const bool row = t < all;
+    V o;
+    if (row && c < p.cols) {
+      const int64_t g = p.tiles ? t / p.rows : 0, band = p.tiles ? g * bands + (t - g * p.rows) / kBlock : t;
+      const float unit = unit_of(p.s[band * p.scale_pitch + c / kBlock]);
+      const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p.q + t * p.pitch + c));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i % 2)), a, b);
+        o.set(2 * i, a * unit);
+        o.set(2 * i + 1, b * unit);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o.set(e, 0.f);
+    }
+    o.store(static_cast<E *>(p.out) + t * p.ld, c, p.cols, row, stage, p.out, size, p.status);
+  }
+}
+
+template <int DT>
+int run_store(BlocksParams &p, bool tiles, bool wide, int sms, cudaStream_t s) {
+  if (tiles) {
+    const int64_t total = (p.rows + kBlock - 1) / kBlock * ((p.cols + kBlock - 1) / kBlock) * p.groups;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(total, static_cast<int64_t>(sms) * 64));
+    if (wide)
+      ns_blocks_store_tiles_kernel<DT, true><<<grid, kThreads, 0, s>>>(p);
+    else
+      ns_blocks_store_tiles_kernel<DT, false><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    const int64_t extent = std::max<int64_t>(p.pitch, static_cast<int64_t>(p.scale_pitch) * kBlock);
+    const EightGrid g(p.rows, extent, kThreads, wide, 4, sms, wide ? 128 : 32);
+    p.lanes_log2 = g.lanes_log2;
+    if (wide)
+      ns_blocks_store_rows_kernel<DT, true><<<g.grid, kThreads, 0, s>>>(p);
+    else
+      ns_blocks_store_rows_kernel<DT, false><<<g.grid, kThreads, 0, s>>>(p);
+  }
+  count_launch();
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int DT>
+int run_load(BlocksParams &p, bool wide, int sms, cudaStream_t s) {
+  const EightGrid g(p.rows * p.groups, p.cols, kThreads, wide, 2, sms, wide ? 128 : 32);
+  p.lanes_log2 = g.lanes_log2;
+  if (wide)
+    ns_blocks_load_kernel<DT, true><<<g.grid, kThreads, 0, s>>>(p);
+  else
+    ns_blocks_load_kernel<DT, false><<<g.grid, kThreads, 0, s>>>(p);
+  count_launch();
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+bool bad_dtype(int dtype) { return dtype != NS_F32 && dtype != NS_BF16; }
+
+}  // namespace
+}  // namespace ns
+
+using namespace ns;
+
+extern "C" int64_t ns_blocks_pitch(int64_t cols) { return cols < 0 ? -1 : (cols + 15) / 16 * 16; }
+extern "C" int64_t ns_blocks_scale_pitch(int64_t cols) { return cols < 0 ? -1 : ((cols + 127) / 128 + 3) / 4 * 4; }
+
+extern "C" int ns_blocks_store_rows(const void *x, int64_t ld_x, int64_t x_rows, const int32_t *index, int per,
+                                    int64_t rows, int64_t cols, void *q, void *scales, int dtype, void *stream) {
+  if (bad_dtype(dtype) || bad_shape(x_rows, cols, ld_x) || bad_shape(rows, cols, cols) || cols > kMaxRowCols || per < 1)
+    return NS_EINVAL;
+  if (!index && (rows != x_rows || per != 1)) return NS_EINVAL;
+  if (rows == 0 || cols == 0) return NS_OK;
+  if ((!x && x_rows > 0) || !q || !scales) return NS_EINVAL;
+  const int elt = dtype == NS_BF16 ? 2 : 4;
+  if (misaligned(x, elt) || misaligned(index, 4) || misaligned(q, 16) || misaligned(scales, 16)) return NS_EALIGN;
+  BlocksParams p{};
+  p.pitch = static_cast<int>(ns_blocks_pitch(cols));
+  p.scale_pitch = static_cast<int>(ns_blocks_scale_pitch(cols));
+  const Range rx(x, x_rows, cols, ld_x, elt), ri(index, 1, rows, rows, 4);
+  const Range rq(q, rows, p.pitch, p.pitch, 1), rs(scales, rows, p.scale_pitch, p.scale_pitch, 1);
+  if (rq.overlaps(rx) || rs.overlaps(rx) || rq.overlaps(rs) || rq.overlaps(ri) || rs.overlaps(ri)) return NS_EINVAL;
+  OpCall call(stream);
+  if (call.rc) return call.rc;
+  p.x = x;
+  p.ld = ld_x;
+  p.rows = rows;
+  p.src_rows = x_rows;
+  p.index = index;
+  p.per = static_cast<uint32_t>(per);
+  p.q = static_cast<uint8_t *>(q);
+  p.s = static_cast<uint8_t *>(scales);
+  p.cols = static_cast<int>(cols);
+  p.groups = 1;
+  p.status = call.status;
+  const bool wide = cols % 8 == 0 && rows_aligned(x, ld_x, elt, 8);
+  return call.launch(kOpBlocks, [&] {
+    return dtype == NS_BF16 ? run_store<kBF16>(p, false, wide, call.sms, call.s) : run_store<kF32>(p, false, wide, call.sms, call.s);
+  });
+}
+
+extern "C" int ns_blocks_store_tiles(const void *x, int64_t ld_x, int groups, int64_t rows, int64_t cols, void *q,
+                                     void *scales, int dtype, void *stream) {
+  if (bad_dtype(dtype) || groups < 0 || bad_shape(rows, cols, ld_x) || cols > kMaxRowCols ||
+      (groups > 0 && bad_shape(static_cast<int64_t>(groups) * rows, cols, ld_x)))
+    return NS_EINVAL;
+  if (groups == 0 || rows == 0 || cols == 0) return NS_OK;
+  if (!x || !q || !scales) return NS_EINVAL;
+  const int elt = dtype == NS_BF16 ? 2 : 4;
+  if (misaligned(x, elt) || misaligned(q, 16) || misaligned(scales, 16)) return NS_EALIGN;
+  BlocksParams p{};
+  p.pitch = static_cast<int>(ns_blocks_pitch(cols));
+  p.scale_pitch = static_cast<int>(ns_blocks_scale_pitch(cols));
+  const int64_t all = static_cast<int64_t>(groups) * rows, bands = static_cast<int64_t>(groups) * ((rows + kBlock - 1) / kBlock);
+  const Range rx(x, all, cols, ld_x, elt), rq(q, all, p.pitch, p.pitch, 1), rs(scales, bands, p.scale_pitch, p.scale_pitch, 1);
+  if (rq.overlaps(rx) || rs.overlaps(rx) || rq.overlaps(rs)) return NS_EINVAL;
+  OpCall call(stream);
+  if (call.rc) return call.rc;
+  p.x = x;
+  p.ld = ld_x;
+  p.rows = rows;
+  p.q = static_cast<uint8_t *>(q);
+  p.s = static_cast<uint8_t *>(scales);
+  p.cols = static_cast<int>(cols);
+  p.groups = groups;
+  p.status = call.status;
+  const bool wide = cols % 8 == 0 && rows_aligned(x, ld_x, elt, 8);
+  return call.launch(kOpBlocks, [&] {
+    return dtype == NS_BF16 ? run_store<kBF16>(p, true, wide, call.sms, call.s) : run_store<kF32>(p, true, wide, call.sms, call.s);
+  });
+}
+
+extern "C" int ns_blocks_load(const void *q, const void *scales, int tiles, int groups, int64_t rows, int64_t cols,
+                              void *out, int64_t ld_out, int dtype, void *stream) {
+  if (bad_dtype(dtype) || groups < 0 || (tiles != 0 && tiles != 1) || (!tiles && groups != 1) ||
+      bad_shape(rows, cols, ld_out) || cols > kMaxRowCols ||
+      (groups > 0 && bad_shape(static_cast<int64_t>(groups) * rows, cols, ld_out)))
+    return NS_EINVAL;
+  if (groups == 0 || rows == 0 || cols == 0) return NS_OK;
+  if (!out || !q || !scales) return NS_EINVAL;
+  const int elt = dtype == NS_BF16 ? 2 : 4;
+  if (misaligned(out, elt) || misaligned(q, 16) || misaligned(scales, 16)) return NS_EALIGN;
+  BlocksParams p{};
+  p.pitch = static_cast<int>(ns_blocks_pitch(cols));
+  p.scale_pitch = static_cast<int>(ns_blocks_scale_pitch(cols));
+  const int64_t all = static_cast<int64_t>(groups) * rows;
+  const int64_t bands = tiles ? static_cast<int64_t>(groups) * ((rows + kBlock - 1) / kBlock) : all;
+  const Range ro(out, all, cols, ld_out, elt);
+  if (ro.overlaps(Range(q, all, p.pitch, p.pitch, 1)) || ro.overlaps(Range(scales, bands, p.scale_pitch, p.scale_pitch, 1)))
+    return NS_EINVAL;
+  OpCall call(stream);
+  if (call.rc) return call.rc;
+  p.out = out;
+  p.ld = ld_out;
+  p.rows = rows;
+  p.q = static_cast<uint8_t *>(const_cast<void *>(q));
+  p.s = static_cast<uint8_t *>(const_cast<void *>(scales));
+  p.cols = static_cast<int>(cols);
+  p.groups = groups;
+  p.tiles = tiles;
+  p.status = call.status;
+  const bool wide = cols % 8 == 0 && rows_aligned(out, ld_out, elt, 8);
+  return call.launch(kOpBlocks, [&] {
+    return dtype == NS_BF16 ? run_load<kBF16>(p, wide, call.sms, call.s) : run_load<kF32>(p, wide, call.sms, call.s);
+  });
+}

@@ -242,6 +242,11 @@ enum OpKind : int {
   kOpPolicy,
   kOpCkpt,
   kOpWgrad,
+  kOpRoute,
+  kOpBlocks,
+  kOpBlocksMatmul,
+  kOpBlockNorm,
+  kOpDropout,
   kOpKindEnd
 };
 // Workspace cache slots of the operators (one scratch per operator and
@@ -263,7 +268,7 @@ struct OpCall {
   ~OpCall();
   // at least `bytes`; when this call allocates it, its first `zero` bytes are zero
   int workspace(int slot, size_t bytes, uint8_t **ptr, size_t zero = 0);
-  // elt 2: bf16, elt 4: fp32; 128-byte swizzle; reads outside give 0, writes outside are dropped
+  // elt 1: bytes, elt 2: bf16, elt 4: fp32; 128-byte swizzle; reads outside give 0, writes outside are dropped
   int tensor_map(CUtensorMap *map, int elt, const void *base, int rank, const int64_t *dims,
                  const int64_t *pitch_bytes, const int *box);
   // fn() launches kernels of one kind and returns 0, or -1 on a launch error

@@ -92,6 +92,83 @@ struct RowPart {
   }
 };
 
+// Eight consecutive columns of a row per lane, for element-wise kernels whose lanes need neighbours. WIDE: rows that
+// allow packs of 8 (whole packs lie in the row or outside). Else a warp's 256 columns from c0 on are read and written
+// lane by lane, coalesced, and exchanged through the warp's piece of shared memory, kStage 16-byte words.
+template <int DT, bool WIDE>
+struct Eight {
+  using E = typename Elem<DT>::T;
+  static constexpr int kStage = 32 * 8 * static_cast<int>(sizeof(E)) / 16;
+  Pack<DT, 8> v;
+  // here: the row is to be read (its other columns read as zeros); all lanes of the warp call these
+  __device__ __forceinline__ void load(const E *row, int c, int cols, bool here) {
+    if constexpr (WIDE) {
+      if (here && c < cols) {
+        v.load_stream(row + c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.set(e, 0.f);
+      }
+    } else {
+      const int lane = threadIdx.x & 31, first = c - lane * 8 + lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        reinterpret_cast<E *>(v.w)[e] = here && first + e * 32 < cols ? __ldcs(row + first + e * 32) : Elem<DT>::from_f(0.f);
+    }
+  }
+  __device__ __forceinline__ void settle(uint4 *stage) {
+    if constexpr (!WIDE) {
+      const int lane = threadIdx.x & 31;
+      E *s = reinterpret_cast<E *>(stage);
+      constexpr int kW = sizeof(v.w) / 16;
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e * 32 + lane] = reinterpret_cast<const E *>(v.w)[e];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kW; ++i) reinterpret_cast<uint4 *>(v.w)[i] = stage[lane * kW + i];
+    }
+  }
+  __device__ __forceinline__ float get(int e) const { return v.get(e); }
+  __device__ __forceinline__ void set(int e, float x) { v.set(e, x); }
+  __device__ __forceinline__ void store(E *row, int c, int cols, bool here, uint4 *stage, const void *base, size_t size,
+                                        int *status) const {
+    if constexpr (WIDE) {
+      if (here && c < cols) v.store_stream(row + c, base, size, status);
+    } else {
+      const int lane = threadIdx.x & 31, first = c - lane * 8 + lane;
+      constexpr int kW = sizeof(v.w) / 16;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kW; ++i) stage[lane * kW + i] = reinterpret_cast<const uint4 *>(v.w)[i];
+      __syncwarp();
+      const E *s = reinterpret_cast<const E *>(stage) + lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (here && first + e * 32 < cols && in_bounds(row + first + e * 32, sizeof(E), base, size, status))
+          __stcs(row + first + e * 32, s[e * 32]);
+    }
+  }
+};
+
+// How a block of kThreads threads covers rows of 8-column packs: lanes 1 << lanes_log2 to a row (at least
+// 1 << least_log2, whole warps where lanes exchange values), kThreads >> lanes_log2 rows at a time, further columns
+// by blockIdx.x, walking down the rows by gridDim.y.
+struct EightGrid {
+  int lanes_log2;
+  dim3 grid;
+  EightGrid(int64_t rows, int64_t extent, int threads, bool wide, int least_log2, int sms, int per_sm) {
+    const int64_t lanes = (extent + 7) / 8;
+    lanes_log2 = wide ? least_log2 : 5;
+    while ((2 << lanes_log2) <= threads && (1 << lanes_log2) < lanes) ++lanes_log2;
+    const int64_t gx = (lanes + (1 << lanes_log2) - 1) >> lanes_log2;
+    const int64_t height = threads >> lanes_log2, want = (rows + height - 1) / height;
+    int64_t most = static_cast<int64_t>(sms) * per_sm / gx;
+    most = most < 1 ? 1 : most > 65535 ? 65535 : most;
+    grid = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(want < most ? want : most), 1);
+  }
+};
+
 // Token ids: int32 or int64; anything outside [0, vocab) becomes -1.
 struct Ids {
   const void *p;
