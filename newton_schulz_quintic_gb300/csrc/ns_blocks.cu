@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) ns_blocks_store_rows_kernel(const __
   const int height = kThreads >> p.lanes_log2;
   const int64_t step = static_cast<int64_t>(gridDim.y) * height;
   const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
+  asm volatile("griddepcontrol.launch_dependents;");  // a product may set itself up meanwhile
   for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < p.rows; t0 += step) {
     const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
     const bool row = t < p.rows;

@@ -80,21 +80,23 @@ def route(logits, top_k: int, live=None, renormalise: bool = True, balance_coef:
         raise ValueError("top_k must be between 1 and the number of experts")
     p_live = None if live is None else _vector(live, "live", n, (torch.bool,), dev)
     slots = n * top_k
+    # everything in one allocation: ids, order, counts, offsets, live rows | weights, logz, loss | scratch
+    at_f = 2 * slots + 2 * experts + 2
+    at_work = at_f + slots + n + 1
     scratch = max(1, min(-(-n // 8), _MAX_STRETCHES)) * (2 * experts + 2)
     with _on(dev, stream):
-        # one allocation for what the call returns, one for its scratch
-        ints = _empty(2 * slots + 2 * experts + 2, dtype=_I32, device=dev)
-        floats = _empty(slots + n + 1, dtype=_F32, device=dev)
-        work = _empty(scratch, dtype=_I32, device=dev)
-        p_i, p_f = ints.data_ptr(), floats.data_ptr()
+        floats = _empty(at_work + scratch, dtype=_F32, device=dev)
+        p = floats.data_ptr()
         _call("ns_route", logits.data_ptr(), ld, n, experts, top_k, p_live, 1 if renormalise else 0, balance_coef, z_coef,
-              p_i, p_f, p_f + 4 * slots, p_i + 8 * slots, p_i + 8 * slots + 4 * experts, p_i + 4 * slots,
-              p_i + 8 * slots + 8 * experts + 4, p_f + 4 * (slots + n), work.data_ptr(), 4 * scratch, _DTYPE[logits.dtype],
+              p, p + 4 * at_f, p + 4 * (at_f + slots), p + 8 * slots, p + 8 * slots + 4 * experts, p + 4 * slots,
+              p + 4 * at_f - 4, p + 4 * at_work - 4, p + 4 * at_work, 4 * scratch, _DTYPE[logits.dtype],
               _raw_stream(dev.index))
-    at = 2 * slots
-    return Routing(ints[:slots].view(n, top_k), floats[:slots].view(n, top_k), ints[at:at + experts],
-                   ints[at + experts:at + 2 * experts + 1], ints[slots:at], floats[slots + n], floats[slots:slots + n],
-                   ints[at + 2 * experts + 1])
+    ints = floats.view(_I32)
+    part, at = ints.as_strided, 2 * slots
+    return Routing(part((n, top_k), (top_k, 1), 0), floats.as_strided((n, top_k), (top_k, 1), at_f),
+                   part((experts,), (1,), at), part((experts + 1,), (1,), at + experts), part((slots,), (1,), slots),
+                   floats.as_strided((), (), at_work - 1), floats.as_strided((n,), (1,), at_f + slots),
+                   part((), (), at_f - 1))
 
 
 def route_backward(logits, routing: Routing, dweights=None, renormalise: bool = True, balance_coef: float = 0.0,
@@ -143,37 +145,59 @@ class Blocks8:
     values, rounded up to 4 a row). Tiles form (a stack of matrices): q groups x
     rows x .., scales groups x ceil(rows / 128) x .., one per 128 x 128 values."""
 
-    __slots__ = ("groups", "rows", "cols", "tiles", "device", "q", "scales")
+    __slots__ = ("groups", "rows", "cols", "tiles", "device", "_q", "_scales", "_buffer", "_p_q", "_p_scales")
 
     def __init__(self, q, scales, cols: int, tiles: bool = False):
-        cols, lead = int(cols), 2 if tiles else 1
-        if q.dim() != lead + 1 or scales.dim() != lead + 1:
+        cols, lead = int(cols), 3 if tiles else 2
+        if q.dim() != lead or scales.dim() != lead:
             raise ValueError("q and scales must be 3-D for tiles, 2-D for rows")
-        groups, rows = (q.shape[0] if tiles else 1), q.shape[-2]
-        head, bands = ((groups,), (rows + 127) // 128) if tiles else ((), rows)
-        if q.dtype != torch.uint8 or q.shape != (*head, rows, _pitch(cols)) or not q.is_contiguous():
-            raise ValueError(f"q must be contiguous uint8 of shape {(*head, rows, _pitch(cols))}")
-        if scales.dtype != torch.uint8 or scales.shape != (*head, bands, _scale_pitch(cols)) or not scales.is_contiguous():
-            raise ValueError(f"scales must be contiguous uint8 of shape {(*head, bands, _scale_pitch(cols))}")
+        self.groups, self.rows, self.cols, self.tiles = (q.shape[0] if tiles else 1), q.shape[-2], cols, bool(tiles)
+        self.device = q.device
+        want_q, want_s = self._shapes()
+        if q.dtype != torch.uint8 or q.shape != want_q or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous uint8 of shape {want_q}")
+        if scales.dtype != torch.uint8 or scales.shape != want_s or not scales.is_contiguous():
+            raise ValueError(f"scales must be contiguous uint8 of shape {want_s}")
         if not q.is_cuda or scales.device != q.device:
             raise ValueError("q and scales must be CUDA tensors on one device")
-        self.groups, self.rows, self.cols, self.tiles, self.device = groups, rows, cols, bool(tiles), q.device
-        self.q, self.scales = q, scales
+        self._q, self._scales, self._buffer = q, scales, None
+        self._p_q, self._p_scales = q.data_ptr(), scales.data_ptr()
+
+    def _shapes(self):
+        pitch, scale_pitch = _pitch(self.cols), _scale_pitch(self.cols)
+        if self.tiles:
+            return (self.groups, self.rows, pitch), (self.groups, (self.rows + 127) // 128, scale_pitch)
+        return (self.rows, pitch), (self.rows, scale_pitch)
 
     @classmethod
     def _empty(cls, groups, rows, cols, tiles, device):
         self = cls.__new__(cls)
         self.groups, self.rows, self.cols, self.tiles, self.device = groups, rows, cols, tiles, device
-        head, bands = ((groups,), (rows + 127) // 128) if tiles else ((), rows)
-        pitch, scale_pitch = _pitch(cols), _scale_pitch(cols)
-        nq = groups * rows * pitch  # a multiple of 16
-        buffer = _empty(nq + groups * bands * scale_pitch, dtype=torch.uint8, device=device)
-        self.q = buffer[:nq].view(*head, rows, pitch)
-        self.scales = buffer[nq:].view(*head, bands, scale_pitch)
+        nq = groups * rows * _pitch(cols)  # a multiple of 16
+        bands = groups * ((rows + 127) // 128) if tiles else rows
+        self._q = self._scales = None  # views of the buffer, made when asked for
+        self._buffer = _empty(nq + bands * _scale_pitch(cols), dtype=torch.uint8, device=device)
+        self._p_q = self._buffer.data_ptr()
+        self._p_scales = self._p_q + nq
         return self
 
+    @property
+    def q(self):
+        if self._q is None:
+            shape = self._shapes()[0]
+            self._q = self._buffer[:self.groups * self.rows * shape[-1]].view(shape)
+        return self._q
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            q, shape = self._shapes()
+            self._scales = self._buffer[self.groups * self.rows * q[-1]:].view(shape)
+        return self._scales
+
     def nbytes(self) -> int:
-        return self.q.numel() + self.scales.numel()
+        bands = self.groups * ((self.rows + 127) // 128) if self.tiles else self.rows
+        return self.groups * self.rows * _pitch(self.cols) + bands * _scale_pitch(self.cols)
 
 
 def blocks_store(x, tiles: bool = False, rows=None, per: int = 1, stream=None) -> Blocks8:
@@ -200,7 +224,7 @@ def blocks_store(x, tiles: bool = False, rows=None, per: int = 1, stream=None) -
         dev = x.device
         with _on(dev, stream):
             b = Blocks8._empty(groups, n, cols, True, dev)
-            _call("ns_blocks_store_tiles", x.data_ptr(), ld, groups, n, cols, b.q.data_ptr(), b.scales.data_ptr(),
+            _call("ns_blocks_store_tiles", x.data_ptr(), ld, groups, n, cols, b._p_q, b._p_scales,
                   _DTYPE[x.dtype], _raw_stream(dev.index))
         return b
     ld = _matrix(x, "x")
@@ -216,7 +240,7 @@ def blocks_store(x, tiles: bool = False, rows=None, per: int = 1, stream=None) -
         raise ValueError("per needs rows")
     with _on(dev, stream):
         b = Blocks8._empty(1, count, cols, False, dev)
-        _call("ns_blocks_store_rows", x.data_ptr(), ld, n, p_rows, per, count, cols, b.q.data_ptr(), b.scales.data_ptr(),
+        _call("ns_blocks_store_rows", x.data_ptr(), ld, n, p_rows, per, count, cols, b._p_q, b._p_scales,
               _DTYPE[x.dtype], _raw_stream(dev.index))
     return b
 
@@ -233,7 +257,7 @@ def blocks_load(b: Blocks8, dtype=torch.bfloat16, out=None, stream=None):
     with _on(dev, stream):
         if out is None:
             out = _empty((b.groups, b.rows, b.cols) if b.tiles else (b.rows, b.cols), dtype=dtype, device=dev)
-        _call("ns_blocks_load", b.q.data_ptr(), b.scales.data_ptr(), 1 if b.tiles else 0, b.groups, b.rows, b.cols,
+        _call("ns_blocks_load", b._p_q, b._p_scales, 1 if b.tiles else 0, b.groups, b.rows, b.cols,
               out.data_ptr(), ld, _DTYPE[out.dtype], _raw_stream(dev.index))
     return out
 
@@ -266,7 +290,7 @@ def blocks_matmul(a: Blocks8, w: Blocks8, transpose: bool = False, offsets=None,
     with _on(dev, stream):
         if out is None:
             out = _empty((a.rows, n), dtype=dtype, device=dev)
-        _call("ns_blocks_matmul", a.q.data_ptr(), a.scales.data_ptr(), a.rows, k, w.q.data_ptr(), w.scales.data_ptr(), n,
+        _call("ns_blocks_matmul", a._p_q, a._p_scales, a.rows, k, w._p_q, w._p_scales, n,
               1 if transpose else 0, p_off, w.groups, out.data_ptr(), ld, _DTYPE[out.dtype], _raw_stream(dev.index))
     return out
 
@@ -275,8 +299,7 @@ def blocks_matmul(a: Blocks8, w: Blocks8, transpose: bool = False, offsets=None,
 class BlockNorm(NamedTuple):
     residual: torch.Tensor            # rows x cols, type of x
     normed: torch.Tensor | None       # rows x cols, type of y
-    post_rstd: torch.Tensor | None    # per row, float32, for the backward pass
-    pre_rstd: torch.Tensor | None
+    rstd: torch.Tensor                # 2 x rows, float32, for the backward pass: of y, of residual
 
 
 class BlockNormGrads(NamedTuple):
@@ -350,12 +373,12 @@ def block_norm(x, y=None, gate=None, post_weight=None, pre_weight=None, residual
             residual = _empty((n, cols), dtype=x.dtype, device=dev)
         if normed is None and pre_weight is not None:
             normed = _empty((n, cols), dtype=bt, device=dev)
-        post = None if post_weight is None else _empty(n, dtype=_F32, device=dev)
-        pre = None if pre_weight is None else _empty(n, dtype=_F32, device=dev)
+        rstd = _empty((2, n), dtype=_F32, device=dev)
+        p_rstd = rstd.data_ptr()
         _call("ns_block_norm", x.data_ptr(), ld_x, _ptr(y), ld_y, _ptr(gate), form, ld_g, _ptr(post_weight),
               _ptr(pre_weight), n, cols, residual_scale, block_scale, eps, residual.data_ptr(), ld_r, _ptr(normed), ld_z,
-              _ptr(post), _ptr(pre), *codes, _raw_stream(dev.index))
-    return BlockNorm(residual, normed, post, pre)
+              p_rstd, p_rstd + 4 * n, *codes, _raw_stream(dev.index))
+    return BlockNorm(residual, normed, rstd)
 
 
 def block_norm_backward(dresidual, dnormed, x, y, saved: BlockNorm, gate=None, post_weight=None, pre_weight=None,
@@ -375,8 +398,7 @@ def block_norm_backward(dresidual, dnormed, x, y, saved: BlockNorm, gate=None, p
     bt = x.dtype if y is None else y.dtype
     ld_dr = cols if dresidual is None else _matrix(dresidual, "dresidual", n, cols, x.dtype)
     ld_dz = cols if dnormed is None else _matrix(dnormed, "dnormed", n, cols, bt)
-    p_post = None if post_weight is None else _contiguous(saved.post_rstd, "saved.post_rstd", (n,), _F32, dev)
-    p_pre = None if pre_weight is None else _contiguous(saved.pre_rstd, "saved.pre_rstd", (n,), _F32, dev)
+    p_rstd = _contiguous(saved.rstd, "saved.rstd", (2, n), _F32, dev)
     ld_dx = cols if dx is None else _matrix(dx, "dx", n, cols, x.dtype)
     if dy is not None and y is None:
         raise ValueError("dy given, but no y")
@@ -388,11 +410,16 @@ def block_norm_backward(dresidual, dnormed, x, y, saved: BlockNorm, gate=None, p
         if dy is None and y is not None:
             dy = _empty((n, cols), dtype=bt, device=dev)
         dgate = None if gate is None else _empty(gate.shape, dtype=gate.dtype, device=dev)
-        dpost = None if post_weight is None else _empty(cols, dtype=post_weight.dtype, device=dev)
-        dpre = None if pre_weight is None else _empty(cols, dtype=pre_weight.dtype, device=dev)
+        dpost = dpre = None
+        if post_weight is not None and pre_weight is not None:  # both in one allocation
+            dpost, dpre = _empty((2, cols), dtype=pre_weight.dtype, device=dev).unbind()
+        elif pre_weight is not None:
+            dpre = _empty(cols, dtype=pre_weight.dtype, device=dev)
+        elif post_weight is not None:
+            dpost = _empty(cols, dtype=post_weight.dtype, device=dev)
         work = _empty(max(scratch, 1), dtype=_F32, device=dev)
         _call("ns_block_norm_backward", _ptr(dresidual), ld_dr, _ptr(dnormed), ld_dz, x.data_ptr(), ld_x, _ptr(y), ld_y,
-              _ptr(gate), form, ld_g, _ptr(post_weight), _ptr(pre_weight), p_post, p_pre, n, cols, residual_scale,
+              _ptr(gate), form, ld_g, _ptr(post_weight), _ptr(pre_weight), p_rstd, p_rstd + 4 * n, n, cols, residual_scale,
               block_scale, dx.data_ptr(), ld_dx, _ptr(dy), ld_dy, _ptr(dgate), 1 if form == _ROWS else cols, _ptr(dpost),
               _ptr(dpre), work.data_ptr(), 4 * max(scratch, 1), *codes, _raw_stream(dev.index))
     return BlockNormGrads(dx, dy, dgate, dpost, dpre)
