@@ -30,7 +30,8 @@ struct BlocksParams {
   int64_t rows;           // rows of q (of one matrix of a stack)
   int64_t src_rows;       // rows form: rows of x
   const int32_t *index;   // rows form: row r holds x[index[r] / per]; nullptr: x[r]
-  uint32_t per;
+  uint32_t per, per_mul;  // a division by per of numbers below 2^31: (mulhi(n, per_mul) + n) >> per_shift
+  int per_shift;
   uint8_t *q, *s;
   int cols, pitch, scale_pitch;
   int groups;             // matrices of a stack (tiles)
@@ -84,51 +85,112 @@ template <typename V>
 __device__ __forceinline__ uint2 eight_e4m3(const V &v, float up) {
   uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = to_e4m3x2(v.get(2 * i) * up, v.get(2 * i + 1) * up);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __fmul2_rn(make_float2(v.get(2 * i), v.get(2 * i + 1)), make_float2(up, up));
+    b[i] = to_e4m3x2(f.x, f.y);
+  }
   return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
 }
 
-template <int DT, bool WIDE>
+// Rows that allow packs: 16 columns a lane, 8 lanes a block, so that what a lane does for its row and block (addresses,
+// the scale, shuffles) is spread over 16 values. What bounds it is instructions: 8 columns a lane took 162 a warp for 256
+// values of bf16, 102 us at 16384 x 8192.
+template <int DT, bool GATHER>
 __global__ void __launch_bounds__(kThreads) ns_blocks_store_rows_kernel(const __grid_constant__ BlocksParams p) {
   using E = typename Elem<DT>::T;
-  using V = Eight<DT, WIDE>;
-  __shared__ uint4 stages[WIDE ? 1 : kThreads / 32][WIDE ? 1 : V::kStage];
-  uint4 *stage = stages[WIDE ? 0 : threadIdx.x / 32];
+  const int lanes = 1 << p.lanes_log2;
+  const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & (lanes - 1))) * 16;
+  const int height = kThreads >> p.lanes_log2, step = gridDim.y * height;
+  const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
+  const E *x = static_cast<const E *>(p.x) + c;
+  const int rows = static_cast<int>(p.rows), src_rows = static_cast<int>(p.src_rows);
+  const bool in0 = c < p.cols, in1 = c + 8 < p.cols;
+  asm volatile("griddepcontrol.launch_dependents;");  // a product may set itself up meanwhile
+  int t = blockIdx.y * height + (threadIdx.x >> p.lanes_log2);
+  auto index_at = [&](int r) { return GATHER && r < rows ? __ldg(p.index + r) : -1; };
+  int32_t index = index_at(t);
+  for (int t0 = blockIdx.y * height; t0 < rows; t0 += step, t += step) {
+    int from = t;
+    bool here = t < rows;
+    if (GATHER) {
+      // index / per: the product with the rounded-up reciprocal, for dividends below 2^31
+      from = static_cast<int>((__umulhi(static_cast<uint32_t>(index), p.per_mul) + static_cast<uint32_t>(index)) >> p.per_shift);
+      here = index >= 0 && from < src_rows;
+      index = index_at(t + step);
+    }
+    const E *at = x + static_cast<int64_t>(from) * p.ld;
+    Pack<DT, 8> v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (here && (h == 0 ? in0 : in1)) {
+        if (GATHER)
+          v[h].load(at + 8 * h);  // rows that are read again stay in the caches
+        else
+          v[h].load_stream(at + 8 * h);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[h].set(e, 0.f);
+      }
+    }
+    uint32_t top = max(top_of<DT>(v[0]), top_of<DT>(v[1]));
+#pragma unroll
+    for (int o = 1; o < kBlock / 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t sb = scale_byte(top);
+    const float up = up_of(sb);
+    const uint2 lo = eight_e4m3(v[0], up), hi = eight_e4m3(v[1], up);
+    if (t < rows) {
+      if (in0) {  // the padding behind the row is part of its last 16
+        const uint2 high = in1 ? hi : make_uint2(0, 0);  // zeros behind a NaN block too
+        uint4 *to = reinterpret_cast<uint4 *>(p.q + static_cast<int64_t>(t) * p.pitch + c);
+        if (in_bounds(to, 16, p.q, qsize, p.status)) {
+          if (GATHER)
+            __stcs(to, make_uint4(lo.x, lo.y, high.x, high.y));
+          else
+            *to = make_uint4(lo.x, lo.y, high.x, high.y);
+        }
+      }
+      if (c % kBlock == 0 && c / kBlock < p.scale_pitch)
+        put(p.s + static_cast<int64_t>(t) * p.scale_pitch + c / kBlock, static_cast<uint8_t>(in0 ? sb : 0), p.s, ssize, p.status);
+    }
+  }
+}
+
+// Any rows: 8 columns a lane, through shared memory.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) ns_blocks_store_any_kernel(const __grid_constant__ BlocksParams p) {
+  using E = typename Elem<DT>::T;
+  using V = Eight<DT, false>;
+  __shared__ uint4 stages[kThreads / 32][V::kStage];
+  uint4 *stage = stages[threadIdx.x / 32];
   const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * 8;
   const int height = kThreads >> p.lanes_log2;
   const int64_t step = static_cast<int64_t>(gridDim.y) * height;
   const size_t qsize = static_cast<size_t>(p.rows) * p.pitch, ssize = static_cast<size_t>(p.rows) * p.scale_pitch;
-  asm volatile("griddepcontrol.launch_dependents;");  // a product may set itself up meanwhile
+  asm volatile("griddepcontrol.launch_dependents;");
   for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < p.rows; t0 += step) {
     const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
-    const bool row = t < p.rows;
-    int64_t from = t;
-    if (p.index) {
-      const int32_t i = row ? __ldg(p.index + t) : -1;
+    int64_t from = t < p.rows ? t : -1;
+    if (p.index && t < p.rows) {
+      const int32_t i = __ldg(p.index + t);
       from = i < 0 ? -1 : static_cast<int64_t>(static_cast<uint32_t>(i) / p.per);
+      if (from >= p.src_rows) from = -1;
     }
-    const bool here = row && from >= 0 && from < p.src_rows;
     V x;
-    x.load(static_cast<const E *>(p.x) + (here ? from : 0) * p.ld, c, p.cols, here);
+    x.load(static_cast<const E *>(p.x) + (from >= 0 ? from : 0) * p.ld, c, p.cols, from >= 0);
     x.settle(stage);
     uint32_t top = top_of<DT>(x.v);
 #pragma unroll
     for (int o = 1; o < kBlock / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const uint32_t sb = scale_byte(top);
-    const uint2 w = eight_e4m3(x, up_of(sb));
-    if (!row) continue;
-    // columns past the row were read as zeros, and so is what lies behind it (a NaN block's too)
-    if (c < p.pitch) {
-      uint2 v = w;
-      if (sb == 255 && c + 8 > p.cols) {
-        uint8_t *b = reinterpret_cast<uint8_t *>(&v);
+    uint2 v = eight_e4m3(x, up_of(sb));
+    if (sb == 255 && c + 8 > p.cols) {  // behind the row lie zeros, in a NaN block too
+      uint8_t *b = reinterpret_cast<uint8_t *>(&v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e >= p.cols) b[e] = 0;
-      }
-      put(p.q + t * p.pitch + c, v, p.q, qsize, p.status);
+      for (int e = 0; e < 8; ++e)
+        if (c + e >= p.cols) b[e] = 0;
     }
-    if (c % kBlock == 0 && c / kBlock < p.scale_pitch)
+    if (t < p.rows && c < p.pitch) put(p.q + t * p.pitch + c, v, p.q, qsize, p.status);
+    if (t < p.rows && c % kBlock == 0 && c / kBlock < p.scale_pitch)
       put(p.s + t * p.scale_pitch + c / kBlock, static_cast<uint8_t>(c < p.cols ? sb : 0), p.s, ssize, p.status);
   }
 }
@@ -193,12 +255,55 @@ __global__ void __launch_bounds__(kThreads) ns_blocks_store_tiles_kernel(const _
   }
 }
 
-template <int DT, bool WIDE>
+// Row of scales that belongs to row t of all.
+__device__ __forceinline__ int64_t scale_row(const BlocksParams &p, int64_t t, int64_t bands) {
+  if (!p.tiles) return t;
+  if (p.groups == 1) return t / kBlock;
+  const int64_t g = t / p.rows;
+  return g * bands + (t - g * p.rows) / kBlock;
+}
+template <int DT>
+__device__ __forceinline__ void eight_values(uint2 w, float unit, Pack<DT, 8> &v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i % 2)), a, b);
+    const float2 f = __fmul2_rn(make_float2(a, b), make_float2(unit, unit));
+    v.set(2 * i, f.x);
+    v.set(2 * i + 1, f.y);
+  }
+}
+
+// Rows that allow packs: 16 columns a lane.
+template <int DT>
 __global__ void __launch_bounds__(kThreads) ns_blocks_load_kernel(const __grid_constant__ BlocksParams p) {
   using E = typename Elem<DT>::T;
-  using V = Eight<DT, WIDE>;
-  __shared__ uint4 stages[WIDE ? 1 : kThreads / 32][WIDE ? 1 : V::kStage];
-  uint4 *stage = stages[WIDE ? 0 : threadIdx.x / 32];
+  const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * 16;
+  const int height = kThreads >> p.lanes_log2;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * height, all = p.rows * p.groups;
+  const int64_t bands = (p.rows + kBlock - 1) / kBlock;
+  const size_t size = static_cast<size_t>((all - 1) * p.ld + p.cols) * sizeof(E);
+  if (c >= p.cols) return;
+  for (int64_t t = static_cast<int64_t>(blockIdx.y) * height + (threadIdx.x >> p.lanes_log2); t < all; t += step) {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.q + t * p.pitch + c));
+    const float unit = unit_of(p.s[scale_row(p, t, bands) * p.scale_pitch + c / kBlock]);
+    E *to = static_cast<E *>(p.out) + t * p.ld + c;
+    Pack<DT, 8> v;
+    eight_values<DT>(make_uint2(w.x, w.y), unit, v);
+    v.store_stream(to, p.out, size, p.status);
+    if (c + 8 < p.cols) {
+      eight_values<DT>(make_uint2(w.z, w.w), unit, v);
+      v.store_stream(to + 8, p.out, size, p.status);
+    }
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) ns_blocks_load_any_kernel(const __grid_constant__ BlocksParams p) {
+  using E = typename Elem<DT>::T;
+  using V = Eight<DT, false>;
+  __shared__ uint4 stages[kThreads / 32][V::kStage];
+  uint4 *stage = stages[threadIdx.x / 32];
   const int c = ((blockIdx.x << p.lanes_log2) + (threadIdx.x & ((1 << p.lanes_log2) - 1))) * 8;
   const int height = kThreads >> p.lanes_log2;
   const int64_t step = static_cast<int64_t>(gridDim.y) * height, all = p.rows * p.groups;
@@ -206,24 +311,11 @@ __global__ void __launch_bounds__(kThreads) ns_blocks_load_kernel(const __grid_c
   const size_t size = static_cast<size_t>((all - 1) * p.ld + p.cols) * sizeof(E);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * height; t0 < all; t0 += step) {
     const int64_t t = t0 + (threadIdx.x >> p.lanes_log2);
-    const bool row = t < all;
     V o;
-    if (row && c < p.cols) {
-      const int64_t g = p.tiles ? t / p.rows : 0, band = p.tiles ? g * bands + (t - g * p.rows) / kBlock : t;
-      const float unit = unit_of(p.s[band * p.scale_pitch + c / kBlock]);
-      const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p.q + t * p.pitch + c));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float a, b;
-        from_e4m3x2((i < 2 ? w.x : w.y) >> (16 * (i % 2)), a, b);
-        o.set(2 * i, a * unit);
-        o.set(2 * i + 1, b * unit);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o.set(e, 0.f);
-    }
-    o.store(static_cast<E *>(p.out) + t * p.ld, c, p.cols, row, stage, p.out, size, p.status);
+    if (t < all && c < p.cols)
+      eight_values<DT>(__ldcs(reinterpret_cast<const uint2 *>(p.q + t * p.pitch + c)),
+                       unit_of(p.s[scale_row(p, t, bands) * p.scale_pitch + c / kBlock]), o.v);
+    o.store(static_cast<E *>(p.out) + t * p.ld, c, p.cols, t < all, stage, p.out, size, p.status);
   }
 }
 
@@ -238,12 +330,18 @@ int run_store(BlocksParams &p, bool tiles, bool wide, int sms, cudaStream_t s) {
       ns_blocks_store_tiles_kernel<DT, false><<<grid, kThreads, 0, s>>>(p);
   } else {
     const int64_t extent = std::max<int64_t>(p.pitch, static_cast<int64_t>(p.scale_pitch) * kBlock);
-    const EightGrid g(p.rows, extent, kThreads, wide, 4, sms, wide ? 128 : 32);
-    p.lanes_log2 = g.lanes_log2;
-    if (wide)
-      ns_blocks_store_rows_kernel<DT, true><<<g.grid, kThreads, 0, s>>>(p);
-    else
-      ns_blocks_store_rows_kernel<DT, false><<<g.grid, kThreads, 0, s>>>(p);
+    if (wide) {
+      const EightGrid g(p.rows, (extent + 1) / 2, kThreads, true, 3, sms, 128);  // 16 columns a lane
+      p.lanes_log2 = g.lanes_log2;
+      if (p.index)
+        ns_blocks_store_rows_kernel<DT, true><<<g.grid, kThreads, 0, s>>>(p);
+      else
+        ns_blocks_store_rows_kernel<DT, false><<<g.grid, kThreads, 0, s>>>(p);
+    } else {
+      const EightGrid g(p.rows, extent, kThreads, false, 4, sms, 32);
+      p.lanes_log2 = g.lanes_log2;
+      ns_blocks_store_any_kernel<DT><<<g.grid, kThreads, 0, s>>>(p);
+    }
   }
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
@@ -251,12 +349,15 @@ int run_store(BlocksParams &p, bool tiles, bool wide, int sms, cudaStream_t s) {
 
 template <int DT>
 int run_load(BlocksParams &p, bool wide, int sms, cudaStream_t s) {
-  const EightGrid g(p.rows * p.groups, p.cols, kThreads, wide, 2, sms, wide ? 128 : 32);
-  p.lanes_log2 = g.lanes_log2;
-  if (wide)
-    ns_blocks_load_kernel<DT, true><<<g.grid, kThreads, 0, s>>>(p);
-  else
-    ns_blocks_load_kernel<DT, false><<<g.grid, kThreads, 0, s>>>(p);
+  if (wide) {
+    const EightGrid g(p.rows * p.groups, (p.cols + 1) / 2, kThreads, true, 2, sms, 128);
+    p.lanes_log2 = g.lanes_log2;
+    ns_blocks_load_kernel<DT><<<g.grid, kThreads, 0, s>>>(p);
+  } else {
+    const EightGrid g(p.rows * p.groups, p.cols, kThreads, false, 5, sms, 32);
+    p.lanes_log2 = g.lanes_log2;
+    ns_blocks_load_any_kernel<DT><<<g.grid, kThreads, 0, s>>>(p);
+  }
   count_launch();
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -273,7 +374,8 @@ extern "C" int64_t ns_blocks_scale_pitch(int64_t cols) { return cols < 0 ? -1 : 
 
 extern "C" int ns_blocks_store_rows(const void *x, int64_t ld_x, int64_t x_rows, const int32_t *index, int per,
                                     int64_t rows, int64_t cols, void *q, void *scales, int dtype, void *stream) {
-  if (bad_dtype(dtype) || bad_shape(x_rows, cols, ld_x) || bad_shape(rows, cols, cols) || cols > kMaxRowCols || per < 1)
+  if (bad_dtype(dtype) || bad_shape(x_rows, cols, ld_x) || bad_shape(rows, cols, cols) || cols > kMaxRowCols || rows > (1 << 30) ||
+      x_rows > (1 << 30) || per < 1)
     return NS_EINVAL;
   if (!index && (rows != x_rows || per != 1)) return NS_EINVAL;
   if (rows == 0 || cols == 0) return NS_OK;
@@ -294,6 +396,8 @@ extern "C" int ns_blocks_store_rows(const void *x, int64_t ld_x, int64_t x_rows,
   p.src_rows = x_rows;
   p.index = index;
   p.per = static_cast<uint32_t>(per);
+  while ((uint64_t(1) << p.per_shift) < p.per) ++p.per_shift;
+  p.per_mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << p.per_shift) - p.per)) / p.per + 1);
   p.q = static_cast<uint8_t *>(q);
   p.s = static_cast<uint8_t *>(scales);
   p.cols = static_cast<int>(cols);
