@@ -26,7 +26,8 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
   using X = typename Elem<XT>::T;
   using Y = typename Elem<YT>::T;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float reds[8][64];
+  __shared__ RowSums reds;
+  reds.clear();
   RingBarriers *bar = start_ring(ring, smem);
   uint8_t *slots = smem + kRingHead;
   const Waiter w{&bar->abort, p.status, p.wait_limit_ns};
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
   const bool fills = WIDE && threadIdx.x < 32;
   if (fills) filler.first(ring, bar, slots, p.rows, w);
   const int group = threadIdx.x / ring.threads, thread = threadIdx.x - group * ring.threads;
-  RowSum sum{reds[group], ring.threads, 1 + group, 0, thread};
+  RowSum sum{reds.red[group], ring.threads, 1 + group, 0, thread};
   const size_t rsize = static_cast<size_t>((p.rows - 1) * p.ld_r + p.cols) * sizeof(X);
   const size_t zsize = static_cast<size_t>((p.rows - 1) * p.ld_z + p.cols) * sizeof(Y);
   const float inv_n = 1.f / static_cast<float>(p.cols);
@@ -48,26 +49,31 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
   for (int i = 0; i < NP; ++i)
     c[i] = WIDE ? (i * ring.threads + thread) * 8 : (i * ring.threads + (thread & ~31)) * 8 + (thread & 31);
   const ColumnWeights<WIDE, NP> held{reinterpret_cast<float4 *>(slots + ring.slots * ring.slot_bytes) + thread, ring.threads};
-  if (kHold<NP> && group == 0) held.keep(p, c);
+  if (p.hold && group == 0) held.keep(p, c);
   asm volatile("bar.sync 15, %0;" ::"r"(consumers) : "memory");
   RowReader reader;
   bool ok = true;
-  for (int64_t b = blockIdx.x; b * ring.height < p.rows; b += gridDim.x) {
+  const uint32_t rows = static_cast<uint32_t>(p.rows), step = gridDim.x * ring.height;
+  uint32_t t = blockIdx.x * ring.height + group;
+  const StreamRow<XT, WIDE, 0> xs(ring, group);
+  const StreamRow<YT, WIDE, 1> ys(ring, group);
+  X *to = static_cast<X *>(p.r) + t * p.ld_r;
+  Y *zt = static_cast<Y *>(p.z) + t * p.ld_z;
+  int64_t ahead = blockIdx.x + static_cast<int64_t>(ring.slots) * gridDim.x;
+  for (uint32_t t0 = blockIdx.x * ring.height; t0 < rows; t0 += step, t += step, to += step * p.ld_r, zt += step * p.ld_z,
+                ahead += gridDim.x) {
     const uint8_t *at = reader.wait(ring, bar, slots, w, ok);
-    const int64_t t = b * ring.height + group;
-    if (t >= p.rows) {  // (never the first group)
+    if (t >= rows) {  // (never the first group)
       reader.release(ring, bar);
       continue;
     }
-    const uint8_t *rows[kStreams];
-    rows_of<WIDE>(ring, at, group, t, rows);
     Eight2 r[NP], y[NP];
     float2 s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      load8<XT, WIDE>(rows[0], c[i], p.cols, r[i]);
+      xs.load(ring, at, t, c[i], p.cols, r[i]);
       if (p.y) {
-        load8<YT, WIDE>(rows[1], c[i], p.cols, y[i]);
+        ys.load(ring, at, t, c[i], p.cols, y[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(y[i].v[j], y[i].v[j], s2);
       }
@@ -100,8 +106,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[i].v[j] = __fmul2_rn(r[i].v[j], both(p.a));
     }
-    if (fills) filler.fill(ring, bar, slots, p.rows, b + static_cast<int64_t>(ring.slots) * gridDim.x, w);
-    X *to = static_cast<X *>(p.r) + t * p.ld_r;
+    if (fills) filler.fill(ring, bar, slots, p.rows, ahead, w);
 #pragma unroll
     for (int i = 0; i < NP; ++i)
       if (ok) store8<XT, WIDE>(to, c[i], p.cols, r[i], p.r, rsize, p.status);
@@ -113,7 +118,6 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
         for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(r[i].v[j], r[i].v[j], s2);
       const float rr = rsqrtf(sum(s2.x + s2.y) * inv_n + p.eps);
       if (thread == 0 && ok) p.pre_rstd[t] = rr;
-      Y *zt = static_cast<Y *>(p.z) + t * p.ld_z;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         Eight2 f;
@@ -177,7 +181,8 @@ extern "C" int ns_block_norm(const void *x, int64_t ld_x, const void *y, int64_t
   p.status = call.status;
   p.wait_limit_ns = kWaitLimitNs;
   const bool wide = packs_fit(p, dtype, block_dtype) && rows_aligned(residual, ld_r, xe, 8) && (!pre || rows_aligned(normed, ld_z, ye, 8));
-  const Shape sh(p, false, wide, dtype, block_dtype);
+  const Shape sh(p, false, wide, dtype, block_dtype, call.sms);
+  p.hold = sh.hold;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(sh.batches(rows), static_cast<int64_t>(call.sms) * sh.per_sm));
   return call.launch(kOpBlockNorm, [&] {
     const int rc = by_types(dtype, block_dtype, wide, [&](auto xt, auto yt, auto w) {

@@ -29,6 +29,7 @@ struct NormParams {
   float a, b, eps;
   int *status;
   uint64_t wait_limit_ns;
+  int hold;                 // the columns' weights are kept in shared memory
 };
 
 // The 8 columns of a pack that starts at column c, in pairs: consecutive where rows allow packs (WIDE), else every 32nd.
@@ -44,13 +45,14 @@ struct Eight2 {
 };
 __device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
 
-// Columns of a row at `row`, in shared memory (ALIGNED to 16 bytes where WIDE) or global; zeros beyond it.
-template <int DT, bool WIDE>
+// Columns of a row at `row`, in shared memory or global (16-byte aligned where WIDE); zeros beyond it. PADDED: zeros lie
+// behind the row.
+template <int DT, bool WIDE, bool PADDED = false>
 __device__ __forceinline__ void load8(const void *row, int c, int cols, Eight2 &o) {
   using E = typename Elem<DT>::T;
   const E *p = static_cast<const E *>(row);
   if constexpr (WIDE) {
-    if (c < cols) {
+    if (PADDED || c < cols) {
       if constexpr (DT == kBF16) {
         const uint4 w = *reinterpret_cast<const uint4 *>(p + c);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -66,7 +68,7 @@ __device__ __forceinline__ void load8(const void *row, int c, int cols, Eight2 &
     } else {
       o.fill(0.f);
     }
-  } else {
+  } else {  // (what lies behind a ragged row is left from others)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o.v[j] = make_float2(c + 64 * j < cols ? Elem<DT>::to_f(p[c + 64 * j]) : 0.f,
@@ -113,26 +115,38 @@ __device__ __forceinline__ float one_of(const void *p, int64_t i, int type) {
   return type == kBF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
 }
 
-// Sum over the threads of a row, the same on all, in a fixed order. red: 2 x 32 floats of the row's threads, used in
-// turn, so one barrier a sum is enough.
+// Sum over the threads of a row, the same on all, in a fixed order. red: 2 x 16 floats of the row's threads, 0 where
+// there is no warp, used in turn, so one barrier a sum is enough.
 struct RowSum {
   float *red;
   int threads, id, turn, thread;
   __device__ __forceinline__ float operator()(float v) {
     v = warp_sum(v);
     if (threads == 32) return v;
-    float *at = red + turn * 32;
+    float *at = red + turn * 16;
     turn ^= 1;
-    const int lane = thread & 31;
-    if (lane == 0) at[thread / 32] = v;
+    if ((thread & 31) == 0) at[thread / 32] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-    return warp_sum(lane < threads / 32 ? at[lane] : 0.f);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 q = reinterpret_cast<const float4 *>(at)[k];
+      s = __fadd2_rn(s, __fadd2_rn(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+    }
+    return s.x + s.y;
+  }
+};
+constexpr int kMaxHeight = 8;  // rows of a batch: their streams are a warp's lanes
+struct alignas(16) RowSums {
+  float red[kMaxHeight][32];
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < kMaxHeight * 32; i += blockDim.x) red[i / 32][i % 32] = 0.f;
   }
 };
 
 // ------------------------------------------------------------------ the ring of rows
 constexpr int kMaxSlots = 8;
-constexpr int kStreams = 3;  // x, y and (backward) dz
+constexpr int kStreams = 4;  // x, y and (backward) dz, dr
 struct RingBarriers {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   int abort;
@@ -146,6 +160,7 @@ struct RingShape {
   int copy_bytes[kStreams];
   int elt[kStreams];
   int slot_bytes, slots, height, threads;  // threads of a row
+  int padded;               // zeros follow a row up to the columns of all its threads
 };
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -164,7 +179,7 @@ struct Ends {
 };
 
 // Fills the ring, a warp's work: batches blockIdx.x, + gridDim.x, ... in turn. What lies between 16-byte boundaries goes by
-// bulk copies, a lane for each row of a stream. WIDE: that is all, and the CTA's first warp does it beside its rows, once
+// bulk copies, a lane for each row of each stream. WIDE: that is all, and the CTA's first warp does it beside its rows, once
 // every warp has left the slot (a warp of its own for it would leave the others 96 registers a thread instead of 128).
 // Else the rows' ends follow by single elements, which is waited for, so a warp of its own does it.
 template <bool WIDE>
@@ -220,21 +235,21 @@ struct Filler {
     }
     if (lane == 0) mbar_arrive_expect_tx(&bar->full[slot], bytes);
     __syncwarp();
-    if (lane < n) {
+    // a lane for each row of each stream
+    const int q = lane % kStreams, r = lane / kStreams;
+    if (r < n && ring.row_bytes[q]) {
+      const uint8_t *from = ring.src[q] + (b * ring.height + r) * ring.ld_bytes[q];
+      uint8_t *dst = to + r * ring.row_bytes[q];
 #pragma unroll
-      for (int q = 0; q < kStreams; ++q)
-        if (ring.row_bytes[q]) {
-          const uint8_t *from = ring.src[q] + (b * ring.height + lane) * ring.ld_bytes[q];
-          uint8_t *dst = to + lane * ring.row_bytes[q];
-          if constexpr (WIDE) {
-            bulk_load(dst, from, static_cast<uint32_t>(ring.copy_bytes[q]), &bar->full[slot]);
-          } else {
-            const int offset = offset_of(from);
-            const Ends ends(offset, ring.copy_bytes[q]);
-            if (ends.body) bulk_load(dst + offset + ends.head, from + ends.head, static_cast<uint32_t>(ends.body), &bar->full[slot]);
-          }
-          to += ring.height * ring.row_bytes[q];
-        }
+      for (int k = 0; k < kStreams; ++k)
+        if (k < q) dst += ring.height * ring.row_bytes[k];
+      if constexpr (WIDE) {
+        bulk_load(dst, from, static_cast<uint32_t>(ring.copy_bytes[q]), &bar->full[slot]);
+      } else {
+        const int offset = offset_of(from);
+        const Ends ends(offset, ring.copy_bytes[q]);
+        if (ends.body) bulk_load(dst + offset + ends.head, from + ends.head, static_cast<uint32_t>(ends.body), &bar->full[slot]);
+      }
     }
     issued |= 1u << slot;
     last = (last & ~(1u << slot)) | (parity << slot);
@@ -281,19 +296,38 @@ struct RowReader {
     }
   }
 };
-// Where this thread's row of each stream lies: in the slot at `at`, or in memory for one that the ring has no room for.
-template <bool WIDE>
-__device__ __forceinline__ void rows_of(const RingShape &ring, const uint8_t *at, int group, int64_t t, const uint8_t *(&rows)[kStreams]) {
+// One stream's row of this thread: in the slot at `at`, or in memory where the ring has no room for the stream. WIDE rows
+// in the ring are followed by zeros up to the columns of all threads.
+template <int DT, bool WIDE, int Q>
+struct StreamRow {
+  int place;  // in a slot
+  __device__ __forceinline__ StreamRow(const RingShape &ring, int group) {
+    place = group * ring.row_bytes[Q];
 #pragma unroll
-  for (int q = 0; q < kStreams; ++q) {
-    const uint8_t *src = ring.src[q] + t * ring.ld_bytes[q];
-    rows[q] = ring.row_bytes[q] ? at + group * ring.row_bytes[q] + (WIDE ? 0 : offset_of(src)) : src;
-    at += ring.height * ring.row_bytes[q];
+    for (int k = 0; k < Q; ++k) place += ring.height * ring.row_bytes[k];
   }
-}
+  __device__ __forceinline__ void load(const RingShape &ring, const uint8_t *at, uint32_t t, int c, int cols, Eight2 &o) const {
+    const uint8_t *src = ring.src[Q] + t * ring.ld_bytes[Q];
+    if (!ring.row_bytes[Q])
+      load8<DT, WIDE>(src, c, cols, o);
+    else
+      load8<DT, WIDE, true>(at + place + (WIDE ? 0 : offset_of(src)), c, cols, o);
+  }
+};
 
 __device__ __forceinline__ RingBarriers *start_ring(const RingShape &ring, uint8_t *smem) {
   RingBarriers *bar = reinterpret_cast<RingBarriers *>(smem);
+  if (ring.padded) {  // the zeros behind rows, where copies never write
+    uint8_t *slots = smem + (static_cast<int>(sizeof(RingBarriers)) + 127) / 128 * 128;
+    for (int s = 0; s < ring.slots; ++s) {
+      uint8_t *row = slots + s * ring.slot_bytes;
+      for (int q = 0; q < kStreams; ++q)
+        for (int r = 0; r < ring.height && ring.row_bytes[q]; ++r, row += ring.row_bytes[q])
+          for (int i = ring.copy_bytes[q] + static_cast<int>(threadIdx.x) * 16; i < ring.row_bytes[q]; i += blockDim.x * 16)
+            *reinterpret_cast<uint4 *>(row + i) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // bulk copies follow
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ring.slots; ++s) {
       mbar_init(&bar->full[s], 1);
@@ -339,11 +373,10 @@ struct ColumnWeights {
     f.v[3] = make_float2(h.z, h.w);
   }
 };
-// Rows of more than 2 packs a thread have no room for them (nor registers for the columns' sums).
-template <int NP> constexpr bool kHold = NP <= 2;
+// Where shared memory has no room for them they are read again for each row.
 template <bool WIDE, int NP>
 __device__ __forceinline__ void weights_of(const NormParams &p, const ColumnWeights<WIDE, NP> &held, int k, int i, int c, Eight2 &f) {
-  if constexpr (kHold<NP>) {
+  if (p.hold) {
     held.get(k, i, f);
   } else if (k == 1) {
     load_any<WIDE>(p.pre, p.weight_type, c, p.cols, f);
@@ -356,45 +389,52 @@ __device__ __forceinline__ void weights_of(const NormParams &p, const ColumnWeig
   }
 }
 
-// Threads of a row, packs a thread, rows of a CTA of about 256 threads, and the ring: as many slots as leave room for
-// `per_sm` CTAs on an SM, two at least where that is possible at all. A stream for which there is no room at all is read
-// past the ring.
+// Threads of a row, packs a thread, rows that a CTA has in hand at once (so that some compute while others wait for their
+// sums), and the ring: as many slots as leave room for `per_sm` CTAs on an SM, two at least where that is possible. dr is
+// left out where the others then get two slots; a stream for which there is no room at all is read past the ring.
 struct Shape {
-  int threads, packs, rows, per_sm, smem;
+  int threads, packs, rows, per_sm, smem, hold;
   RingShape ring{};
-  Shape(const NormParams &p, bool backward, bool wide, int xt, int yt) {
+  Shape(const NormParams &p, bool backward, bool wide, int xt, int yt, int sms) {
     const int lanes = (p.cols + 7) / 8, most = wide ? kRowThreads : kRaggedRowThreads;
-    packs = lanes <= 256 ? 1 : lanes <= 2 * most ? 2 : 4;
+    // backward has registers for the columns' sums of 2 packs
+    packs = lanes <= 256 ? 1 : lanes <= (backward ? 2 * most : 512) ? 2 : 4;
     threads = ((lanes + packs - 1) / packs + 31) / 32 * 32;
-    rows = threads >= 256 ? 1 : std::min(8, 256 / threads);
+    rows = std::max(1, std::min(kMaxHeight, most / threads));
+    if (packs == 1) rows = std::max(1, std::min(rows, 256 / threads));  // two CTAs an SM
     ring.height = rows;
     ring.threads = threads;
-    const void *src[kStreams] = {p.x, p.y, backward && p.pre ? p.dz : nullptr};
-    const int64_t ld[kStreams] = {p.ld_x, p.ld_y, p.ld_dz};
-    const int elt[kStreams] = {xt == kBF16 ? 2 : 4, yt == kBF16 ? 2 : 4, yt == kBF16 ? 2 : 4};
+    const void *src[kStreams] = {p.x, p.y, backward && p.pre ? p.dz : nullptr, backward ? p.dr : nullptr};
+    const int64_t ld[kStreams] = {p.ld_x, p.ld_y, p.ld_dz, p.ld_dr};
+    const int xe = xt == kBF16 ? 2 : 4, ye = yt == kBF16 ? 2 : 4, elt[kStreams] = {xe, ye, ye, xe};
     int bytes[kStreams];
     for (int q = 0; q < kStreams; ++q) {
       ring.src[q] = static_cast<const uint8_t *>(src[q]);
       ring.ld_bytes[q] = ld[q] * elt[q];
       ring.copy_bytes[q] = p.cols * elt[q];
       ring.elt[q] = elt[q];
-      bytes[q] = src[q] ? (p.cols * elt[q] + 15 + (wide ? 0 : 16)) / 16 * 16 : 0;
+      bytes[q] = !src[q] ? 0 : wide ? threads * packs * 8 * elt[q] : (p.cols * elt[q] + 31) / 16 * 16;
     }
     const int sums = backward ? 2 * packs * 8 * threads * rows * 4 : 0;
-    // behind the ring: the weights, or the sums that registers have no room for
-    const int beside = packs <= 2 ? 2 * packs * 8 * threads * 4 : sums;
+    const int weights = 2 * packs * 8 * threads * 4, extra = backward && packs > 2 ? sums : 0;
     const int room = 224 * 1024 - kRingHead - 2048;  // with the kernel's own
-    int streams = kStreams;
     auto slot_of = [&](int n) {
       int v = 0;
       for (int q = 0; q < n; ++q) v += bytes[q] * rows;
       return v;
     };
+    // weights that a CTA uses for one batch or two are as well read where they lie
+    hold = slot_of(2) + weights + extra <= room && p.rows > 2 * static_cast<int64_t>(rows) * sms ? 1 : 0;
+    const int beside = extra + hold * weights;
+    int streams = kStreams;
+    if ((room - beside) / slot_of(4) < 2 && (room - beside) / slot_of(3) >= 2) streams = 3;
     while (streams > 1 && slot_of(streams) + beside > room) --streams;
     for (int q = 0; q < streams; ++q) ring.row_bytes[q] = bytes[q];
     ring.slot_bytes = slot_of(streams);
-    for (per_sm = backward ? 2 : std::max(1, std::min(4, 1024 / (threads * rows))); per_sm > 1; --per_sm)
+    ring.padded = wide && p.cols < threads * packs * 8;
+    for (per_sm = packs == 1 ? 4 : 2; per_sm > 1; --per_sm)
       if ((room / per_sm - kRingHead - 2048 - beside) / ring.slot_bytes >= 2) break;
+    if (backward) per_sm = std::min(per_sm, 2);
     const int mine = per_sm == 1 ? room : room / per_sm - kRingHead - 2048;
     ring.slots = std::max(1, std::min(kMaxSlots, (mine - beside) / ring.slot_bytes));
     smem = kRingHead + std::max(ring.slots * ring.slot_bytes + beside, sums);

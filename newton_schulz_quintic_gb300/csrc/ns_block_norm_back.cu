@@ -7,15 +7,17 @@ namespace ns {
 namespace {
 using namespace block_norm;
 
-// Backward. The columns' sums are in registers, or for rows of more than 2 packs a thread in shared memory behind the
-// ring ([2][NP][8][threads of a row] floats for each row of the CTA, every thread its own).
+// The columns' sums are in registers, or for rows of more than 2 packs a thread in shared memory behind the ring and the
+// weights ([2][NP][8][threads of a row] floats for each row of the CTA, every thread its own).
+template <int NP> constexpr bool kInRegs = NP <= 2;
 template <int XT, int YT, bool WIDE, int NP>
 __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward_kernel(const __grid_constant__ NormParams p,
                                                                      const __grid_constant__ RingShape ring) {
   using X = typename Elem<XT>::T;
   using Y = typename Elem<YT>::T;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float reds[8][64];
+  __shared__ RowSums reds;
+  reds.clear();
   RingBarriers *bar = start_ring(ring, smem);
   uint8_t *slots = smem + kRingHead;
   const Waiter w{&bar->abort, p.status, p.wait_limit_ns};
@@ -29,31 +31,32 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
   if (fills) filler.first(ring, bar, slots, p.rows, w);
   const int group = threadIdx.x / ring.threads, thread = threadIdx.x - group * ring.threads;
   const int step = ring.threads;
-  uint8_t *behind = slots + ring.slots * ring.slot_bytes;  // weights or sums
-  float *acc = reinterpret_cast<float *>(kHold<NP> ? slots : behind) + group * (2 * NP * 8 * step) + thread;
+  uint8_t *behind = slots + ring.slots * ring.slot_bytes;  // the weights, then the sums
   const ColumnWeights<WIDE, NP> held{reinterpret_cast<float4 *>(behind) + thread, ring.threads};
+  float *acc = reinterpret_cast<float *>(kInRegs<NP> ? slots : behind + (p.hold ? 2 * NP * 8 * 4 * step : 0)) +
+               group * (2 * NP * 8 * step) + thread;
   int c[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i)
     c[i] = WIDE ? (i * ring.threads + thread) * 8 : (i * ring.threads + (thread & ~31)) * 8 + (thread & 31);
-  RowSum sum{reds[group], ring.threads, 1 + group, 0, thread};
+  RowSum sum{reds.red[group], ring.threads, 1 + group, 0, thread};
   const size_t xsize = static_cast<size_t>((p.rows - 1) * p.ld_dx + p.cols) * sizeof(X);
   const size_t ysize = static_cast<size_t>((p.rows - 1) * p.ld_dy + p.cols) * sizeof(Y);
   const float inv_n = 1.f / static_cast<float>(p.cols);
-  float2 sums[2][kHold<NP> ? NP : 1][4];
+  float2 sums[2][kInRegs<NP> ? NP : 1][4];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kHold<NP>)
+        if constexpr (kInRegs<NP>)
           sums[k][i][j] = both(0.f);
         else
           acc[((k * NP + i) * 8 + 2 * j) * step] = acc[((k * NP + i) * 8 + 2 * j + 1) * step] = 0.f;
       }
   auto add = [&](int k, int i, int j, float2 a, float2 b) {  // a * b
-    if constexpr (kHold<NP>) {
+    if constexpr (kInRegs<NP>) {
       sums[k][i][j] = __ffma2_rn(a, b, sums[k][i][j]);
     } else {
       float *to = acc + ((k * NP + i) * 8 + 2 * j) * step;
@@ -61,42 +64,51 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
       to[step] = fmaf(a.y, b.y, to[step]);
     }
   };
-  if (kHold<NP> && group == 0) held.keep(p, c);
+  if (p.hold && group == 0) held.keep(p, c);
   asm volatile("bar.sync 15, %0;" ::"r"(consumers) : "memory");
   RowReader reader;
   bool ok = true;
-  for (int64_t b = blockIdx.x; b * ring.height < p.rows; b += gridDim.x) {
-    const int64_t t = b * ring.height + group;
-    const bool here = t < p.rows;
-    Eight2 d[NP];  // the gradient of r; first dR, which is used after the first sum: read past the ring
+  const uint32_t rows = static_cast<uint32_t>(p.rows), stride = gridDim.x * ring.height;
+  uint32_t t = blockIdx.x * ring.height + group;
+  const StreamRow<XT, WIDE, 0> xs(ring, group);
+  const StreamRow<YT, WIDE, 1> ys(ring, group);
+  const StreamRow<YT, WIDE, 2> zs(ring, group);
+  const StreamRow<XT, WIDE, 3> drs(ring, group);
+  X *to = static_cast<X *>(p.dx) + t * p.ld_dx;
+  Y *yt = static_cast<Y *>(p.dy) + t * p.ld_dy;
+  int64_t ahead = blockIdx.x + static_cast<int64_t>(ring.slots) * gridDim.x;
+  const bool post = p.y && p.post;
+  float ry_next = t < rows && post ? p.post_rstd[t] : 1.f, rr_next = t < rows && p.pre ? p.pre_rstd[t] : 0.f;
+  for (uint32_t t0 = blockIdx.x * ring.height; t0 < rows; t0 += stride, t += stride, to += stride * p.ld_dx, yt += stride * p.ld_dy,
+                ahead += gridDim.x) {
+    const bool here = t < rows;
+    const float ry = ry_next, rr = rr_next;
+    {  // the next row's, and this row's dR where it is read past the ring
+      const uint32_t next = t + stride;
+      ry_next = next < rows && post ? p.post_rstd[next] : 1.f;
+      rr_next = next < rows && p.pre ? p.pre_rstd[next] : 0.f;
+      if (p.dr && here && !ring.row_bytes[3])
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if (p.dr && here)
-        load8<XT, WIDE>(at_row(p.dr, t, p.ld_dr, XT), c[i], p.cols, d[i]);
-      else
-        d[i].fill(0.f);
+        for (int i = 0; i < NP; ++i)
+          if (c[i] < p.cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(ring.src[3] + t * ring.ld_bytes[3] + c[i] * sizeof(X))));
     }
-    const float ry = here && p.y && p.post ? p.post_rstd[t] : 1.f, rr = here && p.pre ? p.pre_rstd[t] : 0.f;
     const float grow = here && p.gate_form == kGateRows ? one_of(p.gate, t * p.ld_gate, p.gate_type) : 1.f;
     const uint8_t *at = reader.wait(ring, bar, slots, w, ok);
     if (!here) {  // (never the first group)
       reader.release(ring, bar);
       continue;
     }
-    const uint8_t *rows[kStreams];
-    rows_of<WIDE>(ring, at, group, t, rows);
-    Eight2 y[NP];  // Y / rms
+    Eight2 y[NP], d[NP];  // Y / rms; R / rms, then the gradient of r
     if (p.pre) {
-      Eight2 rh[NP], g[NP];
       float2 s2 = both(0.f);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        load8<XT, WIDE>(rows[0], c[i], p.cols, rh[i]);
+        xs.load(ring, at, t, c[i], p.cols, d[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rh[i].v[j] = __fmul2_rn(rh[i].v[j], both(p.a));
+        for (int j = 0; j < 4; ++j) d[i].v[j] = __fmul2_rn(d[i].v[j], both(p.a));
         Eight2 f;
         if (p.y) {
-          load8<YT, WIDE>(rows[1], c[i], p.cols, y[i]);
+          ys.load(ring, at, t, c[i], p.cols, y[i]);
           weights_of<WIDE, NP>(p, held, 0, i, c[i], f);
           if (p.gate_form == kGateFull) {
             Eight2 full;
@@ -108,37 +120,47 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             y[i].v[j] = __fmul2_rn(y[i].v[j], both(ry));
-            rh[i].v[j] = __ffma2_rn(__fmul2_rn(y[i].v[j], both(k)), f.v[j], rh[i].v[j]);
+            d[i].v[j] = __ffma2_rn(__fmul2_rn(y[i].v[j], both(k)), f.v[j], d[i].v[j]);
           }
         }
-        load8<YT, WIDE>(rows[2], c[i], p.cols, g[i]);
+        Eight2 z;
+        zs.load(ring, at, t, c[i], p.cols, z);
         weights_of<WIDE, NP>(p, held, 1, i, c[i], f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          rh[i].v[j] = __fmul2_rn(rh[i].v[j], both(rr));
-          add(0, i, j, g[i].v[j], rh[i].v[j]);
-          g[i].v[j] = __fmul2_rn(g[i].v[j], f.v[j]);
-          s2 = __ffma2_rn(g[i].v[j], rh[i].v[j], s2);
+          d[i].v[j] = __fmul2_rn(d[i].v[j], both(rr));
+          add(0, i, j, z.v[j], d[i].v[j]);
+          s2 = __ffma2_rn(__fmul2_rn(z.v[j], f.v[j]), d[i].v[j], s2);
         }
       }
-      reader.release(ring, bar);
       const float m = -sum(s2.x + s2.y) * inv_n;
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i) {
+        // dZ again from the ring: registers for it would be spilled
+        Eight2 z, f, o;
+        zs.load(ring, at, t, c[i], p.cols, z);
+        weights_of<WIDE, NP>(p, held, 1, i, c[i], f);
+        if (p.dr)
+          drs.load(ring, at, t, c[i], p.cols, o);
+        else
+          o.fill(0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[i].v[j] = __ffma2_rn(both(rr), __ffma2_rn(rh[i].v[j], both(m), g[i].v[j]), d[i].v[j]);
+        for (int j = 0; j < 4; ++j)
+          d[i].v[j] = __ffma2_rn(both(rr), __ffma2_rn(d[i].v[j], both(m), __fmul2_rn(z.v[j], f.v[j])), o.v[j]);
+      }
+      reader.release(ring, bar);
     } else {
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i) {
+        drs.load(ring, at, t, c[i], p.cols, d[i]);
         if (p.y) {
-          load8<YT, WIDE>(rows[1], c[i], p.cols, y[i]);
+          ys.load(ring, at, t, c[i], p.cols, y[i]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[i].v[j] = __fmul2_rn(y[i].v[j], both(ry));
         }
+      }
       reader.release(ring, bar);
     }
-    if (fills) filler.fill(ring, bar, slots, p.rows, b + static_cast<int64_t>(ring.slots) * gridDim.x, w);
-    X *to = static_cast<X *>(p.dx) + t * p.ld_dx;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       Eight2 o;
@@ -146,7 +168,10 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
       for (int j = 0; j < 4; ++j) o.v[j] = __fmul2_rn(d[i].v[j], both(p.a));
       if (ok) store8<XT, WIDE>(to, c[i], p.cols, o, p.dx, xsize, p.status);
     }
-    if (!p.y) continue;
+    if (!p.y) {
+      if (fills) filler.fill(ring, bar, slots, p.rows, ahead, w);
+      continue;
+    }
     // through the gate: d * yh enters the sums (with a row's or a full gate's factor; the columns' comes at their end);
     // the gradient of y's norm is b gate post d
     float2 s2 = both(0.f);
@@ -179,6 +204,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
         d[i].v[j] = __fmul2_rn(d[i].v[j], __fmul2_rn(f.v[j], both(grow)));
       }
     }
+    if (fills) filler.fill(ring, bar, slots, p.rows, ahead, w);
     const float s = p.post || p.gate_form == kGateRows ? sum(s2.x + s2.y) : 0.f;
     if (p.gate_form == kGateRows && thread == 0 && ok) {
       if (p.gate_type == kBF16)
@@ -187,7 +213,6 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
         static_cast<float *>(p.dgate)[t * p.ld_dgate] = s;
     }
     const float m = p.post ? -s * grow * inv_n : 0.f;
-    Y *yt = static_cast<Y *>(p.dy) + t * p.ld_dy;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       Eight2 o;
@@ -197,7 +222,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
     }
   }
   if (fills) filler.end(ring, bar, w);
-  if constexpr (kHold<NP>) {
+  if constexpr (kInRegs<NP>) {
     // the ring is done with once every thread is here: it takes the sums
     asm volatile("bar.sync 15, %0;" ::"r"(consumers) : "memory");
 #pragma unroll
@@ -340,7 +365,8 @@ extern "C" int ns_block_norm_backward(const void *dresidual, int64_t ld_dr, cons
   const bool wide = packs_fit(p, dtype, block_dtype) && rows_aligned(dresidual, ld_dr, xe, 8) && rows_aligned(dnormed, ld_dz, ye, 8) &&
                     rows_aligned(dx, ld_dx, xe, 8) && rows_aligned(dy, ld_dy, ye, 8) &&
                     (gate_form != kGateFull || rows_aligned(dgate, ld_dgate, ge, 8));
-  const Shape sh(p, true, wide, dtype, block_dtype);
+  const Shape sh(p, true, wide, dtype, block_dtype, call.sms);
+  p.hold = sh.hold;
   const int grid = static_cast<int>(std::min<int64_t>({sh.batches(rows), static_cast<int64_t>(call.sms) * sh.per_sm, kMaxParts}));
   const JoinParams j{p.parts, grid, p.cols, gate_form, gate_dtype, weight_dtype, gate, post, dgate, post ? dpost : nullptr,
                      pre ? dpre : nullptr, b, call.status};

@@ -21,9 +21,10 @@ namespace ns {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxExperts = 1024, kMaxTopK = 32;
-constexpr int kMaxStretches = 304;  // CTAs of a call: what the scratch holds
+// CTAs of a call: what the scratch holds. Every CTA of the second launch reads the parts of all, so no more than fill the SMs.
+constexpr int kMaxStretches = 152;
 
 struct RouteParams {
   const void *logits;
@@ -53,16 +54,51 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   return v == 0.f ? 0x80000000u : k;  // both zeros are equal
 }
 
-// Rows by warps, V logits a lane: expert e of the row is value e / 32 of lane e % 32.
-template <int DT, int V>
-__global__ void __launch_bounds__(kThreads) ns_route_rows_kernel(const __grid_constant__ RouteParams p) {
+// L lanes a row, V logits a lane: expert e of the row is value e / L of lane e % L; 32 / L rows a warp. A group's largest
+// key is found by shuffles among its lanes.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int L>
+__device__ __forceinline__ int group_min(int v) {
+  if constexpr (L == 32) {
+    return __reduce_min_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The float of a key (zero for either zero).
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return key == 0xffffffffu ? __int_as_float(0x7fc00000) : __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+template <int L, int V> constexpr int kRowWarps = L * V <= 512 ? kWarps : kWarps / 2;  // their sums fill 32 KB
+template <int DT, int L, int V>
+__global__ void __launch_bounds__(32 * kRowWarps<L, V>) ns_route_rows_kernel(const __grid_constant__ RouteParams p) {
   using E = typename Elem<DT>::T;
-  __shared__ int32_t hist[V * 32];
-  __shared__ float sums[kWarps][V * 32];
-  __shared__ float zs[kWarps];
-  __shared__ int lives[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < V * 32; e += kThreads) hist[e] = 0;
+  constexpr int kRows = 32 / L, kW = kRowWarps<L, V>;  // rows of a warp at a time, warps
+  __shared__ int32_t hist[V * L];
+  __shared__ float sums[kW][V * L];
+  __shared__ float zs[kW];
+  __shared__ int lives[kW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, sub = lane / L;
+  asm volatile("griddepcontrol.launch_dependents;");  // the slots' launch may set itself up
+  for (int e = threadIdx.x; e < V * L; e += kW * 32) hist[e] = 0;
   __syncthreads();
   const int first = min(p.rows, static_cast<int>(blockIdx.x) * p.stretch), end = min(p.rows, first + p.stretch);
   float prob[V];
@@ -71,93 +107,118 @@ __global__ void __launch_bounds__(kThreads) ns_route_rows_kernel(const __grid_co
   float zsum = 0.f;
   int nlive = 0;
   const size_t slots = static_cast<size_t>(p.rows) * p.top_k;
-  for (int t = first + warp; t < end; t += kWarps) {
+  for (int t0 = first + warp * kRows; t0 < end; t0 += kW * kRows) {
+    const int t = t0 + sub;
     const E *x = static_cast<const E *>(p.logits) + static_cast<int64_t>(t) * p.ld;
-    bool live = !p.live || p.live[t] != 0;
-    float v[V];
+    bool live = t < end && (!p.live || p.live[t] != 0);
     uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * L + l;
+      key[i] = live && e < p.experts ? key_of(Elem<DT>::to_f(x[e])) : 0u;
+    }
+    // the k largest, one after the other: the lane that holds it takes it out of its own
+    uint32_t left[V];
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
-      v[i] = live && e < p.experts ? Elem<DT>::to_f(x[e]) : -INFINITY;
-      key[i] = key_of(v[i]);
+      left[i] = key[i];
       best = max(best, key[i]);
     }
-    int mine = -1;      // lane j: the j-th choice
-    float top = 0.f, chosen = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-      if (m == 0) break;  // nothing left that may be chosen
-      int at = INT32_MAX;
-      if (best == m) {
+    uint32_t chosen[kMaxTopK / L > 0 ? kMaxTopK / L : 1];  // lane j % L: the j-th choice
+    int mine[kMaxTopK / L > 0 ? kMaxTopK / L : 1];
+    constexpr int kHeld = kMaxTopK / L > 0 ? kMaxTopK / L : 1;
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-          if (key[i] == m) at = i * 32 + lane;
-      }
-      const int e = __reduce_min_sync(0xffffffffu, at);
-      float value = 0.f;
-      if (at == e) {  // its lane takes it out
+    for (int h = 0; h < kHeld; ++h) {
+      chosen[h] = 0;
+      mine[h] = -1;
+    }
+    uint32_t top = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+      const uint32_t m = group_max<L>(best);
+      if (j == 0) top = m;
+      if (!__any_sync(0xffffffffu, m != 0)) break;  // nothing left that may be chosen
+      int at = INT32_MAX;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) at = left[i] == m ? i * L + l : at;
+      const int e = group_min<L>(m != 0 ? at : INT32_MAX);
+      if (m != 0 && at == e) {
         best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (i == e / 32) {
-            value = v[i];
-            key[i] = 0;
-          }
-          best = max(best, key[i]);
+          left[i] = i * L + l == e ? 0u : left[i];
+          best = max(best, left[i]);
         }
       }
-      value = __shfl_sync(0xffffffffu, value, e & 31);
-      if (j == 0) top = value;
-      if (lane == j) {
-        mine = e;
-        chosen = value;
-      }
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+        if (m != 0 && l == j - h * L) {
+          mine[h] = e;
+          chosen[h] = m;
+        }
     }
-    live = __shfl_sync(0xffffffffu, mine, 0) >= 0;
+    live = top != 0;
+    const float most = live ? value_of(top) : 0.f;
     float total = 0.f, q[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      q[i] = live ? expf(v[i] - top) : 0.f;
+      q[i] = key[i] != 0 ? expf(value_of(key[i]) - most) : 0.f;
       total += q[i];
     }
-    total = warp_sum(total);
+    total = group_sum<L>(total);
     const float inv = live ? 1.f / total : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) prob[i] += q[i] * inv;
-    const float lz = live ? top + logf(total) : 0.f;
+    const float lz = live ? most + logf(total) : 0.f;
     zsum += lz * lz;
     nlive += live ? 1 : 0;
-    float w = mine >= 0 ? expf(chosen - top) : 0.f;
-    const float sum = p.renormalise ? warp_sum(w) : total;
-    w = live ? w / sum : 0.f;
-    if (lane < p.top_k) {
-      const int64_t at = static_cast<int64_t>(t) * p.top_k + lane;
-      if (in_bounds(p.ids + at, 4, p.ids, slots * 4, p.status)) p.ids[at] = mine;
-      if (in_bounds(p.weights + at, 4, p.weights, slots * 4, p.status)) p.weights[at] = w;
-      if (mine >= 0) atomicAdd(&hist[mine], 1);
-    }
-    if (lane == 0 && in_bounds(p.logz + t, 4, p.logz, static_cast<size_t>(p.rows) * 4, p.status)) p.logz[t] = lz;
-  }
+    float w[kHeld], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sums[warp][i * 32 + lane] = prob[i];
+    for (int h = 0; h < kHeld; ++h) {
+      w[h] = mine[h] >= 0 ? expf(value_of(chosen[h]) - most) : 0.f;
+      sum += w[h];
+    }
+    sum = group_sum<L>(sum);
+    if (!p.renormalise) sum = total;
+    if (t < end) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+        if (h * L + l < p.top_k) {
+          const int64_t at = static_cast<int64_t>(t) * p.top_k + h * L + l;
+          if (in_bounds(p.ids + at, 4, p.ids, slots * 4, p.status)) p.ids[at] = mine[h];
+          if (in_bounds(p.weights + at, 4, p.weights, slots * 4, p.status)) p.weights[at] = live ? w[h] / sum : 0.f;
+          if (mine[h] >= 0) atomicAdd(&hist[mine[h]], 1);
+        }
+      if (l == 0 && in_bounds(p.logz + t, 4, p.logz, static_cast<size_t>(p.rows) * 4, p.status)) p.logz[t] = lz;
+    }
+  }
+  // the warp's groups of lanes are added in order
+#pragma unroll
+  for (int o = L; o < 32; o <<= 1) {
+    zsum += __shfl_down_sync(0xffffffffu, zsum, o);
+    nlive += __shfl_down_sync(0xffffffffu, nlive, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i) prob[i] += __shfl_down_sync(0xffffffffu, prob[i], o);
+  }
+  if (lane < L)
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[warp][i * L + l] = prob[i];
   if (lane == 0) {
     zs[warp] = zsum;
     lives[warp] = nlive;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) {
+  for (int e = threadIdx.x; e < p.experts; e += kW * 32) {
     float s = sums[0][e];
 #pragma unroll
-    for (int k = 1; k < kWarps; ++k) s += sums[k][e];
+    for (int k = 1; k < kW; ++k) s += sums[k][e];
     p.part_prob[static_cast<int64_t>(blockIdx.x) * p.experts + e] = s;
     p.part_count[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
   }
   if (threadIdx.x == 0) {
     float z = 0.f;
     int n = 0;
-    for (int k = 0; k < kWarps; ++k) {
+    for (int k = 0; k < kW; ++k) {
       z += zs[k];
       n += lives[k];
     }
@@ -178,21 +239,23 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 
 // Slots of the CTA's stretch in the experts' order, and the totals.
 __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_constant__ RouteParams p) {
-  __shared__ int32_t next[kWarps][kMaxExperts];  // per warp and expert: place of its next slot
+  extern __shared__ int32_t nexts[];  // per warp and expert: place of its next slot
   __shared__ int32_t scan[kWarps];
   __shared__ float red[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int stretches = gridDim.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int first = min(p.rows, static_cast<int>(blockIdx.x) * p.stretch), end = min(p.rows, first + p.stretch);
   const int slot0 = first * p.top_k, nslots = (end - first) * p.top_k;
   const int share = ((nslots + kWarps - 1) / kWarps + 31) / 32 * 32;  // of a warp
   const int a = min(nslots, warp * share), b = min(nslots, a + share);
-  for (int e = threadIdx.x; e < kWarps * p.experts; e += kThreads) next[e / p.experts][e % p.experts] = 0;
+  for (int e = threadIdx.x; e < kWarps * p.experts; e += kThreads) nexts[e] = 0;
+  int32_t *mine = nexts + warp * p.experts;
   __syncthreads();
   // this stretch's slots per warp and expert
   for (int i = a + lane; i < b; i += 32) {
     const int e = p.ids[slot0 + i];
-    if (e >= 0) atomicAdd(&next[warp][e], 1);
+    if (e >= 0) atomicAdd(mine + e, 1);
   }
   __syncthreads();
   // Experts in turn by threads, kThreads at a time: all slots of the experts before, of the stretches before, of the warps before.
@@ -203,14 +266,14 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     int before = 0, all = 0;
     float prob = 0.f;
     if (e < p.experts) {
-#pragma unroll 8
+#pragma unroll 32
       for (int c = 0; c < stretches; ++c) {
         const int n = __ldg(p.part_count + static_cast<int64_t>(c) * p.experts + e);
         all += n;
         before += c < static_cast<int>(blockIdx.x) ? n : 0;
       }
       if (blockIdx.x == 0) {
-#pragma unroll 8
+#pragma unroll 32
         for (int c = 0; c < stretches; ++c) prob += p.part_prob[static_cast<int64_t>(c) * p.experts + e];
       }
     }
@@ -233,8 +296,8 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     if (e < p.experts) {
       int at = offset + before;
       for (int k = 0; k < kWarps; ++k) {
-        const int n = next[k][e];
-        next[k][e] = at;
+        const int n = nexts[k * p.experts + e];
+        nexts[k * p.experts + e] = at;
         at += n;
       }
       if (blockIdx.x == 0) {
@@ -252,9 +315,9 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     const uint32_t before = same & ((1u << lane) - 1u);
     int at = 0;
-    if (e >= 0) at = next[warp][e] + __popc(before);
+    if (e >= 0) at = mine[e] + __popc(before);
     __syncwarp();
-    if (e >= 0 && before == 0) next[warp][e] += __popc(same);
+    if (e >= 0 && before == 0) mine[e] += __popc(same);
     __syncwarp();
     if (e >= 0 && in_bounds(p.order + at, 4, p.order, size, p.status)) p.order[at] = slot0 + i;
   }
@@ -299,23 +362,24 @@ struct RouteBackParams {
   int *status;
 };
 
+constexpr int kBackWarps = 8;
 // dL = P (s - sum of P s + 2 z logz / T) with s = balance E counts / (k T^2), and the weights' own part.
 template <int DT, int V>
-__global__ void __launch_bounds__(kThreads) ns_route_backward_kernel(const __grid_constant__ RouteBackParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_kernel(const __grid_constant__ RouteBackParams p) {
   using E = typename Elem<DT>::T;
   __shared__ float slope[V * 32];
-  __shared__ float part[kWarps][V * 32];  // a row's weights' part by expert; zero between rows
+  __shared__ float part[kBackWarps][V * 32];  // a row's weights' part by expert; zero between rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float t = static_cast<float>(max(__ldg(p.live_rows), 1));
   const float factor = p.balance * static_cast<float>(p.experts) / static_cast<float>(p.top_k) / t / t;
-  for (int e = threadIdx.x; e < V * 32; e += kThreads) {
+  for (int e = threadIdx.x; e < V * 32; e += kBackWarps * 32) {
     slope[e] = e < p.experts ? factor * static_cast<float>(p.counts[e]) : 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) part[k][e] = 0.f;
+    for (int k = 0; k < kBackWarps; ++k) part[k][e] = 0.f;
   }
   __syncthreads();
   const size_t size = static_cast<size_t>((p.rows - 1) * p.ld_d + p.experts) * sizeof(E);
-  for (int r = blockIdx.x * kWarps + warp; r < p.rows; r += gridDim.x * kWarps) {
+  for (int r = blockIdx.x * kBackWarps + warp; r < p.rows; r += gridDim.x * kBackWarps) {
     const E *x = static_cast<const E *>(p.logits) + static_cast<int64_t>(r) * p.ld;
     E *out = static_cast<E *>(p.dlogits) + static_cast<int64_t>(r) * p.ld_d;
     int e = -1;
@@ -364,6 +428,20 @@ __global__ void __launch_bounds__(kThreads) ns_route_backward_kernel(const __gri
   }
 }
 
+// Lanes of a row and logits a lane of the first launch: rows of up to 256 experts share a warp, 16 logits a lane, so that a
+// step of the choice serves several rows.
+template <typename F>
+int by_lanes(int experts, F &&f) {
+  using std::integral_constant;
+  return experts <= 16    ? f(integral_constant<int, 4>{}, integral_constant<int, 4>{})
+         : experts <= 32  ? f(integral_constant<int, 4>{}, integral_constant<int, 8>{})
+         : experts <= 64  ? f(integral_constant<int, 8>{}, integral_constant<int, 8>{})
+         : experts <= 128 ? f(integral_constant<int, 8>{}, integral_constant<int, 16>{})
+         : experts <= 256 ? f(integral_constant<int, 16>{}, integral_constant<int, 16>{})
+         : experts <= 512 ? f(integral_constant<int, 32>{}, integral_constant<int, 16>{})
+                          : f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
+}
+
 template <typename F>
 int by_width(int experts, F &&f) {
   return experts <= 32 ? f(std::integral_constant<int, 1>{}) : experts <= 64 ? f(std::integral_constant<int, 2>{})
@@ -377,7 +455,7 @@ bool bad_sizes(int64_t rows, int experts, int top_k, int64_t ld, float balance, 
          top_k > experts || rows > (1 << 30) / top_k || !std::isfinite(balance) || !std::isfinite(z);
 }
 size_t scratch_of(int64_t rows, int experts) {
-  const int64_t n = std::min<int64_t>((rows + kWarps - 1) / kWarps, kMaxStretches);
+  const int64_t n = std::min<int64_t>((rows + 15) / 16, kMaxStretches);
   return static_cast<size_t>(std::max<int64_t>(n, 1)) * (8 * static_cast<size_t>(experts) + 8);
 }
 
@@ -436,22 +514,37 @@ extern "C" int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int
   p.balance = balance_coef;
   p.z = z_coef;
   p.status = call.status;
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(rows + kWarps - 1) / kWarps, 2 * call.sms, kMaxStretches})));
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(rows + 15) / 16, call.sms, kMaxStretches})));
   p.stretch = static_cast<int>((rows + grid - 1) / grid);
   p.part_count = static_cast<int32_t *>(workspace);
   p.part_prob = reinterpret_cast<float *>(p.part_count + static_cast<int64_t>(grid) * experts);
   p.part_z = p.part_prob + static_cast<int64_t>(grid) * experts;
   p.part_live = reinterpret_cast<int32_t *>(p.part_z + grid);
   return call.launch(kOpRoute, [&] {
-    by_width(experts, [&](auto v) {
+    by_lanes(experts, [&](auto l, auto v) {
       if (dtype == NS_BF16)
-        ns_route_rows_kernel<kBF16, decltype(v)::value><<<grid, kThreads, 0, call.s>>>(p);
+        ns_route_rows_kernel<kBF16, decltype(l)::value, decltype(v)::value><<<grid, 32 * kRowWarps<decltype(l)::value, decltype(v)::value>, 0, call.s>>>(p);
       else
-        ns_route_rows_kernel<kF32, decltype(v)::value><<<grid, kThreads, 0, call.s>>>(p);
+        ns_route_rows_kernel<kF32, decltype(l)::value, decltype(v)::value><<<grid, 32 * kRowWarps<decltype(l)::value, decltype(v)::value>, 0, call.s>>>(p);
       return 0;
     });
     count_launch();
-    ns_route_order_kernel<<<grid, kThreads, 0, call.s>>>(p);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = call.s;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kWarps) * experts * 4;
+    static SmemOptIn opt_in;
+    if (opt_in.ensure(reinterpret_cast<const void *>(ns_route_order_kernel), static_cast<int>(cfg.dynamicSmemBytes))) return -1;
+    if (cudaLaunchKernelEx(&cfg, ns_route_order_kernel, p) != cudaSuccess) {
+      cudaGetLastError();
+      return -1;
+    }
     count_launch();
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   });
@@ -480,13 +573,13 @@ extern "C" int ns_route_backward(const void *logits, int64_t ld_logits, int64_t 
   if (call.rc) return call.rc;
   RouteBackParams p{logits, ld_logits, static_cast<int>(rows), experts, top_k, renormalise, ids, weights, dweights, logz,
                     counts, live_rows, balance_coef, z_coef, dlogits, ld_dlogits, call.status};
-  const int grid = static_cast<int>(std::min<int64_t>((rows + kWarps - 1) / kWarps, static_cast<int64_t>(call.sms) * 8));
+  const int grid = static_cast<int>(std::min<int64_t>((rows + kBackWarps - 1) / kBackWarps, static_cast<int64_t>(call.sms) * 8));
   return call.launch(kOpRoute, [&] {
     by_width(experts, [&](auto v) {
       if (dtype == NS_BF16)
-        ns_route_backward_kernel<kBF16, decltype(v)::value><<<grid, kThreads, 0, call.s>>>(p);
+        ns_route_backward_kernel<kBF16, decltype(v)::value><<<grid, 32 * kBackWarps, 0, call.s>>>(p);
       else
-        ns_route_backward_kernel<kF32, decltype(v)::value><<<grid, kThreads, 0, call.s>>>(p);
+        ns_route_backward_kernel<kF32, decltype(v)::value><<<grid, 32 * kBackWarps, 0, call.s>>>(p);
       return 0;
     });
     count_launch();

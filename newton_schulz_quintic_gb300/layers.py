@@ -60,7 +60,8 @@ class Routing(NamedTuple):
     live_rows: torch.Tensor  # scalar, int32: rows that are not padding
 
 
-_MAX_STRETCHES = 304
+_MAX_STRETCHES = 152   # of a route call
+_MAX_PARTS = 304       # of a block_norm_backward call
 
 
 def route(logits, top_k: int, live=None, renormalise: bool = True, balance_coef: float = 0.0, z_coef: float = 0.0,
@@ -83,7 +84,7 @@ def route(logits, top_k: int, live=None, renormalise: bool = True, balance_coef:
     # everything in one allocation: ids, order, counts, offsets, live rows | weights, logz, loss | scratch
     at_f = 2 * slots + 2 * experts + 2
     at_work = at_f + slots + n + 1
-    scratch = max(1, min(-(-n // 8), _MAX_STRETCHES)) * (2 * experts + 2)
+    scratch = max(1, min(-(-n // 16), _MAX_STRETCHES)) * (2 * experts + 2)
     with _on(dev, stream):
         floats = _empty(at_work + scratch, dtype=_F32, device=dev)
         p = floats.data_ptr()
@@ -403,7 +404,7 @@ def block_norm_backward(dresidual, dnormed, x, y, saved: BlockNorm, gate=None, p
     if dy is not None and y is None:
         raise ValueError("dy given, but no y")
     ld_dy = cols if dy is None else _matrix(dy, "dy", n, cols, bt)
-    scratch = max(1, min(n, _MAX_STRETCHES)) * 2 * cols
+    scratch = max(1, min(n, _MAX_PARTS)) * 2 * cols
     with _on(dev, stream):
         if dx is None:
             dx = _empty((n, cols), dtype=x.dtype, device=dev)
