@@ -54,51 +54,73 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   return v == 0.f ? 0x80000000u : k;  // both zeros are equal
 }
 
-// L lanes a row, V logits a lane: expert e of the row is value e / L of lane e % L; 32 / L rows a warp. A group's largest
-// key is found by shuffles among its lanes.
-template <int L>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  if constexpr (L == 32) {
-    return __reduce_max_sync(0xffffffffu, v);
-  } else {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+// A lane's logits still to be chosen from: expert e of the row is value e / 32 of lane e % 32. take() gives the warp's
+// largest, lowest index first among equals, and takes it out; -1 when nothing is left.
+template <int DT, int V>
+struct Choice;
+// fp32: the largest key, then the lowest index that has it.
+template <int V>
+struct Choice<kF32, V> {
+  uint32_t left[V], best = 0;
+  __device__ __forceinline__ void set(int i, int, float v) {
+    left[i] = key_of(v);
+    best = max(best, left[i]);
   }
-}
-template <int L>
-__device__ __forceinline__ int group_min(int v) {
-  if constexpr (L == 32) {
-    return __reduce_min_sync(0xffffffffu, v);
-  } else {
+  __device__ __forceinline__ int take() {
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    if (m == 0) return -1;
+    int at = INT32_MAX;
+    if (best == m) {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+      for (int i = V - 1; i >= 0; --i) at = left[i] == m ? i * 32 + lane : at;
+    }
+    const int e = __reduce_min_sync(0xffffffffu, at);
+    if (at == e) {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        left[i] = e == i * 32 + lane ? 0u : left[i];
+        best = max(best, left[i]);
+      }
+    }
+    return e;
   }
-}
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
+};
+// bf16: key and index fit one word, so all are different: one maximum gives both, and what is left is what is smaller.
+template <int V>
+struct Choice<kBF16, V> {
+  uint32_t left[V], best = 0;
+  __device__ __forceinline__ void set(int i, int e, float v) {
+    const uint32_t k = key_of(v) & 0xffff0000u;  // the low half of a positive number's is 0, of a negative one's ones
+    left[i] = k ? k | (0xffffu - static_cast<uint32_t>(e)) : 0u;
+    best = max(best, left[i]);
+  }
+  __device__ __forceinline__ int take() {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    if (m == 0) return -1;
+    if (best == m) {
+      best = 0;
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-// The float of a key (zero for either zero).
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return key == 0xffffffffu ? __int_as_float(0x7fc00000) : __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
+      for (int i = 0; i < V; ++i) best = max(best, left[i] < m ? left[i] : 0u);
+    }
+    return static_cast<int>(0xffffu - (m & 0xffffu));
+  }
+};
 
-template <int L, int V> constexpr int kRowWarps = L * V <= 512 ? kWarps : kWarps / 2;  // their sums fill 32 KB
-template <int DT, int L, int V>
-__global__ void __launch_bounds__(32 * kRowWarps<L, V>) ns_route_rows_kernel(const __grid_constant__ RouteParams p) {
+// Rows by warps, V logits a lane.
+template <int V> constexpr int kRowWarps = V <= 16 ? kWarps : kWarps / 2;  // their sums fill 32 KB
+template <int DT, int V>
+__global__ void __launch_bounds__(32 * kRowWarps<V>) ns_route_rows_kernel(const __grid_constant__ RouteParams p) {
   using E = typename Elem<DT>::T;
-  constexpr int kRows = 32 / L, kW = kRowWarps<L, V>;  // rows of a warp at a time, warps
-  __shared__ int32_t hist[V * L];
-  __shared__ float sums[kW][V * L];
+  constexpr int kW = kRowWarps<V>;
+  __shared__ int32_t hist[V * 32];
+  __shared__ float sums[kW][V * 32];
   __shared__ float zs[kW];
   __shared__ int lives[kW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, sub = lane / L;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;");  // the slots' launch may set itself up
-  for (int e = threadIdx.x; e < V * L; e += kW * 32) hist[e] = 0;
+  for (int e = threadIdx.x; e < V * 32; e += kW * 32) hist[e] = 0;
   __syncthreads();
   const int first = min(p.rows, static_cast<int>(blockIdx.x) * p.stretch), end = min(p.rows, first + p.stretch);
   float prob[V];
@@ -107,102 +129,72 @@ __global__ void __launch_bounds__(32 * kRowWarps<L, V>) ns_route_rows_kernel(con
   float zsum = 0.f;
   int nlive = 0;
   const size_t slots = static_cast<size_t>(p.rows) * p.top_k;
-  for (int t0 = first + warp * kRows; t0 < end; t0 += kW * kRows) {
-    const int t = t0 + sub;
-    const E *x = static_cast<const E *>(p.logits) + static_cast<int64_t>(t) * p.ld;
-    bool live = t < end && (!p.live || p.live[t] != 0);
-    uint32_t key[V];
+  // the next row's logits are read while this one's are chosen from
+  E next[V];
+  bool next_live = false;
+  auto read = [&](int t) {
+    next_live = t < end && (!p.live || p.live[t] != 0);
+    const E *x = static_cast<const E *>(p.logits) + static_cast<int64_t>(t) * p.ld + lane;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (next_live && i * 32 + lane < p.experts) next[i] = x[i * 32];
+  };
+  read(first + warp);
+  for (int t = first + warp; t < end; t += kW) {
+    float v[V];
+    Choice<DT, V> choice;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * L + l;
-      key[i] = live && e < p.experts ? key_of(Elem<DT>::to_f(x[e])) : 0u;
+      v[i] = next_live && i * 32 + lane < p.experts ? Elem<DT>::to_f(next[i]) : -INFINITY;
+      choice.set(i, i * 32 + lane, v[i]);
     }
-    // the k largest, one after the other: the lane that holds it takes it out of its own
-    uint32_t left[V];
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      left[i] = key[i];
-      best = max(best, key[i]);
-    }
-    uint32_t chosen[kMaxTopK / L > 0 ? kMaxTopK / L : 1];  // lane j % L: the j-th choice
-    int mine[kMaxTopK / L > 0 ? kMaxTopK / L : 1];
-    constexpr int kHeld = kMaxTopK / L > 0 ? kMaxTopK / L : 1;
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-      chosen[h] = 0;
-      mine[h] = -1;
-    }
-    uint32_t top = 0;
+    read(t + kW);
+    int mine = -1;  // lane j: the j-th choice
     for (int j = 0; j < p.top_k; ++j) {
-      const uint32_t m = group_max<L>(best);
-      if (j == 0) top = m;
-      if (!__any_sync(0xffffffffu, m != 0)) break;  // nothing left that may be chosen
-      int at = INT32_MAX;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) at = left[i] == m ? i * L + l : at;
-      const int e = group_min<L>(m != 0 ? at : INT32_MAX);
-      if (m != 0 && at == e) {
-        best = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          left[i] = i * L + l == e ? 0u : left[i];
-          best = max(best, left[i]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h)
-        if (m != 0 && l == j - h * L) {
-          mine[h] = e;
-          chosen[h] = m;
-        }
+      const int e = choice.take();
+      if (e < 0) break;
+      if (lane == j) mine = e;
     }
-    live = top != 0;
-    const float most = live ? value_of(top) : 0.f;
+    const int e0 = __shfl_sync(0xffffffffu, mine, 0);
+    const bool live = e0 >= 0;
+    // a chosen one's logit, from where the lane that has it keeps the row
+    auto logit_of = [&](int e) {
+      float r = 0.f;
+      const int from = e >= 0 ? e & 31 : 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float f = __shfl_sync(0xffffffffu, v[i], from);
+        r = e / 32 == i ? f : r;
+      }
+      return r;
+    };
+    const float chosen = logit_of(mine), top = __shfl_sync(0xffffffffu, chosen, 0);
     float total = 0.f, q[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      q[i] = key[i] != 0 ? expf(value_of(key[i]) - most) : 0.f;
+      q[i] = live ? expf(v[i] - top) : 0.f;
       total += q[i];
     }
-    total = group_sum<L>(total);
+    total = warp_sum(total);
     const float inv = live ? 1.f / total : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) prob[i] += q[i] * inv;
-    const float lz = live ? most + logf(total) : 0.f;
+    const float lz = live ? top + logf(total) : 0.f;
     zsum += lz * lz;
     nlive += live ? 1 : 0;
-    float w[kHeld], sum = 0.f;
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-      w[h] = mine[h] >= 0 ? expf(value_of(chosen[h]) - most) : 0.f;
-      sum += w[h];
+    float w = mine >= 0 ? expf(chosen - top) : 0.f;
+    const float sum = p.renormalise ? warp_sum(w) : total;
+    w = live ? w / sum : 0.f;
+    if (lane < p.top_k) {
+      const int64_t at = static_cast<int64_t>(t) * p.top_k + lane;
+      if (in_bounds(p.ids + at, 4, p.ids, slots * 4, p.status)) p.ids[at] = mine;
+      if (in_bounds(p.weights + at, 4, p.weights, slots * 4, p.status)) p.weights[at] = w;
+      if (mine >= 0) atomicAdd(&hist[mine], 1);
     }
-    sum = group_sum<L>(sum);
-    if (!p.renormalise) sum = total;
-    if (t < end) {
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h)
-        if (h * L + l < p.top_k) {
-          const int64_t at = static_cast<int64_t>(t) * p.top_k + h * L + l;
-          if (in_bounds(p.ids + at, 4, p.ids, slots * 4, p.status)) p.ids[at] = mine[h];
-          if (in_bounds(p.weights + at, 4, p.weights, slots * 4, p.status)) p.weights[at] = live ? w[h] / sum : 0.f;
-          if (mine[h] >= 0) atomicAdd(&hist[mine[h]], 1);
-        }
-      if (l == 0 && in_bounds(p.logz + t, 4, p.logz, static_cast<size_t>(p.rows) * 4, p.status)) p.logz[t] = lz;
-    }
+    if (lane == 0 && in_bounds(p.logz + t, 4, p.logz, static_cast<size_t>(p.rows) * 4, p.status)) p.logz[t] = lz;
   }
-  // the warp's groups of lanes are added in order
 #pragma unroll
-  for (int o = L; o < 32; o <<= 1) {
-    zsum += __shfl_down_sync(0xffffffffu, zsum, o);
-    nlive += __shfl_down_sync(0xffffffffu, nlive, o);
-#pragma unroll
-    for (int i = 0; i < V; ++i) prob[i] += __shfl_down_sync(0xffffffffu, prob[i], o);
-  }
-  if (lane < L)
-#pragma unroll
-    for (int i = 0; i < V; ++i) sums[warp][i * L + l] = prob[i];
+  for (int i = 0; i < V; ++i) sums[warp][i * 32 + lane] = prob[i];
   if (lane == 0) {
     zs[warp] = zsum;
     lives[warp] = nlive;
@@ -258,25 +250,53 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     if (e >= 0) atomicAdd(mine + e, 1);
   }
   __syncthreads();
-  // Experts in turn by threads, kThreads at a time: all slots of the experts before, of the stretches before, of the warps before.
+  // Counts of all stretches and of those before this one: warps take 32 experts and a share of the stretches, many reads
+  // in flight (one thread for an expert's stretches was 40 us).
+  __shared__ int32_t part_all[kMaxExperts], part_before[kMaxExperts];
+  __shared__ float part_prob[kMaxExperts];
+  const int groups = (p.experts + 31) / 32, shares = max(1, kWarps / groups);
+  for (int item = warp; item < groups * shares; item += kWarps) {
+    const int e = item % groups * 32 + lane, part = item / groups;
+    const int c0 = stretches * part / shares, c1 = stretches * (part + 1) / shares;
+    int all = 0, before = 0;
+    float prob = 0.f;
+    if (e < p.experts) {
+      constexpr int kDeep = 16;
+      for (int c = c0; c < c1; c += kDeep) {
+        int n[kDeep];
+        float f[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+          const int64_t at = static_cast<int64_t>(c + k) * p.experts + e;
+          n[k] = c + k < c1 ? p.part_count[at] : 0;
+          f[k] = blockIdx.x == 0 && c + k < c1 ? p.part_prob[at] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+          all += n[k];
+          before += c + k < static_cast<int>(blockIdx.x) ? n[k] : 0;
+          prob += f[k];
+        }
+      }
+      part_all[part * p.experts + e] = all;
+      part_before[part * p.experts + e] = before;
+      part_prob[part * p.experts + e] = prob;
+    }
+  }
+  __syncthreads();
+  // experts in turn by threads, kThreads at a time: the slots of all experts before, of the stretches before, of the warps before
   int run = 0;
   float loss = 0.f;
   for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
     const int e = e0 + threadIdx.x;
     int before = 0, all = 0;
     float prob = 0.f;
-    if (e < p.experts) {
-#pragma unroll 32
-      for (int c = 0; c < stretches; ++c) {
-        const int n = __ldg(p.part_count + static_cast<int64_t>(c) * p.experts + e);
-        all += n;
-        before += c < static_cast<int>(blockIdx.x) ? n : 0;
+    if (e < p.experts)
+      for (int k = 0; k < shares; ++k) {
+        all += part_all[k * p.experts + e];
+        before += part_before[k * p.experts + e];
+        prob += part_prob[k * p.experts + e];
       }
-      if (blockIdx.x == 0) {
-#pragma unroll 32
-        for (int c = 0; c < stretches; ++c) prob += p.part_prob[static_cast<int64_t>(c) * p.experts + e];
-      }
-    }
     // exclusive prefix over the threads
     int incl = all;
 #pragma unroll
@@ -428,20 +448,6 @@ __global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_kernel(cons
   }
 }
 
-// Lanes of a row and logits a lane of the first launch: rows of up to 256 experts share a warp, 16 logits a lane, so that a
-// step of the choice serves several rows.
-template <typename F>
-int by_lanes(int experts, F &&f) {
-  using std::integral_constant;
-  return experts <= 16    ? f(integral_constant<int, 4>{}, integral_constant<int, 4>{})
-         : experts <= 32  ? f(integral_constant<int, 4>{}, integral_constant<int, 8>{})
-         : experts <= 64  ? f(integral_constant<int, 8>{}, integral_constant<int, 8>{})
-         : experts <= 128 ? f(integral_constant<int, 8>{}, integral_constant<int, 16>{})
-         : experts <= 256 ? f(integral_constant<int, 16>{}, integral_constant<int, 16>{})
-         : experts <= 512 ? f(integral_constant<int, 32>{}, integral_constant<int, 16>{})
-                          : f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
-}
-
 template <typename F>
 int by_width(int experts, F &&f) {
   return experts <= 32 ? f(std::integral_constant<int, 1>{}) : experts <= 64 ? f(std::integral_constant<int, 2>{})
@@ -521,11 +527,12 @@ extern "C" int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int
   p.part_z = p.part_prob + static_cast<int64_t>(grid) * experts;
   p.part_live = reinterpret_cast<int32_t *>(p.part_z + grid);
   return call.launch(kOpRoute, [&] {
-    by_lanes(experts, [&](auto l, auto v) {
+    by_width(experts, [&](auto v) {
+      constexpr int V = decltype(v)::value;
       if (dtype == NS_BF16)
-        ns_route_rows_kernel<kBF16, decltype(l)::value, decltype(v)::value><<<grid, 32 * kRowWarps<decltype(l)::value, decltype(v)::value>, 0, call.s>>>(p);
+        ns_route_rows_kernel<kBF16, V><<<grid, 32 * kRowWarps<V>, 0, call.s>>>(p);
       else
-        ns_route_rows_kernel<kF32, decltype(l)::value, decltype(v)::value><<<grid, 32 * kRowWarps<decltype(l)::value, decltype(v)::value>, 0, call.s>>>(p);
+        ns_route_rows_kernel<kF32, V><<<grid, 32 * kRowWarps<V>, 0, call.s>>>(p);
       return 0;
     });
     count_launch();
