@@ -410,7 +410,8 @@ int ns_route_backward(const void *logits, int64_t ld_logits, int64_t rows, int e
  *     s     = smallest >= 1 with (largest magnitude of the block) <= 448 * 2^(s - 127)
  *     q     = x * 2^(127 - s) rounded to e4m3, half to even
  * A block that holds an infinity or NaN has s = 255 and reads back as NaN
- * throughout. The scale is a power of two, so x is rounded once.
+ * throughout. The scale is a power of two, so x is rounded once; a magnitude
+ * that rounds to 2^128 (from 1.9375 * 2^127 on) reads back as infinity.
  *   q       rows x ns_blocks_pitch(cols) bytes; bytes beyond cols are 0
  *   scales  rows x ns_blocks_scale_pitch(cols) bytes; for tiles one such row for
  *           every 128 rows of a matrix, counted anew for each of a stack; 0 beyond

@@ -468,7 +468,7 @@ inline int check(NormParams &p, const void *x, int64_t ld_x, const void *y, int6
   if (bad_shape(rows, cols, ld_x) || cols > kMaxCols || gate_form < kGateNone || gate_form > kGateFull) return NS_EINVAL;
   if (!std::isfinite(a) || !std::isfinite(b)) return NS_EINVAL;
   if (y && bad_shape(rows, cols, ld_y)) return NS_EINVAL;
-  if (!y && (gate_form != kGateNone || post)) return NS_EINVAL;
+  if (!y && rows > 0 && (gate_form != kGateNone || post)) return NS_EINVAL;
   if (!y && !pre && rows > 0) return NS_EINVAL;  // nothing to do
   if ((gate_form != kGateNone) != (gate != nullptr) && rows > 0) return NS_EINVAL;
   if (gate_form == kGateFull && bad_shape(rows, cols, ld_gate)) return NS_EINVAL;

@@ -377,8 +377,8 @@ extern "C" int ns_blocks_store_rows(const void *x, int64_t ld_x, int64_t x_rows,
   if (bad_dtype(dtype) || bad_shape(x_rows, cols, ld_x) || bad_shape(rows, cols, cols) || cols > kMaxRowCols || rows > (1 << 30) ||
       x_rows > (1 << 30) || per < 1)
     return NS_EINVAL;
-  if (!index && (rows != x_rows || per != 1)) return NS_EINVAL;
   if (rows == 0 || cols == 0) return NS_OK;
+  if (!index && (rows != x_rows || per != 1)) return NS_EINVAL;
   if ((!x && x_rows > 0) || !q || !scales) return NS_EINVAL;
   const int elt = dtype == NS_BF16 ? 2 : 4;
   if (misaligned(x, elt) || misaligned(index, 4) || misaligned(q, 16) || misaligned(scales, 16)) return NS_EALIGN;
