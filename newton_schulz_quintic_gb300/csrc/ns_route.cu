@@ -109,7 +109,7 @@ struct Choice<kBF16, V> {
 };
 
 // Rows by warps, V logits a lane.
-template <int V> constexpr int kRowWarps = V <= 16 ? kWarps : kWarps / 2;  // their sums fill 32 KB
+template <int V> constexpr int kRowWarps = V <= 8 ? 32 : 256 / V;  // their sums fill up to 32 KB
 template <int DT, int V>
 __global__ void __launch_bounds__(32 * kRowWarps<V>) ns_route_rows_kernel(const __grid_constant__ RouteParams p) {
   using E = typename Elem<DT>::T;
@@ -245,9 +245,14 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
   int32_t *mine = nexts + warp * p.experts;
   __syncthreads();
   // this stretch's slots per warp and expert
-  for (int i = a + lane; i < b; i += 32) {
-    const int e = p.ids[slot0 + i];
-    if (e >= 0) atomicAdd(mine + e, 1);
+  constexpr int kAhead = 4;  // reads in flight
+  for (int i0 = a; i0 < b; i0 += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) e[k] = i0 + 32 * k + lane < b ? p.ids[slot0 + i0 + 32 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (e[k] >= 0) atomicAdd(mine + e[k], 1);
   }
   __syncthreads();
   // Counts of all stretches and of those before this one: warps take 32 experts and a share of the stretches, many reads
@@ -329,17 +334,22 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
   }
   __syncthreads();
   const size_t size = static_cast<size_t>(p.rows) * p.top_k * 4;
-  for (int i0 = a; i0 < b; i0 += 32) {
-    const int i = i0 + lane;
-    const int e = i < b ? p.ids[slot0 + i] : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const uint32_t before = same & ((1u << lane) - 1u);
-    int at = 0;
-    if (e >= 0) at = mine[e] + __popc(before);
-    __syncwarp();
-    if (e >= 0 && before == 0) mine[e] += __popc(same);
-    __syncwarp();
-    if (e >= 0 && in_bounds(p.order + at, 4, p.order, size, p.status)) p.order[at] = slot0 + i;
+  for (int i0 = a; i0 < b; i0 += 32 * kAhead) {
+    int ids[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ids[k] = i0 + 32 * k + lane < b ? p.ids[slot0 + i0 + 32 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int e = ids[k];
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const uint32_t before = same & ((1u << lane) - 1u);
+      int at = 0;
+      if (e >= 0) at = mine[e] + __popc(before);
+      __syncwarp();
+      if (e >= 0 && before == 0) mine[e] += __popc(same);
+      __syncwarp();
+      if (e >= 0 && in_bounds(p.order + at, 4, p.order, size, p.status)) p.order[at] = slot0 + i0 + 32 * k + lane;
+    }
   }
   // places that no slot has
   const int64_t slots = static_cast<int64_t>(p.rows) * p.top_k;

@@ -94,7 +94,7 @@ def reference(layer, x, live, keep, experts, dout):
     t = int(live.sum())
     loss = 0.01 * e / (k * t * t) * (counts * p[live].sum(0)).sum() + 0.001 / t * (torch.logsumexp(n @ v["router"].t(), -1)[live] ** 2).sum()
     grads = torch.autograd.grad((out * dout.double()).sum() + loss, list(v.values()))
-    return out.detach(), float(loss), dict(zip(v, grads))
+    return out.detach(), float(loss.detach()), dict(zip(v, grads))
 
 
 @pytest.mark.parametrize("tokens,d,f,experts,top_k", [(700, 256, 320, 8, 2), (333, 520, 136, 5, 3)])
