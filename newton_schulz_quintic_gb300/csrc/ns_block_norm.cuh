@@ -401,7 +401,8 @@ struct Shape {
     packs = lanes <= 256 ? 1 : lanes <= (backward ? 2 * most : 512) ? 2 : 4;
     threads = ((lanes + packs - 1) / packs + 31) / 32 * 32;
     rows = std::max(1, std::min(kMaxHeight, most / threads));
-    if (packs == 1) rows = std::max(1, std::min(rows, 256 / threads));  // two CTAs an SM
+    // narrow rows: CTAs of half the threads that an SM has registers for, so that two stay
+    if (packs == 1) rows = std::max(1, std::min(rows, (wide ? 256 : 224) / threads));
     ring.height = rows;
     ring.threads = threads;
     const void *src[kStreams] = {p.x, p.y, backward && p.pre ? p.dz : nullptr, backward ? p.dr : nullptr};
@@ -434,7 +435,8 @@ struct Shape {
     ring.padded = wide && p.cols < threads * packs * 8;
     for (per_sm = packs == 1 ? 4 : 2; per_sm > 1; --per_sm)
       if ((room / per_sm - kRingHead - 2048 - beside) / ring.slot_bytes >= 2) break;
-    if (backward) per_sm = std::min(per_sm, 2);
+    // backward takes up to 128 registers a thread, forward less for one pack
+    per_sm = std::max(1, std::min(per_sm, (backward ? 512 : packs == 1 ? 1024 : 512) / block(wide)));
     const int mine = per_sm == 1 ? room : room / per_sm - kRingHead - 2048;
     ring.slots = std::max(1, std::min(kMaxSlots, (mine - beside) / ring.slot_bytes));
     smem = kRingHead + std::max(ring.slots * ring.slot_bytes + beside, sums);
