@@ -7,10 +7,12 @@
 // magnitude to 448 or less, found in the bits of that magnitude, so x * 2^-e is
 // exact and the conversion to e4m3 rounds once, half to even.
 //
-// Element-wise work bound by HBM: one read, one write. Rows: a lane holds 8
-// consecutive values and the 16 lanes of a block find its largest magnitude by
-// shuffles. Weights: a CTA holds one 128 x 128 block in registers between the
-// two steps.
+// Element-wise work bound by HBM: one read, one write. Rows: a lane holds 16
+// consecutive values (8 where rows allow no packs) and the lanes of a block find
+// its largest magnitude by shuffles. Weights: a CTA holds one 128 x 128 block in
+// registers between the two steps. Stored: 16384 x 8192 bf16 rows in 60 us, 6.7
+// TB/s, 8 x 8192 x 6144 weights in 181 us, 6.7 TB/s; read back 68 and 206 us, 5.9 TB/s;
+// 38912 rows gathered from 9728 of 6144: 94 us (rows that left L2 are read again).
 #include <algorithm>
 
 #include "../../include/ns.h"

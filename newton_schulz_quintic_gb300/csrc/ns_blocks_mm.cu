@@ -37,6 +37,10 @@
 // of a cluster: each leaves its sums in its own shared memory, and every CTA adds
 // and stores a share of the rows, in order.
 //
+// Bound by the tensor pipe: 8192 rows, W of 8192 x 6144 in 244 to 253 us, 3.3 PFLOP/s (its input's gradient 255 to 296);
+// 76 experts of 2048 x 6144 over 38912 rows in 349 to 376 us, where a group's last tile is on average half full. Few rows:
+// 7 of them with W of 8192 x 6144 in 15 us, twice the time of W's bytes.
+//
 // Every wait is bounded (mbar_wait): on a timeout the status word is set, the
 // CTA waits for its own copies and MMAs, frees TMEM and exits.
 #include <algorithm>

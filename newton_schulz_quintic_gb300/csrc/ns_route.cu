@@ -3,13 +3,15 @@
 // experts' order, a balance loss; and the gradient of the logits.
 //
 // Small data (rows x experts) read once: what counts is latency. Two launches
-// forward. The first takes a warp per row, the row in registers: the k largest
-// by repeated warp maxima of order-preserving keys, the softmax in the same
-// pass. A CTA walks over a stretch of rows and leaves its counts and its sum of
+// forward. The first takes a warp per row, the row in registers and the next one
+// under way: the k largest by repeated warp maxima of order-preserving keys, the
+// softmax in the same pass. (Several rows a warp, their maxima by shuffles: 71 us
+// against 39 for 32768 x 256, top 8.) A CTA walks over a stretch of rows and leaves its counts and its sum of
 // probabilities per expert. In the second every CTA adds up the counts of the
 // stretches before its own and ranks its slots from there, so the order is
 // stable and no atomic decides anything; the first one also writes the totals
-// and the loss, whose sums run in a fixed order.
+// and the loss, whose sums run in a fixed order. 32768 x 256 bf16, top 8: 52 us
+// forward, 18 backward; 1021 x 76 fp32, top 3: 12 and 4.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
