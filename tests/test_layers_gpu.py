@@ -203,6 +203,52 @@ def test_route_views_in_place_and_many_rows():
     check_route(x, 5, torch.rand(40000, device="cuda", generator=g) > 0.5)
 
 
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("n,e,k", [(10001, 136, 4), (5003, 264, 8), (5003, 512, 3), (2503, 1024, 16), (4, 200, 32)])
+def test_route_wide_rows_several_a_warp(n, e, k, renormalise):
+    # bf16 rows that packs fit, more of them than warps: the next row is read while one is worked on. The fast exponential
+    # is off by (2 + 1.2 |l - logz|) 2 E at most, within the 8 (span + 90) E that check_route allows a gradient's terms.
+    g = gen(e)
+    x = normal((n, e), g, BF16, 2.0)
+    x[1] = -INF                       # padding by its logits
+    x[2, 1:] = -INF                   # one expert
+    x[3, e // 2:] = -INF
+    live = torch.rand(n, device="cuda", generator=g) > 0.3
+    live[:4] = True
+    x[~live] = NAN
+    dw = normal((n, k), g, F32)
+    kw = dict(renormalise=renormalise, balance_coef=0.03, z_coef=0.002)
+    r, d = check_route(x, k, live, renormalise, dw=dw)
+    assert torch.isfinite(d).all() and torch.all(d[1] == 0) and torch.all(d[~live] == 0)
+    # -infinity is a probability of zero: the row's gradient is the short row's (zero where nothing was held)
+    assert torch.all(d[2, 1:] == 0) and torch.all(d[3, e // 2:] == 0)
+    ok = live.clone()
+    ok[1:4] = False
+    z = x.double().masked_fill(~ok[:, None], 0).requires_grad_(True)
+    p = torch.softmax(z, -1)
+    has = ok[:, None] & (r.experts >= 0)
+    ids = r.experts.clamp(min=0).long()
+    w = p.gather(1, ids) * has
+    if renormalise:
+        w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
+    t = int(r.live_rows)
+    s = 0.03 * e / (k * t * t) * r.counts.double()
+    total = (p[ok] * s).sum() + 0.002 / t * (torch.logsumexp(z, -1)[ok] ** 2).sum() + (w * dw.double())[ok].sum()
+    ref = torch.autograd.grad(total, z)[0]
+    dwm = torch.where(has, dw.double().abs(), 0.0)
+    p, w = p.detach(), w.detach()
+    full = torch.zeros_like(p).scatter_add_(1, ids, dwm)
+    lz = torch.logsumexp(z, -1).abs().detach()[:, None]
+    mag = p * (s + (p * (s + full)).sum(-1, keepdim=True) + 0.004 / t * lz + full)
+    mag = mag + torch.zeros_like(p).scatter_add_(1, ids, w * (dwm + (w * dwm).sum(-1, keepdim=True)))
+    span = float(z.detach().amax() - z.detach().amin())
+    within(d[ok], ref[ok], (8 * (span + 90) * E * mag + U[BF16] * ref.abs())[ok])
+    # a view that packs fit, in place; one that they do not fit
+    wide, odd = padded(x, 8, 16), padded(x, 5, 3)
+    assert api.route_backward(wide, r, dw, dlogits=wide, **kw) is wide and torch.equal(wide, d)
+    within(api.route_backward(odd, r, dw, **kw)[ok], ref[ok], (8 * (span + 90) * E * mag + U[BF16] * ref.abs())[ok])
+
+
 def test_route_gradient_by_differences():
     # the loss moves by the gradient along a direction that leaves the choice as it is
     g = gen(7)
