@@ -10,7 +10,7 @@
 // probabilities per expert. In the second every CTA adds up the counts of the
 // stretches before its own and ranks its slots from there, so the order is
 // stable and no atomic decides anything; the first one also writes the totals
-// and the loss, whose sums run in a fixed order. 32768 x 256 bf16, top 8: 52 us
+// and the loss, whose sums run in a fixed order. 32768 x 256 bf16, top 8: 44 us
 // forward, 11 backward; 1021 x 76 fp32, top 3: 12 and 4.
 #include <algorithm>
 #include <cmath>
@@ -23,7 +23,6 @@ namespace ns {
 
 namespace {
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxExperts = 1024, kMaxTopK = 32;
 // CTAs of a call: what the scratch holds. Every CTA of the second launch reads the parts of all, so no more than fill the SMs.
 constexpr int kMaxStretches = 152;
@@ -221,29 +220,31 @@ __global__ void __launch_bounds__(32 * kRowWarps<V>) ns_route_rows_kernel(const 
   }
 }
 
+template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
   __syncthreads();
   float s = 0.f;
-  for (int k = 0; k < kWarps; ++k) s += red[k];
+  for (int k = 0; k < W; ++k) s += red[k];
   return s;
 }
 
-// Slots of the CTA's stretch in the experts' order, and the totals.
-__global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_constant__ RouteParams p) {
+// Slots of the CTA's stretch in the experts' order, and the totals, by W warps.
+template <int W>
+__global__ void __launch_bounds__(W * 32) ns_route_order_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ int32_t nexts[];  // per warp and expert: place of its next slot
-  __shared__ int32_t scan[kWarps];
-  __shared__ float red[kWarps];
+  __shared__ int32_t scan[W];
+  __shared__ float red[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int stretches = gridDim.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int first = min(p.rows, static_cast<int>(blockIdx.x) * p.stretch), end = min(p.rows, first + p.stretch);
   const int slot0 = first * p.top_k, nslots = (end - first) * p.top_k;
-  const int share = ((nslots + kWarps - 1) / kWarps + 31) / 32 * 32;  // of a warp
+  const int share = ((nslots + W - 1) / W + 31) / 32 * 32;  // of a warp
   const int a = min(nslots, warp * share), b = min(nslots, a + share);
-  for (int e = threadIdx.x; e < kWarps * p.experts; e += kThreads) nexts[e] = 0;
+  for (int e = threadIdx.x; e < W * p.experts; e += W * 32) nexts[e] = 0;
   int32_t *mine = nexts + warp * p.experts;
   __syncthreads();
   // this stretch's slots per warp and expert
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
   // in flight (one thread for an expert's stretches was 40 us).
   __shared__ int32_t part_all[kMaxExperts], part_before[kMaxExperts];
   __shared__ float part_prob[kMaxExperts];
-  const int groups = (p.experts + 31) / 32, shares = max(1, kWarps / groups);
-  for (int item = warp; item < groups * shares; item += kWarps) {
+  const int groups = (p.experts + 31) / 32, shares = max(1, W / groups);
+  for (int item = warp; item < groups * shares; item += W) {
     const int e = item % groups * 32 + lane, part = item / groups;
     const int c0 = stretches * part / shares, c1 = stretches * (part + 1) / shares;
     int all = 0, before = 0;
@@ -291,10 +292,10 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     }
   }
   __syncthreads();
-  // experts in turn by threads, kThreads at a time: the slots of all experts before, of the stretches before, of the warps before
+  // experts in turn by threads, W * 32 at a time: the slots of all experts before, of the stretches before, of the warps before
   int run = 0;
   float loss = 0.f;
-  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+  for (int e0 = 0; e0 < p.experts; e0 += W * 32) {
     const int e = e0 + threadIdx.x;
     int before = 0, all = 0;
     float prob = 0.f;
@@ -315,14 +316,14 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int base = run;
-    for (int k = 0; k < kWarps; ++k) {
+    for (int k = 0; k < W; ++k) {
       if (k < warp) base += scan[k];
       run += scan[k];
     }
     const int offset = base + incl - all;
     if (e < p.experts) {
       int at = offset + before;
-      for (int k = 0; k < kWarps; ++k) {
+      for (int k = 0; k < W; ++k) {
         const int n = nexts[k * p.experts + e];
         nexts[k * p.experts + e] = at;
         at += n;
@@ -355,24 +356,24 @@ __global__ void __launch_bounds__(kThreads) ns_route_order_kernel(const __grid_c
   }
   // places that no slot has
   const int64_t slots = static_cast<int64_t>(p.rows) * p.top_k;
-  for (int64_t i = run + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < slots; i += static_cast<int64_t>(stretches) * kThreads)
+  for (int64_t i = run + static_cast<int64_t>(blockIdx.x) * W * 32 + threadIdx.x; i < slots; i += static_cast<int64_t>(stretches) * W * 32)
     if (in_bounds(p.order + i, 4, p.order, size, p.status)) p.order[i] = -1;
   if (blockIdx.x == 0) {
     float z = 0.f;
     int live = 0;
-    for (int c = threadIdx.x; c < stretches; c += kThreads) {
+    for (int c = threadIdx.x; c < stretches; c += W * 32) {
       z += p.part_z[c];
       live += p.part_live[c];
     }
-    loss = block_sum(loss, red);
-    z = block_sum(z, red);
+    loss = block_sum<W>(loss, red);
+    z = block_sum<W>(z, red);
     live = __reduce_add_sync(0xffffffffu, live);
     __syncthreads();
     if (lane == 0) scan[warp] = live;
     __syncthreads();
     if (threadIdx.x == 0) {
       live = 0;
-      for (int k = 0; k < kWarps; ++k) live += scan[k];
+      for (int k = 0; k < W; ++k) live += scan[k];
       const double t = live;
       if (in_bounds(p.offsets + p.experts, 4, p.offsets, (static_cast<size_t>(p.experts) + 1) * 4, p.status)) p.offsets[p.experts] = run;
       *p.live_rows = live;
@@ -649,22 +650,29 @@ extern "C" int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int
       return 0;
     });
     count_launch();
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = call.s;
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(kWarps) * experts * 4;
-    static SmemOptIn opt_in;
-    if (opt_in.ensure(reinterpret_cast<const void *>(ns_route_order_kernel), static_cast<int>(cfg.dynamicSmemBytes))) return -1;
-    if (cudaLaunchKernelEx(&cfg, ns_route_order_kernel, p) != cudaSuccess) {
+    const auto order = [&](auto w) {
+      constexpr int W = decltype(w)::value;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      cfg.stream = call.s;
+      cfg.gridDim = dim3(grid, 1, 1);
+      cfg.blockDim = dim3(W * 32, 1, 1);
+      cfg.dynamicSmemBytes = static_cast<size_t>(W) * experts * 4;
+      static SmemOptIn opt_in;
+      if (opt_in.ensure(reinterpret_cast<const void *>(ns_route_order_kernel<W>), static_cast<int>(cfg.dynamicSmemBytes))) return -1;
+      if (cudaLaunchKernelEx(&cfg, ns_route_order_kernel<W>, p) == cudaSuccess) return 0;
       cudaGetLastError();
       return -1;
-    }
+    };
+    // Every CTA reads the counts of all stretches: 32 warps where these are many (both launches, 16 warps / 32, us: 32768 x
+    // 256 52 / 44, 8192 x 1024 94 / 70, 32768 x 64 29 / 26), 16 where barriers of few reads count more (32768 x 8 19.3 /
+    // 19.7, 1021 x 76 11.4 / 12.2, one row of 256 9.7 / 11.4).
+    const int rc = static_cast<int64_t>(grid) * experts > 8192 ? order(std::integral_constant<int, 32>{}) : order(std::integral_constant<int, 16>{});
+    if (rc) return rc;
     count_launch();
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   });
