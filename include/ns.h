@@ -374,7 +374,8 @@ int ns_ckpt_wgrad(const void *dy, int64_t ld_dy, int64_t rows, int64_t n_out, co
  *              order, ascending within an expert, then -1
  *   live_rows  one int: T, the rows that are not padding
  *   loss       one float: balance_coef * experts / (top_k T^2) * sum_e counts[e] *
- *              (sum over rows of softmax(l)[e]) + z_coef / T * sum of logz^2 (T = 0: 0)
+ *              (sum over rows of softmax(l)[e]) + z_coef / T * sum of logz^2 (T = 0: 0;
+ *              squares in fp32, infinite from |logz| = 1.8e19 on; z_coef = 0 leaves them out)
  * A NaN orders above every number; a NaN or +infinity in a row makes its
  * weights, its logz and the loss NaN. offsets is what ns_blocks_matmul and
  * ns_ckpt_wgrad take, order what ns_blocks_store_rows takes (per = top_k).

@@ -377,7 +377,9 @@ __global__ void __launch_bounds__(W * 32) ns_route_order_kernel(const __grid_con
       const double t = live;
       if (in_bounds(p.offsets + p.experts, 4, p.offsets, (static_cast<size_t>(p.experts) + 1) * 4, p.status)) p.offsets[p.experts] = run;
       *p.live_rows = live;
-      *p.loss = live == 0 ? 0.f : static_cast<float>(p.balance * (p.experts * static_cast<double>(loss) / (p.top_k * t * t)) + p.z * (z / t));
+      // logz^2 may be beyond fp32: with a coefficient of 0 its mean stays out (a NaN of a row is in the balance as well)
+      const double squares = p.z != 0.f ? p.z * (z / t) : 0.;
+      *p.loss = live == 0 ? 0.f : static_cast<float>(p.balance * (p.experts * static_cast<double>(loss) / (p.top_k * t * t)) + squares);
     }
   }
 }

@@ -1,0 +1,111 @@
+"""GPU tests of the expert-layer operators where a bound taken over a whole call says nothing: rows of logits far from
+zero, each with its own bound; sums that a coefficient of zero leaves out; forms that other tests leave out.
+
+U is the unit roundoff of a type, E = 2^-24 that of fp32 arithmetic."""
+import math
+
+import pytest
+import torch
+
+from newton_schulz_quintic_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+E = 2.0 ** -24
+TINY = 2.0 ** -126  # what fp32 may lose below its normal numbers
+INF, NAN = math.inf, math.nan
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from newton_schulz_quintic_gb300 import build
+    build.build()
+    api.load_library()
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(shape, g, dtype=F32, std=1.0):
+    return (torch.randn(shape, device="cuda", generator=g) * std).to(dtype)
+
+
+def within(got, ref, bound):
+    """Every element of got within bound of ref; a reference beyond the type's numbers is its infinity."""
+    largest = torch.finfo(got.dtype).max
+    got, ref = got.double(), ref.double()
+    ref = torch.where(ref.abs() > largest * (1 + U[BF16]), ref.sign() * INF, ref)
+    assert got.shape == ref.shape
+    bad = ~((got == ref) | ((got - ref).abs() <= bound))
+    assert not bad.any(), (int(bad.sum()), torch.nonzero(bad)[:4].tolist(), got[bad][:4].tolist(), ref[bad][:4].tolist())
+
+
+# ------------------------------------------------------------------ router
+def check_rows(x, top_k, renormalise, cb, cz):
+    """A routing against the formulas in 64 bits, every row by its own bound. x holds no NaN and no
+    +infinity.
+
+    A logit's distance to its row's largest, D, is rounded once (D E relative in the exponential); a kernel that takes
+    another number of the row's size in its place is at most 16 from it. exp: 2 units in the last place, or
+    (2 + 1.2 D) 2^-23 for the fast one of bf16. Sums of 1024 terms by 32 lanes: 37 roundings. So a probability is off by
+    rel = (4 D + 4 sum p D + 120) E of itself, and what underflows by TINY."""
+    n, e = x.shape
+    kw = dict(renormalise=renormalise, balance_coef=cb, z_coef=cz)
+    r = api.route(x, top_k, **kw)
+    z = x.double()
+    live = (z > -INF).any(-1)
+    z = torch.where(live[:, None], z, 0.0)
+    top = z.amax(-1, keepdim=True)
+    far = (top - z).clamp(max=1e6) + 16  # beyond 1e6 (beyond 110) the exponential is 0 in any precision
+    q = torch.exp(z - top)
+    total = q.sum(-1, keepdim=True)
+    p = torch.where(live[:, None], q / total, 0.0)
+    logz = torch.where(live, (top + total.log())[:, 0], 0.0)
+    spread = (p * far).sum(-1, keepdim=True)
+    rel = (4 * far + 4 * spread + 120) * E
+    ids = r.experts.long()
+    has = ids >= 0
+    order = torch.sort(z, dim=-1, descending=True, stable=True).indices[:, :top_k]
+    want = torch.where(live[:, None] & (z.gather(1, order) > -INF), order, -1)
+    assert torch.equal(ids, want)
+    at = ids.clamp(min=0)
+    w, wrel = torch.where(has, p.gather(1, at), 0.0), rel.gather(1, at)
+    if renormalise:
+        w = torch.where(has, w / w.sum(-1, keepdim=True).clamp(min=1e-300), 0.0)
+        wrel = wrel + (w * wrel).sum(-1, keepdim=True)
+    within(r.weights, w, wrel * w + TINY)
+    lz_err = (4 * spread[:, 0] + 120) * E + E * logz.abs()  # of a total and its logarithm, the sum rounded
+    within(r.logz, logz, lz_err)
+    t = max(int(live.sum()), 1)
+    counts = torch.bincount(ids[has], minlength=e).double()
+    assert torch.equal(r.counts.double(), counts)
+    share = cb * e / (top_k * t * t)
+    balance, zterm = share * (counts * p.sum(0)).sum(), cz / t * (logz ** 2).sum()
+    # sums of n terms of one sign in fp32 (at most one rounding a row, a stretch and an expert), and what they take over
+    err = (n + 400) * E * (abs(balance) + abs(zterm)) + abs(share) * (counts * (p * rel).sum(0)).sum()
+    err = err + abs(cz) / t * (2 * logz.abs() * lz_err).sum()
+    within(r.loss, balance + zterm, err)
+    return r
+
+
+def test_route_z_term_stays_out_of_the_loss_at_coefficient_zero():
+    # squares of these rows' logz are beyond fp32: a coefficient of zero takes no part of them
+    for dtype in (BF16, F32):
+        x = normal((7, 40), gen(3), dtype)
+        want = api.route(x[:5], 3, balance_coef=0.0)
+        assert float(want.loss) == 0
+        x[5], x[6] = torch.finfo(dtype).min, 1e25
+        r = api.route(x, 3)
+        assert float(r.loss) == 0
+        r = check_rows(x, 3, True, 0.1, 0.0)
+        assert math.isfinite(float(r.loss)) and float(r.loss) > 0
+        # with a coefficient they count: infinite in fp32
+        assert float(api.route(x, 3, z_coef=1e-3).loss) == INF
+        # a NaN reaches the loss at any coefficient
+        x[0, 0] = NAN
+        assert math.isnan(float(api.route(x, 3).loss))
