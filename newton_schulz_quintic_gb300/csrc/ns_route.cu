@@ -11,7 +11,7 @@
 // stretches before its own and ranks its slots from there, so the order is
 // stable and no atomic decides anything; the first one also writes the totals
 // and the loss, whose sums run in a fixed order. 32768 x 256 bf16, top 8: 44 us
-// forward, 11 backward; 1021 x 76 fp32, top 3: 12 and 4.
+// forward, 13 backward; 1021 x 76 fp32, top 3: 11 and 3.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -398,9 +398,14 @@ struct RouteBackParams {
 };
 
 constexpr int kBackWarps = 8;
-// dL = P (s - sum of P s + 2 z logz / T) with s = balance E counts / (k T^2), and the weights' own part.
+// dL = P (s - sum of P s + 2 z logz / T) with s = balance E counts / (k T^2), and the weights' own part. P is exp(l - logz)
+// over the sum of these: logz is rounded to fp32 (at logits around 1e5 by up to 2^-8), so alone it gives no probabilities.
+// As the offset of its row any number of that size will do, which spares the row's maximum; sum and division are 1 us of
+// 13 at 32768 x 256. CTAs an SM: what 32, 40, 64 and 128 registers a thread allow (128 experts, 35 registers: 13.2 us
+// against 11.0).
+template <int V> constexpr int kBackCtas = V <= 4 ? 8 : V == 8 ? 6 : V == 16 ? 4 : 2;
 template <int DT, int V>
-__global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_kernel(const __grid_constant__ RouteBackParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32, kBackCtas<V>) ns_route_backward_kernel(const __grid_constant__ RouteBackParams p) {
   using E = typename Elem<DT>::T;
   __shared__ float slope[V * 32];
   __shared__ float part[kBackWarps][V * 32];  // a row's weights' part by expert; zero between rows
@@ -441,19 +446,21 @@ __global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_kernel(cons
     if (e >= 0) part[warp][e] = dw;
     __syncwarp();
     const float lz = p.logz[r];
-    float q[V], s[V], dot = 0.f;
+    float q[V], s[V], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * 32 + lane;
       q[i] = c < p.experts ? expf(Elem<DT>::to_f(x[c]) - lz) : 0.f;
       s[i] = slope[c] + (p.renormalise ? 0.f : part[warp][c]);
+      total += q[i];
       dot += q[i] * s[i];
     }
-    dot = warp_sum(dot) - 2.f * p.z / t * lz;
+    const float inv = 1.f / warp_sum(total);
+    dot = warp_sum(dot) * inv - 2.f * p.z / t * lz;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * 32 + lane;
-      float d = q[i] * (s[i] - dot);
+      float d = q[i] * inv * (s[i] - dot);
       if (p.renormalise) d += part[warp][c];
       if (c < p.experts && in_bounds(out + c, sizeof(E), p.dlogits, size, p.status)) out[c] = Elem<DT>::from_f(d);
     }
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_packs_kerne
       if (p.renormalise) dw = w * (dw - warp_sum(w * dw));
       if (e >= 0) part[e] = dw;
       __syncwarp();
-      float q[N][8], s[N][8], own[N][8], dot = 0.f;
+      float q[N][8], s[N][8], own[N][8], total = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = (i * 32 + lane) * 8;
@@ -532,15 +539,17 @@ __global__ void __launch_bounds__(kBackWarps * 32) ns_route_backward_packs_kerne
             q[i][j] = __expf(z);
             own[i][j] = p.renormalise ? sb[k] : 0.f;
             s[i][j] = sa[k] + (p.renormalise ? 0.f : sb[k]);
+            total += q[i][j];
             dot = fmaf(q[i][j], s[i][j], dot);
           }
         }
       }
-      dot = warp_sum(dot) - 2.f * p.z / t * lz;
+      const float inv = 1.f / warp_sum(total);
+      dot = warp_sum(dot) * inv - 2.f * p.z / t * lz;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i].set(j, fmaf(q[i][j], s[i][j] - dot, own[i][j]));
+        for (int j = 0; j < 8; ++j) v[i].set(j, fmaf(q[i][j] * inv, s[i][j] - dot, own[i][j]));
       __syncwarp();
       if (e >= 0) part[e] = 0.f;
       __syncwarp();
@@ -703,8 +712,8 @@ extern "C" int ns_route_backward(const void *logits, int64_t ld_logits, int64_t 
   if (call.rc) return call.rc;
   RouteBackParams p{logits, ld_logits, static_cast<int>(rows), experts, top_k, renormalise, ids, weights, dweights, logz,
                     counts, live_rows, balance_coef, z_coef, dlogits, ld_dlogits, call.status};
-  // 32768 rows, us, packs against elements: 64 experts 10.8 / 8.8, 128 11.2 / 10.6, 192 11.6 / 18.1, 256 11.4 / 18.4;
-  // 8192 rows of 512 7.2 / 9.3, of 1024 13.7 / 22.4. fp32 gains nothing by them (4096 x 256 4.6 / 4.5).
+  // 32768 rows, us, packs against elements: 64 experts 11.3 / 9.0, 128 11.8 / 11.0, 192 12.1 / 17.7, 256 12.8 / 21.1;
+  // 8192 rows of 512 7.6 / 9.3, of 1024 14.0 / 26.8. fp32 gains nothing by them (4096 x 256 4.6 / 4.5).
   const bool packs = dtype == NS_BF16 && experts > 128 && experts % 8 == 0 && rows_aligned(logits, ld_logits, elt, 8) &&
                      rows_aligned(dlogits, ld_dlogits, elt, 8);
   const auto grid = [&](int per_sm) {

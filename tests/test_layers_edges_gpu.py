@@ -46,8 +46,8 @@ def within(got, ref, bound):
 
 
 # ------------------------------------------------------------------ router
-def check_rows(x, top_k, renormalise, cb, cz):
-    """A routing against the formulas in 64 bits, every row by its own bound. x holds no NaN and no
+def check_rows(x, top_k, renormalise, cb, cz, seed=0):
+    """A routing and its gradient against the formulas in 64 bits, every row by its own bound. x holds no NaN and no
     +infinity.
 
     A logit's distance to its row's largest, D, is rounded once (D E relative in the exponential); a kernel that takes
@@ -90,7 +90,57 @@ def check_rows(x, top_k, renormalise, cb, cz):
     err = (n + 400) * E * (abs(balance) + abs(zterm)) + abs(share) * (counts * (p * rel).sum(0)).sum()
     err = err + abs(cz) / t * (2 * logz.abs() * lz_err).sum()
     within(r.loss, balance + zterm, err)
-    return r
+    dw = normal((n, top_k), gen(seed + 1))
+    d = api.route_backward(x, r, dw, **kw)
+    dwd = torch.where(has, dw.double(), 0.0)
+    s = (share * counts)[None].expand(n, e)
+    zero = torch.zeros_like(z)
+    if renormalise:
+        own = w * (dwd - (w * dwd).sum(-1, keepdim=True))
+        own_err = w * (dwd.abs() + (w * dwd.abs()).sum(-1, keepdim=True)) * (2 * wrel + 40 * E)
+        own, own_err = zero.scatter_add(1, at, own), zero.scatter_add(1, at, own_err)
+    else:
+        s = s.scatter_add(1, at, dwd)
+        own = own_err = zero
+    zl = 2 * cz / t * logz[:, None]
+    want = p * (s - (p * s).sum(-1, keepdim=True) + zl) + own
+    want = torch.where(live[:, None], want, 0.0)
+    inner = (p * s.abs() * (rel + 40 * E)).sum(-1, keepdim=True)
+    err = p * ((s.abs() + (p * s.abs()).sum(-1, keepdim=True) + zl.abs()) * (rel + 40 * E) + inner + abs(2 * cz / t) * lz_err[:, None])
+    within(d, want, err + own_err + U[x.dtype] * want.abs() + TINY)
+    return r, d
+
+
+OFFSETS = [0.0, -40.0, 1e3, -1e4, 1e5, -1e6, 1e7, -1e9, 1e12, -1e20, 1e30, -3e38]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("e,k", [(5, 2), (40, 8), (76, 3), (256, 8), (264, 4), (512, 3), (1000, 16), (1024, 32)])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_route_of_logits_far_from_zero(dtype, e, k, renormalise):
+    # probabilities are those of the distances within a row, wherever the row lies
+    g = gen(e)
+    rows = torch.tensor(OFFSETS, device="cuda").repeat(5)
+    x = (normal((rows.numel(), e), g, F32, 3.0) + rows[:, None]).clamp(min=torch.finfo(dtype).min).to(dtype)
+    check_rows(x, k, renormalise, 0.03, 0.0, e)   # (a z term of such rows hides the balance)
+    check_rows(x[(rows.abs() < 2e7)], k, renormalise, 0.03, 0.002, e)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_route_of_the_lowest_logits(dtype):
+    # a row masked by the type's lowest number is a distribution, all equal: its probabilities sum to 1, forward and back
+    low = torch.finfo(dtype).min
+    for e in (24, 256, 1000):
+        x = torch.full((6, e), low, dtype=dtype, device="cuda")
+        x[1, 3:] = 2.0
+        x[2, :e // 2] = -INF
+        x[3] = normal((e,), gen(2), dtype)
+        r, d = check_rows(x, 4, True, 0.05, 0.0)
+        assert float(r.loss) > 0
+        r, d = check_rows(x, 4, False, 0.05, 0.0)
+        # without the weights' part only the balance is left, and its gradient is small beside it: s - sum p s
+        d = api.route_backward(x, r, None, renormalise=False, balance_coef=0.05)
+        assert float(d.double().sum(-1).abs().max()) <= 2 * e * U[dtype] * float(d.double().abs().max()) + e * TINY
 
 
 def test_route_z_term_stays_out_of_the_loss_at_coefficient_zero():
@@ -102,10 +152,40 @@ def test_route_z_term_stays_out_of_the_loss_at_coefficient_zero():
         x[5], x[6] = torch.finfo(dtype).min, 1e25
         r = api.route(x, 3)
         assert float(r.loss) == 0
-        r = check_rows(x, 3, True, 0.1, 0.0)
+        r, _ = check_rows(x, 3, True, 0.1, 0.0)
         assert math.isfinite(float(r.loss)) and float(r.loss) > 0
         # with a coefficient they count: infinite in fp32
         assert float(api.route(x, 3, z_coef=1e-3).loss) == INF
         # a NaN reaches the loss at any coefficient
         x[0, 0] = NAN
         assert math.isnan(float(api.route(x, 3).loss))
+
+
+@pytest.mark.parametrize("e,k", [(16, 2), (256, 8)])
+def test_route_loss_moves_by_its_gradient(e, k):
+    # logits at least 1/2 apart and steps of at most 1/16: the choice stays as it is
+    g = gen(e)
+    n, cb, cz = 64, 2.0, 0.5
+    place = torch.argsort(torch.rand((n, e), device="cuda", generator=g), dim=-1)
+    x = place.float() * 0.5 - e / 8
+    v = normal((n, e), g).clamp(-4, 4)
+    h = 2.0 ** -6
+    kw = dict(balance_coef=cb, z_coef=cz)
+    r = api.route(x, k, **kw)
+    a, b = api.route(x + h * v, k, **kw), api.route(x - h * v, k, **kw)
+    assert torch.equal(a.experts, r.experts) and torch.equal(b.experts, r.experts)
+    d = api.route_backward(x, r, None, **kw)
+    slope = float((d.double() * v.double()).sum())
+
+    def value(step):
+        y = x.double() + step * v.double()
+        p = torch.softmax(y, -1)
+        return float(cb * e / (k * n * n) * (r.counts.double() * p.sum(0)).sum() + cz / n * (torch.logsumexp(y, -1) ** 2).sum())
+
+    def quotient(step):
+        return (value(step) - value(-step)) / (2 * step)
+    rest = 2 * abs(quotient(h) - quotient(h / 2))  # the third derivative's share is 4/3 of that
+    # x + h v is rounded (E of up to e / 4 a logit, which the gradient multiplies); the losses' own roundings, see check_rows
+    inputs = float(d.double().abs().sum()) * (e / 4 + 1) * E * 2 / (2 * h)
+    losses = 2 * (n + 400 + 4 * 60 + 240) * E * float(r.loss) * 1.1 / (2 * h)
+    assert abs((float(a.loss) - float(b.loss)) / (2 * h) - slope) <= rest + inputs + losses + 400 * E * float((d.abs() * v.abs()).sum())
