@@ -425,21 +425,23 @@ struct Shape {
       for (int q = 0; q < n; ++q) v += bytes[q] * rows;
       return v;
     };
+    // a call of no rows may have no stream at all (their pointers are null): its slots are empty, but there is no dividing by 0
+    auto slots_in = [](int space, int slot) { return space / std::max(1, slot); };
     // weights that a CTA uses for one batch or two are as well read where they lie
     hold = slot_of(2) + weights + extra <= room && p.rows > 2 * static_cast<int64_t>(rows) * sms ? 1 : 0;
     const int beside = extra + hold * weights;
     int streams = kStreams;
-    if ((room - beside) / slot_of(4) < 2 && (room - beside) / slot_of(3) >= 2) streams = 3;
+    if (slots_in(room - beside, slot_of(4)) < 2 && slots_in(room - beside, slot_of(3)) >= 2) streams = 3;
     while (streams > 1 && slot_of(streams) + beside > room) --streams;
     for (int q = 0; q < streams; ++q) ring.row_bytes[q] = bytes[q];
     ring.slot_bytes = slot_of(streams);
     ring.padded = wide && p.cols < threads * packs * 8;
     for (per_sm = packs == 1 ? 4 : 2; per_sm > 1; --per_sm)
-      if ((room / per_sm - kRingHead - 2048 - beside) / ring.slot_bytes >= 2) break;
+      if (slots_in(room / per_sm - kRingHead - 2048 - beside, ring.slot_bytes) >= 2) break;
     // backward takes up to 128 registers a thread, forward less for one pack
     per_sm = std::max(1, std::min(per_sm, (backward ? 512 : packs == 1 ? 1024 : 512) / block(wide)));
     const int mine = per_sm == 1 ? room : room / per_sm - kRingHead - 2048;
-    ring.slots = std::max(1, std::min(kMaxSlots, (mine - beside) / ring.slot_bytes));
+    ring.slots = std::max(1, std::min(kMaxSlots, slots_in(mine - beside, ring.slot_bytes)));
     smem = kRingHead + std::max(ring.slots * ring.slot_bytes + beside, sums);
   }
   int block(bool wide) const { return threads * rows + (wide ? 0 : 32); }
