@@ -406,7 +406,8 @@ struct Shape {
     if (packs == 1) rows = std::max(1, std::min(rows, (wide ? 256 : 224) / threads));
     ring.height = rows;
     ring.threads = threads;
-    const void *src[kStreams] = {p.x, p.y, backward && p.pre ? p.dz : nullptr, backward ? p.dr : nullptr};
+    // backward reads X for the norm of r alone
+    const void *src[kStreams] = {backward && !p.pre ? nullptr : p.x, p.y, backward && p.pre ? p.dz : nullptr, backward ? p.dr : nullptr};
     const int64_t ld[kStreams] = {p.ld_x, p.ld_y, p.ld_dz, p.ld_dr};
     const int xe = xt == kBF16 ? 2 : 4, ye = yt == kBF16 ? 2 : 4, elt[kStreams] = {xe, ye, ye, xe};
     int bytes[kStreams];
@@ -425,7 +426,8 @@ struct Shape {
       for (int q = 0; q < n; ++q) v += bytes[q] * rows;
       return v;
     };
-    // a call of no rows may have no stream at all (their pointers are null): its slots are empty, but there is no dividing by 0
+    // a call of no rows may have no stream at all (their pointers are null), and one stream may be read past the ring: slots
+    // are empty then, but there is no dividing by 0
     auto slots_in = [](int space, int slot) { return space / std::max(1, slot); };
     // weights that a CTA uses for one batch or two are as well read where they lie
     hold = slot_of(2) + weights + extra <= room && p.rows > 2 * static_cast<int64_t>(rows) * sms ? 1 : 0;

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from newton_schulz_quintic_gb300 import api
+from test_layers_gpu import check_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +190,19 @@ def test_route_loss_moves_by_its_gradient(e, k):
     inputs = float(d.double().abs().sum()) * (e / 4 + 1) * E * 2 / (2 * h)
     losses = 2 * (n + 400 + 4 * 60 + 240) * E * float(r.loss) * 1.1 / (2 * h)
     assert abs((float(a.loss) - float(b.loss)) / (2 * h) - slope) <= rest + inputs + losses + 400 * E * float((d.abs() * v.abs()).sum())
+
+
+# ------------------------------------------------------------------ block norms
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("rows,cols", [(1, 8), (700, 64), (5, 1000), (9, 2303), (400, 4096), (3, 8200), (320, 8192), (4, 12289), (2, 16384)])
+def test_block_norm_backward_without_a_second_norm(xt, yt, rows, cols):
+    # X is not read then, whatever it holds
+    for post in (True, False):
+        for gate in ("cols", "rows"):
+            check_norm(rows, cols, xt, yt, yt, gate, post=post, pre=False)
+    g = gen(cols)
+    x, y, dr, w = normal((rows, cols), g, xt), normal((rows, cols), g, yt), normal((rows, cols), g, xt), normal((cols,), g, yt)
+    f = api.block_norm(x, y, post_weight=w)
+    a = api.block_norm_backward(dr, None, x, y, f, post_weight=w)
+    b = api.block_norm_backward(dr, None, torch.full_like(x, NAN), y, f, post_weight=w)
+    assert torch.equal(a.dx, b.dx) and torch.equal(a.dy, b.dy) and torch.equal(a.dpost_weight, b.dpost_weight)

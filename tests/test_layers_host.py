@@ -73,3 +73,12 @@ def test_norm_plans_fit_the_shared_memory(shapes):
         assert s["smem"] + 2048 <= 227 * 1024 and 1 <= s["slots"] <= 8, (c, s)
         assert s["smem"] >= s["slots"] * s["slot_bytes"] and s["slot_bytes"] == s["rows"] * sum(s["row_bytes"]), (c, s)
         assert s["threads"] * s["packs"] * 8 >= c[1] and s["threads"] * s["rows"] <= 512, (c, s)
+
+
+def test_norm_plans_copy_what_is_read(shapes):
+    # through the ring: X for the norm of r alone, dZ with pre alone; Y wherever there is room
+    cases = [(5000, cols, 1, int(cols % 8 == 0), 2, 2, mask) for cols in COLS for mask in (X | Y | DR, X | Y | DZ | PRE, X | Y | DZ | DR | PRE)]
+    for c, s in zip(cases, shapes(cases)):
+        x, y, dz, dr = s["row_bytes"]
+        assert (x > 0) == bool(c[6] & PRE), (c, s)
+        assert y > 0 and (dr == 0 or c[6] & DR) and (dz == 0 or c[6] & PRE), (c, s)
