@@ -231,6 +231,8 @@ struct Filler {
         }
         row += ring.height * ring.row_bytes[q];
       }
+      // rows start at other places of a 16-byte word when a slot is used again: copies may fall on ends written for its last rows
+      fence_proxy_async_shared();
       __syncwarp();
     }
     if (lane == 0) mbar_arrive_expect_tx(&bar->full[slot], bytes);

@@ -206,3 +206,26 @@ def test_block_norm_backward_without_a_second_norm(xt, yt, rows, cols):
     a = api.block_norm_backward(dr, None, x, y, f, post_weight=w)
     b = api.block_norm_backward(dr, None, torch.full_like(x, NAN), y, f, post_weight=w)
     assert torch.equal(a.dx, b.dx) and torch.equal(a.dy, b.dy) and torch.equal(a.dpost_weight, b.dpost_weight)
+
+
+@pytest.mark.parametrize("dtype,cols", [(BF16, 3), (BF16, 259), (BF16, 1001), (F32, 333), (BF16, 4099), (F32, 2305)])
+def test_block_norm_ragged_rows_wherever_they_lie(dtype, cols):
+    # rows of an odd width start at another place of a 16-byte word each, and so do those that share a slot in turn: what a row
+    # gives does not depend on it
+    g = gen(cols)
+    n = 6000 if cols < 2000 else 1500
+    x, y, dr, dz = (normal((n, cols), g, dtype) for _ in range(4))
+    w1, w2 = normal((cols,), g, dtype), normal((cols,), g, dtype)
+    kw = dict(post_weight=w1, pre_weight=w2)
+    f = api.block_norm(x, y, **kw)
+    b = api.block_norm_backward(dr, dz, x, y, f, **kw)
+    order = torch.randperm(n, device="cuda", generator=g)
+    xs, ys, drs, dzs = (t[order] for t in (x, y, dr, dz))
+    for _ in range(3):
+        fs = api.block_norm(xs, ys, **kw)
+        bs = api.block_norm_backward(drs, dzs, xs, ys, fs, **kw)
+        assert torch.equal(fs.residual, f.residual[order]) and torch.equal(fs.normed, f.normed[order]) and torch.equal(fs.rstd, f.rstd[:, order])
+        assert torch.equal(bs.dx, b.dx[order]) and torch.equal(bs.dy, b.dy[order])
+    # and it is the row's alone
+    one = api.block_norm(x[5:6], y[5:6], **kw)
+    assert torch.equal(one.normed[0], f.normed[5]) and torch.equal(one.residual[0], f.residual[5])
