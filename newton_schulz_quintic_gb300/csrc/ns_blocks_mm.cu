@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
       while (ok && tiles.take(bar, t, w)) {
         const int w0 = t.n0 + r * 128, a0 = t.m0 + r * (TN / 2);
         for (int b = t.b0; b < t.b1; b += 2) {
-          if (!(ok = mbar_wait(&bar->empty[stage], parity ^ 1u, w))) break;
+          if (!(ok = mbar_wait<true>(&bar->empty[stage], parity ^ 1u, w))) break;
           const bool two = b + 1 < t.b1;
           mbar_arrive_expect_tx(&bar->full[stage], two ? S::kStageBytes : S::kStageBytes / 2);
           uint8_t *dw = sW + stage * (2 * S::kW), *da = sA + stage * (2 * S::kA);
@@ -434,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
       while (ok && tiles.take(bar, t, w)) {
         const int n = t.b1 - t.b0;
         for (int i = 0; i < n; i += 2) {
-          if (i % kChunk == 0 && !(ok = mbar_wait(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
+          if (i % kChunk == 0 && !(ok = mbar_wait<true>(&bar->tempty[acc], acc_parity ^ 1u, w))) break;
           if (i % 4 == 0 && !(ok = mbar_wait<true>(&bar->sfull[set], set_parity, w))) break;
-          if (!seen && !(ok = mbar_wait(&bar->ready[stage], parity, w))) break;
+          if (!seen && !(ok = mbar_wait<true>(&bar->ready[stage], parity, w))) break;
           tc_fence_after();
           const uint32_t d = tmem + static_cast<uint32_t>(acc * TN);
           const uint32_t sfw = tmem + static_cast<uint32_t>(S::kScaleAt + set * kScaleCols), sfa = sfw + 4u;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
           umma_mx_pair(d, dw + 2 * kStepW, da + 4u, id, sfw, sfa, 1);
           umma_mx_pair(d, dw + 3 * kStepW, da + 6u, id, sfw, sfa, 1);
           // look at the next stage while these run, so that its first MMA follows the last one here at once
-          seen = mbar_try_wait(&bar->ready[stage], parity);
+          seen = mbar_try_wait_cluster(&bar->ready[stage], parity);
           if (i + 1 < n) {
             id += scale_byte_of(1);
             dw += S::kW >> 4;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
       while (ok && tiles.take(bar, t, w)) {
         for (int b = t.b0; b < t.b1; b += 2) {
           if (!(ok = mbar_wait(&bar->full[stage], parity, w))) break;
-          arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), lead));
+          arrive_pair_shared(mapa_shared(smem_u32(&bar->ready[stage]), lead));
           if (++stage == kStages) {
             stage = 0;
             parity ^= 1u;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) {
           if (!ok || b + 4 * s >= t.b1) continue;
-          if (!warp_mbar_wait<false>(&bar->sempty[set], set_parity ^ 1u, w)) {
+          if (!warp_mbar_wait<true>(&bar->sempty[set], set_parity ^ 1u, w)) {
             ok = false;
             continue;
           }
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          // at CTA scope, as all it orders are TMEM stores that are complete; at cluster scope it took 1400 cycles
+          // (a release at cluster scope took 1400 cycles here)
           if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->sfull[set]), lead));
           if (++set == S::kSets) {
             set = 0;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_blocks_mm_kernel(const __grid_
       Sums<TN / 2> sum;
       sum.clear();
       for (int i = 0; i < t.b1 - t.b0; i += kChunk) {
-        if (!warp_mbar_wait<false>(&bar->tfull[acc], acc_parity, w)) {
+        if (!warp_mbar_wait<true>(&bar->tfull[acc], acc_parity, w)) {
           ok = false;
           break;
         }

@@ -401,13 +401,22 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// Arrive on a barrier of either CTA of the pair. What it orders are copies
-// that have landed, writes to this CTA's own shared memory that have passed
-// the proxy fence and TMEM loads that have passed theirs, so the release is
-// at CTA scope (at cluster scope it waits for the warp's other accesses, the
-// stores of the last tile included: 2500 cycles a drain).
+// Arrive on a barrier of either CTA of the pair, whose waits acquire at cluster
+// scope (mbar_wait<true>). arrive_pair hands over TMEM alone: its accesses are
+// complete (tcgen05.wait) and ordered before the arrival by tc_fence_before, so
+// the arrival itself is relaxed (a release at cluster scope waits for the
+// warp's other accesses, the stores of the last tile included: 2500 cycles a
+// drain). arrive_pair_shared also hands over this CTA's shared memory: copies
+// that have landed, and writes that have passed the proxy fence; its release
+// is restricted to shared memory for the same reason.
 __device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+__device__ __forceinline__ void arrive_pair_shared(uint32_t bar_cluster) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+      : "memory");
 }
 
 // 32 lanes x 16 columns of TMEM words, complete on return.

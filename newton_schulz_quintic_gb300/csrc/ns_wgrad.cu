@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(threads_of(kWiden), 1) ns_wgrad_kernel(const _
           fence_proxy_async_shared();
           __syncwarp();
         }
-        if (lane == 0) arrive_pair(mapa_shared(smem_u32(&bar->ready[stage]), 0));
+        if (lane == 0) arrive_pair_shared(mapa_shared(smem_u32(&bar->ready[stage]), 0));
         if (++stage == kStages) {
           stage = 0;
           parity ^= 1u;
