@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
       float k = p.b * (p.gate_form == kGateRows ? one_of(p.gate, t * p.ld_gate, p.gate_type) : 1.f);
       if (p.post) {
         const float ry = rsqrtf(sum(s2.x + s2.y) * inv_n + p.eps);
-        if (thread == 0 && ok) p.post_rstd[t] = ry;
+        if (thread == 0 && ok) put(p.post_rstd + t, ry, p.post_rstd, static_cast<size_t>(p.rows) * 4, p.status);
         k *= ry;
       }
 #pragma unroll
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_kernel(c
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(r[i].v[j], r[i].v[j], s2);
       const float rr = rsqrtf(sum(s2.x + s2.y) * inv_n + p.eps);
-      if (thread == 0 && ok) p.pre_rstd[t] = rr;
+      if (thread == 0 && ok) put(p.pre_rstd + t, rr, p.pre_rstd, static_cast<size_t>(p.rows) * 4, p.status);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         Eight2 f;

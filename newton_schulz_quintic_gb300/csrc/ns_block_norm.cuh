@@ -23,6 +23,7 @@ struct NormParams {
   const void *dr, *dz;      // backward
   void *dx, *dy, *dgate;
   float *parts;             // CTAs x 2 x cols: sums of dz * rh, and of the gate's (none, cols: drt * yh; else: g * drt * yh)
+  size_t parts_size;        // bytes of the scratch they are in
   int64_t ld_x, ld_y, ld_gate, ld_r, ld_z, ld_dr, ld_dz, ld_dx, ld_dy, ld_dgate;
   int64_t rows;
   int cols, gate_form, gate_type, weight_type;

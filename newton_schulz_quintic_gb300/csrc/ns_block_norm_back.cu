@@ -59,9 +59,9 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
     if constexpr (kInRegs<NP>) {
       sums[k][i][j] = __ffma2_rn(a, b, sums[k][i][j]);
     } else {
-      float *to = acc + ((k * NP + i) * 8 + 2 * j) * step;
-      to[0] = fmaf(a.x, b.x, to[0]);
-      to[step] = fmaf(a.y, b.y, to[step]);
+      float *own = acc + ((k * NP + i) * 8 + 2 * j) * step;
+      own[0] = fmaf(a.x, b.x, own[0]);
+      own[step] = fmaf(a.y, b.y, own[step]);
     }
   };
   if (p.hold && group == 0) held.keep(p, c);
@@ -207,10 +207,11 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
     if (fills) filler.fill(ring, bar, slots, p.rows, ahead, w);
     const float s = p.post || p.gate_form == kGateRows ? sum(s2.x + s2.y) : 0.f;
     if (p.gate_form == kGateRows && thread == 0 && ok) {
+      const size_t places = static_cast<size_t>((p.rows - 1) * p.ld_dgate + 1);
       if (p.gate_type == kBF16)
-        static_cast<__nv_bfloat16 *>(p.dgate)[t * p.ld_dgate] = __float2bfloat16_rn(s);
+        put(static_cast<__nv_bfloat16 *>(p.dgate) + t * p.ld_dgate, __float2bfloat16_rn(s), p.dgate, places * 2, p.status);
       else
-        static_cast<float *>(p.dgate)[t * p.ld_dgate] = s;
+        put(static_cast<float *>(p.dgate) + t * p.ld_dgate, s, p.dgate, places * 4, p.status);
     }
     const float m = p.post ? -s * grow * inv_n : 0.f;
 #pragma unroll
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kMostThreads<WIDE, NP>) ns_block_norm_backward
           const int at = (k * NP + i) * 8 + e, col = col_of<WIDE>(c[i], e);
           float v = acc[at * step];
           for (int j = 1; j < ring.height; ++j) v += acc[at * step + j * (2 * NP * 8 * step)];
-          if (col < p.cols) part[k * p.cols + col] = v;
+          if (col < p.cols) put(part + k * p.cols + col, v, p.parts, p.parts_size, p.status);
         }
   }
 }
@@ -360,6 +361,7 @@ extern "C" int ns_block_norm_backward(const void *dresidual, int64_t ld_dr, cons
   p.post_rstd = const_cast<float *>(post_rstd);
   p.pre_rstd = const_cast<float *>(pre_rstd);
   p.parts = static_cast<float *>(workspace);
+  p.parts_size = workspace_bytes;
   p.status = call.status;
   p.wait_limit_ns = kWaitLimitNs;
   const bool wide = packs_fit(p, dtype, block_dtype) && rows_aligned(dresidual, ld_dr, xe, 8) && rows_aligned(dnormed, ld_dz, ye, 8) &&

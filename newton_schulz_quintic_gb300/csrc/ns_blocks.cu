@@ -64,11 +64,6 @@ __device__ __forceinline__ void from_e4m3x2(uint32_t v, float &low, float &high)
   asm("{.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}" : "=f"(low), "=f"(high) : "r"(h));
 }
 
-template <typename T>
-__device__ __forceinline__ void put(void *at, T v, const void *base, size_t size, int *status) {
-  if (in_bounds(at, sizeof(T), base, size, status)) *static_cast<T *>(at) = v;
-}
-
 // Largest magnitude of a lane's 8 values as float bits; NaN is the largest of all.
 template <int DT, typename V>
 __device__ __forceinline__ uint32_t top_of(const V &v) {

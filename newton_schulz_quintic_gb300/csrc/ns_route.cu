@@ -43,6 +43,7 @@ struct RouteParams {
   float *part_prob;         // stretches x experts
   float *part_z;            // stretches
   int32_t *part_live;       // stretches
+  size_t work_size;         // bytes of the scratch, which starts at part_count
   int *status;
 };
 
@@ -205,8 +206,9 @@ __global__ void __launch_bounds__(32 * kRowWarps<V>) ns_route_rows_kernel(const 
     float s = sums[0][e];
 #pragma unroll
     for (int k = 1; k < kW; ++k) s += sums[k][e];
-    p.part_prob[static_cast<int64_t>(blockIdx.x) * p.experts + e] = s;
-    p.part_count[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * p.experts + e;
+    put(p.part_prob + at, s, p.part_count, p.work_size, p.status);
+    put(p.part_count + at, hist[e], p.part_count, p.work_size, p.status);
   }
   if (threadIdx.x == 0) {
     float z = 0.f;
@@ -215,8 +217,8 @@ __global__ void __launch_bounds__(32 * kRowWarps<V>) ns_route_rows_kernel(const 
       z += zs[k];
       n += lives[k];
     }
-    p.part_z[blockIdx.x] = z;
-    p.part_live[blockIdx.x] = n;
+    put(p.part_z + blockIdx.x, z, p.part_count, p.work_size, p.status);
+    put(p.part_live + blockIdx.x, n, p.part_count, p.work_size, p.status);
   }
 }
 
@@ -376,10 +378,11 @@ __global__ void __launch_bounds__(W * 32) ns_route_order_kernel(const __grid_con
       for (int k = 0; k < W; ++k) live += scan[k];
       const double t = live;
       if (in_bounds(p.offsets + p.experts, 4, p.offsets, (static_cast<size_t>(p.experts) + 1) * 4, p.status)) p.offsets[p.experts] = run;
-      *p.live_rows = live;
+      put(p.live_rows, live, p.live_rows, 4, p.status);
       // logz^2 may be beyond fp32: with a coefficient of 0 its mean stays out (a NaN of a row is in the balance as well)
       const double squares = p.z != 0.f ? p.z * (z / t) : 0.;
-      *p.loss = live == 0 ? 0.f : static_cast<float>(p.balance * (p.experts * static_cast<double>(loss) / (p.top_k * t * t)) + squares);
+      const double mean = p.balance * (p.experts * static_cast<double>(loss) / (p.top_k * t * t)) + squares;
+      put(p.loss, live == 0 ? 0.f : static_cast<float>(mean), p.loss, 4, p.status);
     }
   }
 }
@@ -648,6 +651,7 @@ extern "C" int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(rows + 15) / 16, call.sms, kMaxStretches})));
   p.stretch = static_cast<int>((rows + grid - 1) / grid);
   p.part_count = static_cast<int32_t *>(workspace);
+  p.work_size = workspace_bytes;
   p.part_prob = reinterpret_cast<float *>(p.part_count + static_cast<int64_t>(grid) * experts);
   p.part_z = p.part_prob + static_cast<int64_t>(grid) * experts;
   p.part_live = reinterpret_cast<int32_t *>(p.part_z + grid);

@@ -8,6 +8,12 @@
 
 namespace ns {
 
+// One value to `at`, in the buffer of `size` bytes at `base` (debug builds check that).
+template <typename T>
+__device__ __forceinline__ void put(void *at, T v, const void *base, size_t size, int *status) {
+  if (in_bounds(at, sizeof(T), base, size, status)) *static_cast<T *>(at) = v;
+}
+
 template <int BYTES> struct Word;
 template <> struct Word<2> { using T = uint16_t; };
 template <> struct Word<4> { using T = uint32_t; };
