@@ -478,9 +478,11 @@ inline int check(NormParams &p, const void *x, int64_t ld_x, const void *y, int6
   if (bad_shape(rows, cols, ld_x) || cols > kMaxCols || gate_form < kGateNone || gate_form > kGateFull) return NS_EINVAL;
   if (!std::isfinite(a) || !std::isfinite(b)) return NS_EINVAL;
   if (y && bad_shape(rows, cols, ld_y)) return NS_EINVAL;
-  if (!y && rows > 0 && (gate_form != kGateNone || post)) return NS_EINVAL;
-  if (!y && !pre && rows > 0) return NS_EINVAL;  // nothing to do
-  if ((gate_form != kGateNone) != (gate != nullptr) && rows > 0) return NS_EINVAL;
+  if (rows > 0 && cols > 0) {  // (a null pointer may stand for what is empty)
+    if (!y && (gate_form != kGateNone || post)) return NS_EINVAL;
+    if (!y && !pre) return NS_EINVAL;  // nothing to do
+    if ((gate_form != kGateNone) != (gate != nullptr)) return NS_EINVAL;
+  }
   if (gate_form == kGateFull && bad_shape(rows, cols, ld_gate)) return NS_EINVAL;
   if (gate_form == kGateRows && bad_shape(rows, 1, ld_gate)) return NS_EINVAL;
   if (misaligned(x, size_of(dtype)) || misaligned(y, size_of(block_dtype)) || misaligned(gate, size_of(gate_dtype)) ||

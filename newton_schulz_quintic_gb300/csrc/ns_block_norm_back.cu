@@ -320,7 +320,20 @@ extern "C" int ns_block_norm_backward(const void *dresidual, int64_t ld_dr, cons
       (y && bad_shape(rows, cols, ld_dy)) || (gate_form == kGateFull && bad_shape(rows, cols, ld_dgate)) ||
       (gate_form == kGateRows && bad_shape(rows, 1, ld_dgate)))
     return NS_EINVAL;
-  if (cols == 0) return NS_OK;
+  if (cols == 0 && (rows == 0 || gate_form != kGateRows)) return NS_OK;
+  if (cols == 0) {  // a row's gate has a gradient all the same: a sum over no columns
+    const int ge = size_of(gate_dtype);
+    if (!dgate) return NS_EINVAL;
+    if (misaligned(dgate, ge)) return NS_EALIGN;
+    if (Range(dgate, rows, 1, ld_dgate, ge).overlaps(Range(gate, rows, 1, ld_gate, ge))) return NS_EINVAL;
+    OpCall call(stream);
+    if (call.rc) return call.rc;
+    return call.launch(kOpBlockNorm, [&] {
+      if (cudaMemset2DAsync(dgate, static_cast<size_t>(ld_dgate) * ge, 0, ge, rows, call.s) == cudaSuccess) return 0;
+      cudaGetLastError();
+      return -1;
+    });
+  }
   if ((post && !dpost) || (pre && !dpre) || (gate_form == kGateCols && !dgate) || !workspace) return NS_EINVAL;
   if (rows > 0 && (!x || !dx || (y && !dy) || (pre && (!dnormed || !pre_rstd)) || (post && !post_rstd) ||
                    (gate_form != kGateNone && !dgate) || (!dresidual && !pre)))

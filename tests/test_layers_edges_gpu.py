@@ -229,3 +229,29 @@ def test_block_norm_ragged_rows_wherever_they_lie(dtype, cols):
     # and it is the row's alone
     one = api.block_norm(x[5:6], y[5:6], **kw)
     assert torch.equal(one.normed[0], f.normed[5]) and torch.equal(one.residual[0], f.residual[5])
+
+
+def test_block_norm_gradients_of_no_columns_and_of_no_rows(monkeypatch):
+    # sums over nothing are zeros, whatever the memory held
+    from newton_schulz_quintic_gb300 import layers
+
+    def garbage(shape, dtype, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t.fill_(NAN) if t.is_floating_point() else t
+    monkeypatch.setattr(layers, "_empty", garbage)
+    for xt, yt in ((BF16, BF16), (F32, BF16), (F32, F32)):
+        x, y, w = torch.zeros((5, 0), dtype=xt, device="cuda"), torch.zeros((5, 0), dtype=yt, device="cuda"), torch.zeros(0, dtype=yt, device="cuda")
+        for gate in (torch.ones((5, 1), dtype=yt, device="cuda"), torch.ones((5, 7), dtype=F32, device="cuda")[:, 3:4]):
+            f = api.block_norm(x, y, gate=gate, post_weight=w, pre_weight=w)
+            b = api.block_norm_backward(x, y, x, y, f, gate=gate, post_weight=w, pre_weight=w)
+            assert b.dgate.shape == (5, 1) and torch.all(b.dgate == 0) and b.dx.shape == (5, 0) and b.dpost_weight.shape == (0,)
+        for kw in (dict(pre_weight=w), dict(post_weight=w), dict(gate=w, post_weight=w, pre_weight=w), dict(gate=y, pre_weight=w)):
+            f = api.block_norm(x, y, **kw)
+            b = api.block_norm_backward(x, y if "pre_weight" in kw else None, x, y, f, **kw)
+            assert f.residual.shape == b.dx.shape == b.dy.shape == (5, 0)
+        assert api.block_norm(x, pre_weight=torch.zeros(0, dtype=yt, device="cuda")).residual.shape == (5, 0)
+    x, w = torch.zeros((0, 40), dtype=BF16, device="cuda"), torch.ones(40, dtype=BF16, device="cuda")
+    f = api.block_norm(x, x, gate=w, post_weight=w, pre_weight=w)
+    b = api.block_norm_backward(x, x, x, x, f, gate=w, post_weight=w, pre_weight=w)
+    for t in (b.dgate, b.dpost_weight, b.dpre_weight):
+        assert t.shape == (40,) and torch.all(t == 0)
