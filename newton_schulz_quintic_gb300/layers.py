@@ -235,8 +235,8 @@ def blocks_store(x, tiles: bool = False, rows=None, per: int = 1, stream=None) -
     if rows is not None:
         count = rows.numel()
         p_rows = _vector(rows, "rows", count, (_I32,), dev)
-        if per < 1:
-            raise ValueError("per must be positive")
+        if not 1 <= per < 1 << 31:  # (an int of the C call, which ctypes would cut short)
+            raise ValueError("per must be positive and below 2^31")
     elif per != 1:
         raise ValueError("per needs rows")
     with _on(dev, stream):

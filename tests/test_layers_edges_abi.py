@@ -1,6 +1,10 @@
 """Calls of the expert-layer entry points that are empty one way, and arguments that the foreign-function layer would cut
 short (no GPU needed: fake device pointers, so only where nothing can launch)."""
-from test_layers_abi import A, EALIGN, EINVAL, ENODEV, NBACK, NO_GPU, NORM, OK, call  # noqa: F401
+import pytest
+import torch
+from test_layers_abi import A, EALIGN, EINVAL, ENODEV, NBACK, NO_GPU, NORM, OK, Stub, call, calls  # noqa: F401
+
+from newton_schulz_quintic_gb300 import api
 
 
 @NO_GPU
@@ -15,3 +19,13 @@ def test_block_norm_of_no_columns(call):  # noqa: F811
     rows = dict(null, form=2, ldg=1, lddg=1)
     assert b(**rows) == ENODEV and b(**rows, rows=0, dgate=None) == OK and b(**rows, dgate=None) == EINVAL
     assert b(**rows, dgate=NBACK["gate"] + 2) == EINVAL and b(**rows, dgate=A + 1) == EALIGN and b(**dict(rows, lddg=0)) == EINVAL
+
+
+def test_per_beyond_an_int_is_refused(calls):  # noqa: F811
+    x, rows = Stub((6, 16), torch.bfloat16), Stub((9,), torch.int32)
+    for per in (0, -1, 1 << 31, (1 << 32) + 1):
+        with pytest.raises(ValueError):
+            api.blocks_store(x, rows=rows, per=per)
+    assert not calls
+    api.blocks_store(x, rows=rows, per=(1 << 31) - 1)
+    assert calls[0][1][4] == (1 << 31) - 1
