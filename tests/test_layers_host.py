@@ -1,9 +1,12 @@
-"""Host-side plans of the expert-layer operators, from a small program that includes them (compiled here, no GPU needed)."""
-import os
+"""Host-side plans of the expert-layer operators, from a small program that includes them (compiled here, no GPU needed),
+and the generator that the dropout tests take their masks from."""
+import random
 import subprocess
 import textwrap
 
+import numpy as np
 import pytest
+from test_layers_gpu import philox
 
 from newton_schulz_quintic_gb300 import build
 
@@ -82,3 +85,29 @@ def test_norm_plans_copy_what_is_read(shapes):
         x, y, dz, dr = s["row_bytes"]
         assert (x > 0) == bool(c[6] & PRE), (c, s)
         assert y > 0 and (dr == 0 or c[6] & DR) and (dz == 0 or c[6] & PRE), (c, s)
+
+
+def philox4x32(counter, key):
+    """Philox4x32-10 of four counter words and two key words."""
+    a, b, c, d = counter
+    k0, k1 = key
+    m = 0xFFFFFFFF
+    for _ in range(10):
+        p, q = a * 0xD2511F53, c * 0xCD9E8D57
+        a, b, c, d = (q >> 32) ^ b ^ k0, q & m, (p >> 32) ^ d ^ k1, p & m
+        k0, k1 = (k0 + 0x9E3779B9) & m, (k1 + 0xBB67AE85) & m
+    return a, b, c, d
+
+
+def test_the_reference_generator_has_the_published_answers():
+    # zeros, ones, and the digits of pi; and the form that the dropout tests compare with is this one
+    m = 0xFFFFFFFF
+    assert philox4x32((0, 0, 0, 0), (0, 0)) == (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)
+    assert philox4x32((m, m, m, m), (m, m)) == (0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD)
+    assert philox4x32((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0)) == (
+        0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1)
+    r = random.Random(1)
+    for third in (0, 1):
+        for n, seed in [(0, 0), ((1 << 64) - 1, (1 << 64) - 1)] + [(r.getrandbits(64), r.getrandbits(64)) for _ in range(20)]:
+            got = philox(np.array([n], np.uint64), seed, third)[0]
+            assert tuple(int(v) for v in got) == philox4x32((n & m, n >> 32, third, 0), (seed & m, seed >> 32))
