@@ -390,8 +390,8 @@ int ns_route(const void *logits, int64_t ld_logits, int64_t rows, int experts, i
 
 /*
  * ns_route_backward -- the logits' gradient of the loss (its own gradient 1)
- * and of the weights, dweights (rows x top_k, NULL: none; not read where the id
- * is -1). ids, weights, logz, counts, live_rows and the coefficients as ns_route
+ * and of the weights, dweights (rows x top_k, NULL: none; without effect where the
+ * id is -1). ids, weights, logz, counts, live_rows and the coefficients as ns_route
  * gave and got them; counts are taken as constants. With p = softmax(l) and s[e] =
  * balance_coef * experts * counts[e] / (top_k T^2):
  *     dl = p (s - sum p s + 2 z_coef logz / T) + the weights' part:
@@ -444,9 +444,11 @@ int ns_blocks_load(const void *q, const void *scales, int tiles, int groups, int
  *            group e is rows [offsets[e], offsets[e+1]); rows of no group become
  *            zeros. NULL with groups = 1 for all rows.
  *   out      rows x n of dtype
- * The tensor cores add the 128 products of a block in their fp32 accumulators;
- * the blocks' sums are scaled and added in fp32 registers, and rounded once. rows, n
- * and k <= 2^30, groups <= 2^20, groups * n * k <= 2^42.
+ * The tensor cores apply the scales and add up to 1024 products along k in their
+ * fp32 accumulators, which may lose a unit in the last place for every 32 products:
+ * less than 2^-17 of the sum of the products' magnitudes for k <= 32768 (2^-21 measured, products of
+ * one sign). Accumulators are added in fp32 registers, the result is rounded once.
+ * rows, n and k <= 2^30, groups <= 2^20, groups * n * k <= 2^42.
  */
 int ns_blocks_matmul(const void *qa, const void *sa, int64_t rows, int64_t k, const void *qw, const void *sw, int64_t n,
                      int back, const int32_t *offsets, int groups, void *out, int64_t ld_out, int dtype, void *stream);
@@ -465,6 +467,8 @@ int ns_blocks_matmul(const void *qa, const void *sa, int64_t rows, int64_t k, co
  *   post, pre   cols values of weight_dtype
  *   post_rstd, pre_rstd   rows floats for the backward pass (where post / pre)
  * r may be x and z may be y (same pitch). cols <= 16384. Y or pre must be given.
+ * Squares are summed in fp32: a row whose sum is beyond it (magnitudes from about
+ * 1.8e19 / sqrt(cols) on) counts as infinitely long, and its norm is 0.
  */
 #define NS_GATE_NONE 0
 #define NS_GATE_COLS 1
@@ -478,8 +482,8 @@ int ns_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, cons
 /*
  * ns_block_norm_backward -- from dR (NULL: zero, only with pre) and dZ: dX, dY, the
  * gate's gradient in the gate's form, and dpost, dpre (weight_dtype). X, Y, gate, post,
- * pre, a and b as given to ns_block_norm, whose rstd's it takes; R is formed again
- * from them. dx may be dR and dy may be dZ (same type and pitch). Sums over rows
+ * pre, a and b as given to ns_block_norm (copies of X and Y where that wrote over
+ * them), whose rstd's it takes; R is formed again from them, and without pre X is not read. dx may be dR and dy may be dZ (same type and pitch). Sums over rows
  * are taken in fp32 in a fixed order. workspace: ns_block_norm_workspace(rows, cols)
  * bytes, 4-byte aligned (less: NS_ENOMEM).
  */
@@ -501,7 +505,8 @@ int ns_block_norm_backward(const void *dr, int64_t ld_dr, const void *dz, int64_
  * counter words (n mod 2^32, n / 2^32, 0, 0) gives eight 16-bit numbers h, a word's
  * low half first; with (.., .., 1, 0) eight more, l. An element is dropped when
  * h * 65536 + l < limit = round(prob * 2^32), the others are multiplied by 2^32 /
- * (2^32 - limit). A call uses rows * ceil(cols / 8) counters.
+ * (2^32 - limit), rounded to fp32; with a residual the product and the sum take one
+ * rounding in fp32. A call uses rows * ceil(cols / 8) counters.
  *   state     NULL, or {seed, offset} on the device (two 64-bit numbers, 8-byte
  *             aligned) added to the arguments: a captured call draws anew when
  *             they change

@@ -10,8 +10,9 @@
 // one another at those sums, rows come through a ring in shared memory that a
 // warp keeps full by bulk copies (the ends of rows that are not 16-byte aligned
 // element by element). With reads straight into registers, 16384 rows of 8192 bf16
-// took 268 us forward and 603 back; now 172, 94 % of the copy rate, and 393. Forward
-// has two rows of 256 threads in hand: one of 512 took 221.
+// took 268 us forward and 603 back; now 172, 92 % of the copy rate, and 393 to 404 (232
+// without pre, where X is not read). Forward has two rows of 256 threads in hand: one of
+// 512 took 221.
 // The weights' gradients are sums over rows: a CTA walks over rows and adds in
 // fp32, each thread its own columns, and a second launch adds the CTAs' parts in
 // order.

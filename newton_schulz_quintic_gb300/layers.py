@@ -387,8 +387,8 @@ def block_norm_backward(dresidual, dnormed, x, y, saved: BlockNorm, gate=None, p
                         stream=None) -> BlockNormGrads:
     """Backward of block_norm (ns_block_norm_backward) from the gradients of
     ``residual`` (None: zero) and ``normed`` (None without pre_weight). The other
-    arguments are those of the forward call, ``saved`` is its result. ``dx`` (may be
-    dresidual) and ``dy`` (may be dnormed) are where those gradients go; allocated when
+    arguments are those of the forward call (``x`` and ``y`` as they were before it, where it
+    wrote over them), ``saved`` is its result. ``dx`` (may be dresidual) and ``dy`` (may be dnormed) are where those gradients go; allocated when
     not given. Gradients have the types of what they belong to; a gate's has its shape."""
     n, cols, dev, ld_x, ld_y, form, ld_g, codes = _norm_arguments(x, y, gate, post_weight, pre_weight)
     if dresidual is None and pre_weight is None:
