@@ -446,8 +446,9 @@ int ns_blocks_load(const void *q, const void *scales, int tiles, int groups, int
  *   out      rows x n of dtype
  * The tensor cores apply the scales and add up to 1024 products along k in their
  * fp32 accumulators, which may lose a unit in the last place for every 32 products:
- * less than 2^-17 of the sum of the products' magnitudes for k <= 32768 (2^-21 measured, products of
- * one sign). Accumulators are added in fp32 registers, the result is rounded once.
+ * less than 2^-17 of the sum of the products' magnitudes for k <= 32768 (2^-21
+ * measured, products of one sign). Accumulators are added in fp32 registers, the
+ * result is rounded once.
  * rows, n and k <= 2^30, groups <= 2^20, groups * n * k <= 2^42.
  */
 int ns_blocks_matmul(const void *qa, const void *sa, int64_t rows, int64_t k, const void *qw, const void *sw, int64_t n,
@@ -483,7 +484,8 @@ int ns_block_norm(const void *x, int64_t ld_x, const void *y, int64_t ld_y, cons
  * ns_block_norm_backward -- from dR (NULL: zero, only with pre) and dZ: dX, dY, the
  * gate's gradient in the gate's form, and dpost, dpre (weight_dtype). X, Y, gate, post,
  * pre, a and b as given to ns_block_norm (copies of X and Y where that wrote over
- * them), whose rstd's it takes; R is formed again from them, and without pre X is not read. dx may be dR and dy may be dZ (same type and pitch). Sums over rows
+ * them), whose rstd's it takes; R is formed again from them, and without pre X is
+ * not read. dx may be dR and dy may be dZ (same type and pitch). Sums over rows
  * are taken in fp32 in a fixed order. workspace: ns_block_norm_workspace(rows, cols)
  * bytes, 4-byte aligned (less: NS_ENOMEM).
  */
